@@ -18,6 +18,7 @@ from . import _build
 
 BF16, FP32 = 0, 1
 MASK_NONE, MASK_LOCAL_GLOBAL, MASK_SLIDING, MASK_CAUSAL = 0, 1, 2, 3
+ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "parts": 3}
 
 STATUS = {0: "BSA_OK", 1: "BSA_ERR_INVALID_ARG", 2: "BSA_ERR_UNSUPPORTED",
           3: "BSA_ERR_BAD_INDEX", 4: "BSA_ERR_WORKSPACE", 5: "BSA_ERR_CUDA",
@@ -35,6 +36,11 @@ EXPORTS = (
     "bsa_static_max_blocks",
     "bsa_static_blocks", "bsa_get_device_status", "bsa_selftest_wait_timeout", "bsa_status_string",
     "bsa_last_error", "bsa_version",
+    "bsa_rope_frequencies", "bsa_rope_table", "bsa_rope", "bsa_rope_backward",
+    "bsa_cache_append", "bsa_cache_copy_pages", "bsa_paged_decode",
+    "bsa_pages_create", "bsa_pages_destroy", "bsa_pages_reserve", "bsa_pages_fork",
+    "bsa_pages_truncate", "bsa_pages_take_copies", "bsa_pages_compact", "bsa_pages_tables",
+    "bsa_pages_free_pages",
 )
 
 
@@ -64,6 +70,36 @@ class Select(ctypes.Structure):
     selection, always-include-local-block."""
     _fields_ = [("head_topk", ctypes.c_void_p), ("causal", ctypes.c_int32),
                 ("local_block", ctypes.c_int32)]
+
+
+class RopeParams(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double)]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("n", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class Strides(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("head", ctypes.c_int64), ("token", ctypes.c_int64)]
+
+
+class Rotation(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("rot", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("factor", ctypes.c_float)]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("kbar", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("d", ctypes.c_int32)]
+
+
+class DecodeOptions(ctypes.Structure):
+    _fields_ = [("local_block", ctypes.c_int32), ("share_group", ctypes.c_int32)]
 
 
 _lib = None
@@ -118,6 +154,23 @@ def lib():
         "bsa_status_string": ([i32], ctypes.c_char_p),
         "bsa_last_error": ([], ctypes.c_char_p),
         "bsa_version": ([], i32),
+        "bsa_rope_frequencies": ([RopeParams, vp], i32),
+        "bsa_rope_table": ([vp, i32, vp], i32),
+        "bsa_rope": ([Heads, vp, Strides, vp, i64, Rotation, vp, Strides, vp], i32),
+        "bsa_rope_backward": ([Heads, vp, Strides, vp, i64, Rotation, vp, Strides, vp], i32),
+        "bsa_cache_append": ([Cache, vp, i64, vp, i64, i64, i64, vp, vp, vp, i32, vp], i32),
+        "bsa_cache_copy_pages": ([Cache, vp, i64, vp], i32),
+        "bsa_paged_decode": ([Cache, vp, i64, i64, i32, vp, i32, i64, vp, vp, i32,
+                              ctypes.POINTER(DecodeOptions), f32, vp, vp, vp], i32),
+        "bsa_pages_create": ([i64, i32, i32, i32, ctypes.POINTER(vp)], i32),
+        "bsa_pages_destroy": ([vp], i32),
+        "bsa_pages_reserve": ([vp, i32, i64], i32),
+        "bsa_pages_fork": ([vp, i32, i32], i32),
+        "bsa_pages_truncate": ([vp, i32, i64], i32),
+        "bsa_pages_take_copies": ([vp, vp, i64, ctypes.POINTER(i64)], i32),
+        "bsa_pages_compact": ([vp, vp, i64, ctypes.POINTER(i64)], i32),
+        "bsa_pages_tables": ([vp, vp, vp], i32),
+        "bsa_pages_free_pages": ([vp], i64),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -410,3 +463,243 @@ def selftest_wait_timeout(kind: int, limit_ns: int) -> None:
     nothing completes gives up after about limit_ns and records
     BSA_ERR_TIMEOUT; read it with device_status()."""
     _check(lib().bsa_selftest_wait_timeout(int(kind), int(limit_ns), _stream()))
+
+
+# ------------------------------------------------------------ rotary positions
+class Rope:
+    """A rotation's plan: frequencies, fixed-point table on the device, layout
+    and factor (see bsa_rope_params and bsa_rotation in bsa.h).  ``inv_freq``
+    replaces the computed frequencies by the caller's (rot / 2 numbers)."""
+
+    def __init__(self, rot: int, theta: float = 10000.0, *, interleaved: bool = False,
+                 scaling: str = "none", factor: float = 1.0, original: float = 0.0,
+                 low: float = 1.0, high: float = 32.0, attention_factor: float = 1.0,
+                 inv_freq=None, device="cuda"):
+        torch = _torch()
+        if inv_freq is None:
+            p = RopeParams(rot, ROPE_SCALING[scaling], theta, factor, original, low, high)
+            self.inv_freq = np.empty(max(rot, 2) // 2, dtype=np.float64)
+            _check(lib().bsa_rope_frequencies(p, self.inv_freq.ctypes.data_as(ctypes.c_void_p)))
+        else:
+            self.inv_freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
+            if self.inv_freq.shape != (rot // 2,) or rot % 2:
+                raise ValueError("inv_freq must hold rot / 2 numbers")
+        table = np.empty(self.inv_freq.shape, dtype=np.uint64)
+        _check(lib().bsa_rope_table(self.inv_freq.ctypes.data_as(ctypes.c_void_p), table.size,
+                                    table.ctypes.data_as(ctypes.c_void_p)))
+        self.rot, self.interleaved, self.attention_factor = rot, interleaved, attention_factor
+        self.table = torch.from_numpy(table.view(np.int64)).to(device)
+        self.rotation = Rotation(self.table.data_ptr(), rot, int(interleaved), attention_factor)
+
+
+def _one_device(*tensors):
+    """All on one CUDA device, and that the current one: pointers of another
+    device would be launched on this one's stream."""
+    torch = _torch()
+    here = torch.cuda.current_device() if any(t is not None and t.is_cuda for t in tensors) else None
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != here):
+            raise ValueError("tensors must be on the current CUDA device")
+
+
+def _i32(t, name: str, shape):
+    torch = _torch()
+    if t.dtype != torch.int32 or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise TypeError(f"{name} must be a contiguous int32 tensor {list(shape)}")
+    return t
+
+
+def _rope(fn, x, rope: Rope, positions, out):
+    torch = _torch()
+    if x.dim() not in (3, 4) or x.stride(-1) != 1:
+        raise ValueError("x must be [batch, heads, n, d] or [heads, n, d] with contiguous channels")
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape or out.dtype != x.dtype or out.stride(-1) != 1:
+        raise ValueError("out must have x's shape and dtype and contiguous channels")
+    batch = x.shape[0] if x.dim() == 4 else 1
+    heads, n, d = x.shape[-3:]
+    first = 0
+    if isinstance(positions, torch.Tensor):
+        shape = (batch, n) if positions.dim() == 2 else (n,)
+        if positions.dim() == 1 and batch != 1:
+            raise TypeError("positions must be [batch, n]")
+        _i32(positions, "positions", shape)
+        _one_device(x, out, rope.table, positions)
+    else:
+        first, positions = int(positions), None
+        _one_device(x, out, rope.table)
+    s = Heads(batch, n, heads, d, BF16 if x.dtype == torch.bfloat16 else FP32)
+    st = [Strides(t.stride(0) if t.dim() == 4 else 0, t.stride(-3), t.stride(-2)) for t in (x, out)]
+    _check(fn(s, _ptr(x), st[0], _ptr(positions), first, rope.rotation, _ptr(out), st[1], _stream()))
+    return out
+
+
+def rope(x, rope: Rope, positions=0, *, out=None):
+    """Rotated x: [batch, heads, n, d] (or [heads, n, d]), any strides with
+    contiguous channels.  ``positions``: the first token's position, or an
+    int32 device tensor [batch, n].  ``out`` may be x itself; by default a
+    contiguous tensor, the layout ``forward`` takes."""
+    return _rope(lib().bsa_rope, x, rope, positions, out)
+
+
+def rope_backward(dout, rope: Rope, positions=0, *, out=None):
+    """Gradient of ``rope`` with respect to its input."""
+    return _rope(lib().bsa_rope_backward, dout, rope, positions, out)
+
+
+# ---------------------------------------------------------------- paged cache
+class PagedCache:
+    """A paged cache's device tensors: k, v [pages, heads, page, d] bf16 and
+    the block means kbar [pages, heads, d] fp32 (bsa_cache in bsa.h)."""
+
+    def __init__(self, k, v, kbar):
+        torch = _torch()
+        if k.dim() != 4 or k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 \
+                or k.shape != v.shape or not k.is_contiguous() or not v.is_contiguous():
+            raise ValueError("k and v must be contiguous bfloat16 [pages, heads, page, d]")
+        if kbar.dtype != torch.float32 or not kbar.is_contiguous() \
+                or tuple(kbar.shape) != (k.shape[0], k.shape[1], k.shape[3]):
+            raise ValueError("kbar must be contiguous float32 [pages, heads, d]")
+        _one_device(k, v, kbar)
+        self.k, self.v, self.kbar = k, v, kbar
+        self.num_pages, self.heads, self.page, self.d = k.shape
+        self.struct = Cache(k.data_ptr(), v.data_ptr(), kbar.data_ptr(), self.num_pages,
+                            self.heads, self.page, self.d)
+
+    @classmethod
+    def empty(cls, num_pages: int, heads: int, page: int, d: int, device="cuda"):
+        torch = _torch()
+        k, v = (torch.zeros((num_pages, heads, page, d), dtype=torch.bfloat16, device=device)
+                for _ in range(2))
+        return cls(k, v, torch.zeros((num_pages, heads, d), dtype=torch.float32, device=device))
+
+
+def _token_rows(t, name: str, heads: int, d: int):
+    torch = _torch()
+    if t.dim() != 3 or t.dtype != torch.bfloat16 or t.shape[1:] != (heads, d) \
+            or t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{name} must be bfloat16 [tokens, {heads}, {d}] with contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else heads * d
+
+
+def cache_append(cache: PagedCache, k, v, table, start, *, cu_tokens=None):
+    """Append k, v [tokens, heads, d] (token stride free) to their sequences'
+    pages and refresh the touched blocks' means.  ``table`` int32 [seqs,
+    width], ``start`` int32 [seqs] (lengths before); ``cu_tokens`` int32
+    [seqs + 1], None: as many tokens for each.  See bsa_cache_append."""
+    seqs, width = table.shape
+    ks, vs = (_token_rows(t, n, cache.heads, cache.d) for t, n in ((k, "k"), (v, "v")))
+    if k.shape != v.shape:
+        raise ValueError("k and v must have one shape")
+    _i32(table, "table", (seqs, width))
+    _i32(start, "start", (seqs,))
+    if cu_tokens is not None:
+        _i32(cu_tokens, "cu_tokens", (seqs + 1,))
+    _one_device(cache.k, k, v, table, start, cu_tokens)
+    _check(lib().bsa_cache_append(cache.struct, _ptr(k), ks, _ptr(v), vs, k.shape[0], seqs,
+                                  _ptr(cu_tokens), _ptr(start), _ptr(table), width, _stream()))
+
+
+def copy_pages(cache: PagedCache, pairs):
+    """Copy whole pages: ``pairs`` int32 [count, 2] of (from, to) on the
+    device, or a host array as PageTable hands them out."""
+    torch = _torch()
+    if not isinstance(pairs, torch.Tensor):
+        pairs = torch.from_numpy(np.ascontiguousarray(pairs, dtype=np.int32)).to(cache.k.device)
+    _i32(pairs, "pairs", (pairs.shape[0], 2))
+    _one_device(cache.k, pairs)
+    _check(lib().bsa_cache_copy_pages(cache.struct, _ptr(pairs), pairs.shape[0], _stream()))
+
+
+def paged_decode(cache: PagedCache, q, table, lens, topk: int, *, token_seq=None,
+                 local_block: bool = True, share_group: bool = False, scale: float = 0.0,
+                 out=None):
+    """(out, idx): each token of q [tokens, q_heads, d] attends to the first
+    ``lens`` keys of its sequence, in the topk blocks it selects.  idx int32
+    [tokens, q_heads or cache heads, topk], ascending, -1 padded.  See
+    bsa_paged_decode in bsa.h."""
+    torch = _torch()
+    seqs, width = table.shape
+    tokens, q_heads = q.shape[0], q.shape[1]
+    qs = _token_rows(q, "q", q_heads, cache.d)
+    _i32(table, "table", (seqs, width))
+    _i32(lens, "lens", (tokens,))
+    if token_seq is not None:
+        _i32(token_seq, "token_seq", (tokens,))
+    if out is None:
+        out = torch.empty((tokens, q_heads, cache.d), dtype=q.dtype, device=q.device)
+    elif out.dtype != q.dtype or not out.is_contiguous() \
+            or tuple(out.shape) != (tokens, q_heads, cache.d):
+        raise ValueError("out must be contiguous bfloat16 [tokens, q_heads, d]")
+    _one_device(cache.k, q, table, lens, token_seq, out)
+    idx = torch.empty((tokens, cache.heads if share_group else q_heads, topk), dtype=torch.int32,
+                      device=q.device)
+    opts = DecodeOptions(int(local_block), int(share_group))
+    _check(lib().bsa_paged_decode(cache.struct, _ptr(q), qs, tokens, q_heads, _ptr(table), width,
+                                  seqs, _ptr(token_seq), _ptr(lens), topk, ctypes.byref(opts),
+                                  float(scale), _ptr(out), _ptr(idx), _stream()))
+    return out, idx
+
+
+class PageTable:
+    """Which sequence owns which page (host side, bsa_pages_* in bsa.h):
+    ``reserve`` room, ``fork`` with copy on write, ``truncate`` or ``free``,
+    ``compact``.  ``take_copies`` and ``compact`` return int32 [count, 2]
+    arrays for ``copy_pages``; run the former's before the next append."""
+
+    def __init__(self, num_pages: int, page: int, max_seqs: int, width: int):
+        self.num_pages, self.max_seqs, self.width = num_pages, max_seqs, width
+        self._h = ctypes.c_void_p()
+        _check(lib().bsa_pages_create(num_pages, page, max_seqs, width, ctypes.byref(self._h)))
+
+    def reserve(self, seq: int, tokens: int):
+        _check(lib().bsa_pages_reserve(self._h, seq, tokens))
+
+    def fork(self, source: int, to: int):
+        _check(lib().bsa_pages_fork(self._h, source, to))
+
+    def truncate(self, seq: int, length: int):
+        _check(lib().bsa_pages_truncate(self._h, seq, length))
+
+    def free(self, seq: int):
+        self.truncate(seq, 0)
+
+    def _pairs(self, fn):
+        count = ctypes.c_int64(0)
+        _check(fn(self._h, None, 0, ctypes.byref(count)))
+        pairs = np.empty((count.value, 2), dtype=np.int32)
+        _check(fn(self._h, pairs.ctypes.data_as(ctypes.c_void_p), count.value,
+                  ctypes.byref(count)))
+        return pairs
+
+    def take_copies(self):
+        return self._pairs(lib().bsa_pages_take_copies)
+
+    def compact(self):
+        return self._pairs(lib().bsa_pages_compact)
+
+    def tables(self):
+        """(table int32 [max_seqs, width], lengths int32 [max_seqs])."""
+        table = np.empty((self.max_seqs, self.width), dtype=np.int32)
+        lengths = np.empty(self.max_seqs, dtype=np.int32)
+        _check(lib().bsa_pages_tables(self._h, table.ctypes.data_as(ctypes.c_void_p),
+                                      lengths.ctypes.data_as(ctypes.c_void_p)))
+        return table, lengths
+
+    @property
+    def free_pages(self) -> int:
+        return int(lib().bsa_pages_free_pages(self._h))
+
+    def close(self):
+        if self._h:
+            lib().bsa_pages_destroy(self._h)
+            self._h = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass

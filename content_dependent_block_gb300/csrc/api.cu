@@ -13,7 +13,7 @@
 
 namespace {
 
-constexpr int32_t kVersion = 100;   // 0.1.0
+constexpr int32_t kVersion = 200;   // 0.2.0
 constexpr int kMaxDevices = 64;
 
 thread_local char g_last_error[256] = "";
@@ -792,6 +792,219 @@ bsa_status bsa_fine_backward_lse(bsa_shape shape, const void *q, const void *k, 
     if (!aligned(lse, 4)) return fail(BSA_ERR_ALIGNMENT, "lse is not 4-byte aligned");
     return fine_backward_impl(shape, q, k, v, out, dout, list, ld, mask, scale, lse, dq, dk, dv,
                               ws, ws_bytes, stream);
+}
+
+// --------------------------------------------------------- rotary positions
+static bsa_status rope_impl(const bsa_heads &h, const void *x, const bsa_strides &xs,
+                            const int32_t *positions, int64_t first, const bsa_rotation &rot,
+                            float sign, void *out, const bsa_strides &os, void *stream) {
+    if (h.batch < 1 || h.n < 1 || h.heads < 1)
+        return fail(BSA_ERR_INVALID_ARG, "batch, n and heads must be >= 1");
+    if (h.d != 64 && h.d != 128) return fail(BSA_ERR_UNSUPPORTED, "d must be 64 or 128 (got %d)", h.d);
+    if (h.dtype != BSA_BF16 && h.dtype != BSA_FP32) return fail(BSA_ERR_INVALID_ARG, "bad dtype %d", h.dtype);
+    const int64_t most = int64_t(1) << 40;
+    if (h.n > most || h.batch > most / h.n || h.heads > most / (h.n * h.batch))
+        return fail(BSA_ERR_UNSUPPORTED, "batch * heads * n must be <= 2^40");
+    if (rot.rot < 2 || rot.rot % 2 != 0 || rot.rot > h.d)
+        return fail(BSA_ERR_INVALID_ARG, "rot must be even and in [2, d] (got %d)", rot.rot);
+    if (rot.table == nullptr) return fail(BSA_ERR_INVALID_ARG, "rotation table is NULL");
+    if (!aligned(rot.table, 8)) return fail(BSA_ERR_ALIGNMENT, "rotation table is not 8-byte aligned");
+    if (!std::isfinite(rot.factor)) return fail(BSA_ERR_INVALID_ARG, "factor must be finite");
+    if (positions != nullptr && !aligned(positions, 4))
+        return fail(BSA_ERR_ALIGNMENT, "positions is not 4-byte aligned");
+    BSA_TRY(check_ptr(x, "x"));
+    BSA_TRY(check_ptr(out, "out"));
+    const int64_t vec = h.dtype == BSA_BF16 ? 8 : 4, esize = h.dtype == BSA_BF16 ? 2 : 4;
+    const int64_t size[3] = {h.batch, h.heads, h.n};
+    const int64_t xst[3] = {xs.batch, xs.head, xs.token}, ost[3] = {os.batch, os.head, os.token};
+    int64_t x_end = h.d, o_end = h.d;      // one past the last element
+    bool same = x == out;
+    for (int i = 0; i < 3; ++i) {
+        if (size[i] == 1) continue;
+        if (xst[i] < 0 || ost[i] < 0 || xst[i] >= most || ost[i] >= most)
+            return fail(BSA_ERR_UNSUPPORTED, "strides must be in [0, 2^40)");
+        if (xst[i] % vec != 0 || ost[i] % vec != 0)
+            return fail(BSA_ERR_ALIGNMENT, "strides must be multiples of 16 bytes");
+        if (xst[i] * double(size[i]) > 4e18 / 64 || ost[i] * double(size[i]) > 4e18 / 64)
+            return fail(BSA_ERR_UNSUPPORTED, "tensor extent is too large");
+        x_end += xst[i] * (size[i] - 1);
+        o_end += ost[i] * (size[i] - 1);
+        same = same && xst[i] == ost[i];
+    }
+    // rows of out must be apart: from the smallest stride up, each is at
+    // least the extent of what lies below it
+    int order[3] = {0, 1, 2};
+    std::sort(order, order + 3, [&](int a, int b) { return ost[a] < ost[b]; });
+    int64_t extent = h.d;
+    for (int i : order) {
+        if (size[i] == 1) continue;
+        if (ost[i] < extent) return fail(BSA_ERR_INVALID_ARG, "rows of out overlap");
+        extent += ost[i] * (size[i] - 1);
+    }
+    const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), o0 = reinterpret_cast<uintptr_t>(out);
+    if (!same && x0 < o0 + uintptr_t(o_end * esize) && o0 < x0 + uintptr_t(x_end * esize))
+        return fail(BSA_ERR_INVALID_ARG, "out overlaps x but is not x with x's strides");
+    bsa::RopeArgs a = {};
+    a.x = x;
+    a.out = out;
+    a.positions = positions;
+    a.table = rot.table;
+    a.first = first;
+    a.batch = h.batch;
+    a.n = h.n;
+    a.heads = h.heads;
+    a.d = h.d;
+    a.rot = rot.rot;
+    a.xs_b = xs.batch;
+    a.xs_h = xs.head;
+    a.xs_n = xs.token;
+    a.os_b = os.batch;
+    a.os_h = os.head;
+    a.os_n = os.token;
+    a.factor = rot.factor;
+    a.sign = sign;
+    a.in_place = same ? 1 : 0;
+    a.heads_inner = os.head < os.token ? 1 : 0;
+    return launched(bsa::launch_rope(a, h.dtype, rot.interleaved != 0, static_cast<cudaStream_t>(stream)),
+                    "rotary launch");
+}
+
+bsa_status bsa_rope(bsa_heads shape, const void *x, bsa_strides x_strides,
+                    const int32_t *positions, int64_t first, bsa_rotation rotation, void *out,
+                    bsa_strides out_strides, void *stream) {
+    return rope_impl(shape, x, x_strides, positions, first, rotation, 1.f, out, out_strides, stream);
+}
+
+bsa_status bsa_rope_backward(bsa_heads shape, const void *dout, bsa_strides dout_strides,
+                             const int32_t *positions, int64_t first, bsa_rotation rotation,
+                             void *dx, bsa_strides dx_strides, void *stream) {
+    return rope_impl(shape, dout, dout_strides, positions, first, rotation, -1.f, dx, dx_strides,
+                     stream);
+}
+
+// -------------------------------------------------------------- paged cache
+static bsa_status cache_view(const bsa_cache &c, bsa::CacheView *v) {
+    if (c.d != 64 && c.d != 128) return fail(BSA_ERR_UNSUPPORTED, "d must be 64 or 128 (got %d)", c.d);
+    if (c.page != 16 && c.page != 32 && c.page != 64 && c.page != 128)
+        return fail(BSA_ERR_UNSUPPORTED, "page must be 16, 32, 64 or 128 (got %d)", c.page);
+    if (c.num_pages < 1 || c.heads < 1)
+        return fail(BSA_ERR_INVALID_ARG, "num_pages and heads must be >= 1");
+    if (c.num_pages > 0x7fffffff || c.heads > 65535)
+        return fail(BSA_ERR_UNSUPPORTED, "num_pages must fit in int32, heads in 16 bits");
+    BSA_TRY(check_ptr(c.k, "cache.k"));
+    BSA_TRY(check_ptr(c.v, "cache.v"));
+    BSA_TRY(check_ptr(c.kbar, "cache.kbar"));
+    *v = {static_cast<uint16_t *>(c.k), static_cast<uint16_t *>(c.v), c.kbar, c.num_pages, c.heads,
+          c.page, c.d};
+    return BSA_OK;
+}
+
+static bsa_status check_i32(const int32_t *p, const char *name) {
+    if (p == nullptr) return fail(BSA_ERR_INVALID_ARG, "%s is NULL", name);
+    if (!aligned(p, 4)) return fail(BSA_ERR_ALIGNMENT, "%s is not 4-byte aligned", name);
+    return BSA_OK;
+}
+
+static bsa_status check_token_stride(int64_t stride, int64_t row, const char *name) {
+    if (stride < row) return fail(BSA_ERR_INVALID_ARG, "%s must be >= heads * d", name);
+    if (stride % 8 != 0) return fail(BSA_ERR_ALIGNMENT, "%s must be a multiple of 8", name);
+    if (stride >= (int64_t(1) << 31)) return fail(BSA_ERR_UNSUPPORTED, "%s must be < 2^31", name);
+    return BSA_OK;
+}
+
+bsa_status bsa_cache_append(bsa_cache cache, const void *k, int64_t k_stride, const void *v,
+                            int64_t v_stride, int64_t tokens, int64_t seqs,
+                            const int32_t *cu_tokens, const int32_t *start, const int32_t *table,
+                            int32_t table_width, void *stream) {
+    bsa::AppendArgs a = {};
+    BSA_TRY(cache_view(cache, &a.c));
+    if (tokens < 0 || seqs < 1 || table_width < 1)
+        return fail(BSA_ERR_INVALID_ARG, "tokens must be >= 0, seqs and table_width >= 1");
+    if (tokens > 0x7fffffff || seqs > 0x7fffff)
+        return fail(BSA_ERR_UNSUPPORTED, "tokens must fit in int32, seqs in 23 bits");
+    if (cu_tokens == nullptr && tokens % seqs != 0)
+        return fail(BSA_ERR_INVALID_ARG, "tokens must be a multiple of seqs without cu_tokens");
+    if (tokens == 0) return ok();           // k and v may be empty then
+    BSA_TRY(check_ptr(k, "k"));
+    BSA_TRY(check_ptr(v, "v"));
+    BSA_TRY(check_token_stride(k_stride, int64_t(cache.heads) * cache.d, "k_stride"));
+    BSA_TRY(check_token_stride(v_stride, int64_t(cache.heads) * cache.d, "v_stride"));
+    if (cu_tokens != nullptr) BSA_TRY(check_i32(cu_tokens, "cu_tokens"));
+    BSA_TRY(check_i32(start, "start"));
+    BSA_TRY(check_i32(table, "table"));
+    a.k = static_cast<const uint16_t *>(k);
+    a.v = static_cast<const uint16_t *>(v);
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.tokens = tokens;
+    a.seqs = seqs;
+    a.cu = cu_tokens;
+    a.start = start;
+    a.table = table;
+    a.width = table_width;
+    a.status = device_status_ptr();
+    if (a.status == nullptr) return fail(BSA_ERR_CUDA, "status word unavailable");
+    return launched(bsa::launch_cache_append(a, static_cast<cudaStream_t>(stream)), "append launch");
+}
+
+bsa_status bsa_cache_copy_pages(bsa_cache cache, const int32_t *pairs, int64_t count, void *stream) {
+    bsa::CacheView c;
+    BSA_TRY(cache_view(cache, &c));
+    if (count < 0) return fail(BSA_ERR_INVALID_ARG, "count must be >= 0");
+    if (count == 0) return ok();
+    BSA_TRY(check_i32(pairs, "pairs"));
+    int32_t *status = device_status_ptr();
+    if (status == nullptr) return fail(BSA_ERR_CUDA, "status word unavailable");
+    return launched(bsa::launch_copy_pages(c, pairs, count, status, static_cast<cudaStream_t>(stream)),
+                    "page copy launch");
+}
+
+bsa_status bsa_paged_decode(bsa_cache cache, const void *q, int64_t q_stride, int64_t tokens,
+                            int32_t q_heads, const int32_t *table, int32_t table_width,
+                            int64_t seqs, const int32_t *token_seq, const int32_t *lens,
+                            int32_t topk, const bsa_decode_options *options, float scale,
+                            void *out, int32_t *idx_out, void *stream) {
+    bsa::DecodeArgs a = {};
+    BSA_TRY(cache_view(cache, &a.c));
+    if (tokens < 1 || seqs < 1 || table_width < 1)
+        return fail(BSA_ERR_INVALID_ARG, "tokens, seqs and table_width must be >= 1");
+    if (tokens > 0x7fffffff || seqs > 0x7fffffff)
+        return fail(BSA_ERR_UNSUPPORTED, "tokens and seqs must fit in int32");
+    if (q_heads < 1 || q_heads % cache.heads != 0)
+        return fail(BSA_ERR_INVALID_ARG, "q_heads must be a multiple of the cache's heads");
+    if (q_heads / cache.heads > bsa::kDecodeMaxGroup)
+        return fail(BSA_ERR_UNSUPPORTED, "at most %d query heads per cache head", bsa::kDecodeMaxGroup);
+    if (topk < 1 || topk > 32) return fail(BSA_ERR_UNSUPPORTED, "topk must be in [1, 32] (got %d)", topk);
+    if (table_width > bsa::kDecodeMaxWidth)
+        return fail(BSA_ERR_UNSUPPORTED, "table_width must be <= %d", bsa::kDecodeMaxWidth);
+    if (token_seq == nullptr && seqs < tokens)
+        return fail(BSA_ERR_INVALID_ARG, "without token_seq there must be a sequence per token");
+    BSA_TRY(check_ptr(q, "q"));
+    BSA_TRY(check_ptr(out, "out"));
+    BSA_TRY(check_token_stride(q_stride, int64_t(q_heads) * cache.d, "q_stride"));
+    BSA_TRY(check_i32(table, "table"));
+    BSA_TRY(check_i32(lens, "lens"));
+    if (token_seq != nullptr) BSA_TRY(check_i32(token_seq, "token_seq"));
+    if (idx_out != nullptr) BSA_TRY(check_i32(idx_out, "idx_out"));
+    if (std::isnan(scale)) return fail(BSA_ERR_INVALID_ARG, "scale is NaN");
+    a.q = static_cast<const uint16_t *>(q);
+    a.q_stride = q_stride;
+    a.tokens = tokens;
+    a.seqs = seqs;
+    a.q_heads = q_heads;
+    a.table = table;
+    a.width = table_width;
+    a.token_seq = token_seq;
+    a.lens = lens;
+    a.topk = topk;
+    a.local = options != nullptr && options->local_block ? 1 : 0;
+    a.share = options != nullptr && options->share_group ? 1 : 0;
+    a.scale_log2 = (scale > 0.f ? scale : 1.f / std::sqrt(float(cache.d))) * 1.4426950408889634f;
+    a.out = static_cast<uint16_t *>(out);
+    a.idx = idx_out;
+    a.status = device_status_ptr();
+    if (a.status == nullptr) return fail(BSA_ERR_CUDA, "status word unavailable");
+    return launched(bsa::launch_paged_decode(a, static_cast<cudaStream_t>(stream)), "decode launch");
 }
 
 // ------------------------------------------------------- failure path

@@ -186,4 +186,60 @@ bool fine_static_tc_supported(const FineArgs &a, int32_t dtype);
 size_t fine_static_tc_workspace(int64_t bh, int64_t n, int32_t kb);
 cudaError_t launch_fine_static_tc(const FineArgs &a, cudaStream_t st);
 
+// ---- rotary positions -------------------------------------------------
+struct RopeArgs {
+    const void *x;
+    void *out;
+    const int32_t *positions;     // [batch][n], or null: first + i
+    const uint64_t *table;        // [rot / 2] turns per position, units of 2^-64
+    int64_t first, batch, n;
+    int32_t heads, d, rot;
+    int64_t xs_b, xs_h, xs_n, os_b, os_h, os_n;   // strides in elements
+    float factor, sign;           // times cos and sin; sign of the angle
+    int32_t in_place;             // out is x: the copied channels are there
+    int32_t heads_inner;          // out holds a token's heads side by side
+};
+cudaError_t launch_rope(const RopeArgs &a, int32_t dtype, bool interleaved, cudaStream_t st);
+
+// ---- paged cache --------------------------------------------------------
+// k, v [num_pages][heads][page][d] bf16, kbar [num_pages][heads][d] fp32.
+struct CacheView {
+    uint16_t *k, *v;
+    float *kbar;
+    int64_t num_pages;
+    int32_t heads, page, d;
+};
+struct AppendArgs {
+    CacheView c;
+    const uint16_t *k, *v;        // [tokens][heads][d], token strides below
+    int64_t k_stride, v_stride, tokens, seqs;
+    const int32_t *cu;            // [seqs + 1], or null: tokens / seqs each
+    const int32_t *start;         // [seqs]
+    const int32_t *table;         // [seqs][width]
+    int32_t width;
+    int32_t *status;
+};
+cudaError_t launch_cache_append(const AppendArgs &a, cudaStream_t st);
+cudaError_t launch_copy_pages(const CacheView &c, const int32_t *pairs, int64_t count,
+                              int32_t *status, cudaStream_t st);
+
+struct DecodeArgs {
+    CacheView c;
+    const uint16_t *q;            // [tokens][q_heads][d], token stride below
+    int64_t q_stride, tokens, seqs;
+    int32_t q_heads;
+    const int32_t *table;         // [seqs][width]
+    int32_t width;
+    const int32_t *token_seq;     // [tokens], or null: token t is sequence t's
+    const int32_t *lens;          // [tokens]
+    int32_t topk, local, share;
+    float scale_log2;
+    uint16_t *out;                // [tokens][q_heads][d]
+    int32_t *idx;                 // optional [tokens][share ? heads : q_heads][topk]
+    int32_t *status;
+};
+constexpr int32_t kDecodeMaxWidth = 16384;   // blocks of a sequence
+constexpr int32_t kDecodeMaxGroup = 128;     // query heads of a cache head
+cudaError_t launch_paged_decode(const DecodeArgs &a, cudaStream_t st);
+
 }  // namespace bsa

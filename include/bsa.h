@@ -1,6 +1,7 @@
 /*
- * bsa.h -- C ABI of libbsa.so: content-dependent block-sparse attention
- * (forward) on one NVIDIA GB300 (sm_103a).
+ * bsa.h -- C ABI of libbsa.so: content-dependent block-sparse attention on
+ * one NVIDIA GB300 (sm_103a): the forward, its backward, rotary positions,
+ * and decoding of single tokens over a paged cache.
  *
  * The method (page "sparse-attention-triton-bench", section "Two-stage
  * block indexer"):
@@ -369,6 +370,225 @@ bsa_status bsa_forward_noalloc(bsa_shape shape, const void *q, const void *k,
                                const void *v, int32_t key_block, int32_t topk,
                                float scale, void *out, int32_t *idx_out,
                                void *stream);
+
+/*
+ * Rotary positions, on q and k before bsa_forward, bsa_cache_append or
+ * bsa_paged_decode, and their gradient.  (The pages do not rotate; a model
+ * around the method does.)  Pair i of a token at position p turns by
+ * t = p * f_i:
+ *   x_a' = m (x_a cos t - x_b sin t),  x_b' = m (x_b cos t + x_a sin t),
+ * with (a, b) = (i, i + rot/2), or (2i, 2i + 1) when interleaved; channels
+ * from rot on are copied.  Angles are exact in the position (below), the
+ * rotation is computed in fp32 and rounded once.
+ *
+ * The frequencies f_i are made on the host, in two steps so that a caller
+ * can put its own in between:
+ *   bsa_rope_frequencies  inv_freq[i] = theta^(-2i/rot), i < rot/2, scaled
+ *       for longer contexts (s = factor):
+ *         LINEAR  f / s;
+ *         BASE    theta * s^(rot/(rot-2)) in place of theta (rot >= 4);
+ *         PARTS   by the turns r = original * f / 2 pi a frequency makes
+ *                 over the original context: f where r >= high, f / s where
+ *                 r <= low, in between g f + (1 - g) f / s with
+ *                 g = (r - low) / (high - low).
+ *   bsa_rope_table        f as turns per position modulo one turn, in units
+ *       of 2^-64.  Products with a position wrap modulo one turn exactly.
+ * Both write HOST arrays; the caller copies the table to the device once.
+ */
+typedef enum {
+    BSA_ROPE_NONE = 0,
+    BSA_ROPE_LINEAR = 1,
+    BSA_ROPE_BASE = 2,
+    BSA_ROPE_PARTS = 3
+} bsa_rope_scaling;
+
+typedef struct {
+    int32_t rot;            /* rotated channels, even                       */
+    int32_t scaling;        /* bsa_rope_scaling                             */
+    double theta;           /* base of the frequencies                      */
+    double factor;          /* s (ignored by NONE)                          */
+    double original;        /* PARTS: tokens of the original context        */
+    double low, high;       /* PARTS: bounds on the turns, low < high       */
+} bsa_rope_params;
+
+bsa_status bsa_rope_frequencies(bsa_rope_params params, double *inv_freq);
+bsa_status bsa_rope_table(const double *inv_freq, int32_t count, uint64_t *table);
+
+/*
+ * x and out are [batch][heads][n][d] in any order of strides (in elements;
+ * the d channels of a row contiguous), so that q and k can be rotated where a
+ * projection left them and come out in the layout bsa_forward takes.
+ *   positions  int32 [batch][n] (device), or NULL: token i is at first + i.
+ *              Any int32 value, negative ones too.
+ *   rotation   table (DEVICE uint64 [rot/2], from bsa_rope_table), rot even
+ *              and in [2, d], layout, and the factor m on cos and sin.
+ *   out        may be x itself, with x's strides; otherwise the two must not
+ *              overlap.  Rows of out must not overlap (no stride 0); x may be
+ *              broadcast.
+ * bf16 or fp32; d in {64, 128}; strides multiples of 16 bytes, not negative.
+ * bsa_rope_backward: dx = the gradient with respect to x given dout (the
+ * same map with -t; m applies again, the map being linear).
+ */
+typedef struct {
+    int64_t batch, n;
+    int32_t heads, d, dtype;
+} bsa_heads;
+
+typedef struct {
+    int64_t batch, head, token;
+} bsa_strides;
+
+typedef struct {
+    const uint64_t *table;
+    int32_t rot;
+    int32_t interleaved;
+    float factor;
+} bsa_rotation;
+
+bsa_status bsa_rope(bsa_heads shape, const void *x, bsa_strides x_strides,
+                    const int32_t *positions, int64_t first, bsa_rotation rotation,
+                    void *out, bsa_strides out_strides, void *stream);
+bsa_status bsa_rope_backward(bsa_heads shape, const void *dout, bsa_strides dout_strides,
+                             const int32_t *positions, int64_t first, bsa_rotation rotation,
+                             void *dx, bsa_strides dx_strides, void *stream);
+
+/*
+ * A paged key/value cache.  A page is one key block of the selection: it
+ * holds `page` tokens' K and V of every head, and the mean of its keys, so
+ * that decoding scores pages without reading their keys.  Sequence s's block
+ * b (tokens [b * page, (b + 1) * page)) is in page table[s][b].
+ *   k, v   [num_pages][heads][page][d] bf16 (device)
+ *   kbar   [num_pages][heads][d] fp32 (device): the mean of the rows the last
+ *          append left filled
+ * page in {16, 32, 64, 128}, d in {64, 128}, heads <= 65535.
+ */
+typedef struct {
+    void *k;
+    void *v;
+    float *kbar;
+    int64_t num_pages;
+    int32_t heads, page, d;
+} bsa_cache;
+
+/*
+ * Appends new tokens' K and V to their sequences' pages and writes the means
+ * of the pages they fall in (over all of a page's filled rows, so a call may
+ * be repeated, and a sequence that was cut short may be appended to).
+ *   k, v        [tokens][heads][d] bf16 (device), the tokens of sequence 0
+ *               first; k_stride, v_stride: elements from a token to the next
+ *               (multiples of 8, >= heads * d).  They must not overlap the
+ *               cache.
+ *   cu_tokens   int32 [seqs + 1] (device): sequence s has the tokens
+ *               [cu[s], cu[s + 1]), possibly none; tokens from cu[seqs] on
+ *               are ignored.  NULL: tokens / seqs each (it must divide).
+ *   start       int32 [seqs] (device): tokens each sequence holds already.
+ *   table       int32 [seqs][table_width] (device).  A page may be listed by
+ *               several sequences, but a page that is written to by one only.
+ * A sequence whose new tokens do not fit its table (or whose cu_tokens or
+ * start make no sense) is skipped and reported as BSA_ERR_INVALID_ARG
+ * through bsa_get_device_status(), a page outside [0, num_pages) is skipped
+ * and reported as BSA_ERR_BAD_INDEX.
+ */
+bsa_status bsa_cache_append(bsa_cache cache, const void *k, int64_t k_stride, const void *v,
+                            int64_t v_stride, int64_t tokens, int64_t seqs,
+                            const int32_t *cu_tokens, const int32_t *start,
+                            const int32_t *table, int32_t table_width, void *stream);
+
+/*
+ * Copies whole pages (K, V and means): pairs int32 [count][2] (device) of
+ * (from, to).  No page may be the target of two pairs, nor the target of one
+ * and the source of another (bsa_pages_take_copies and bsa_pages_compact
+ * give such lists).  A pair with a page outside [0, num_pages) is skipped and
+ * reported as BSA_ERR_BAD_INDEX.
+ */
+bsa_status bsa_cache_copy_pages(bsa_cache cache, const int32_t *pairs, int64_t count,
+                                void *stream);
+
+/*
+ * Decoding: the two stages of the method for single tokens over the paged
+ * cache, in one launch.  Token t of sequence token_seq[t] sees its first
+ * lens[t] keys.  Every query head h scores the ceil(lens[t] / page) blocks of
+ * cache head h / (q_heads / heads) (score = q . kbar, unscaled), keeps its
+ * topk best, and attends to their keys j < lens[t].  The selection is that of
+ * the scores' exact values for the given kbar (close calls are settled in
+ * fp64), ties to the lower block id; a NaN score ranks as -inf.
+ *   q          [tokens][q_heads][d] bf16 (device); q_stride: elements from a
+ *              token to the next (multiple of 8, >= q_heads * d).
+ *   table      int32 [seqs][table_width] (device), table_width <= 16384.
+ *   token_seq  int32 [tokens] (device) in [0, seqs), or NULL: token t is
+ *              sequence t's (seqs >= tokens then).
+ *   lens       int32 [tokens] (device), the token itself included.  0: the
+ *              output row is zero.
+ *   options    NULL = none;
+ *              local_block  the last block (the token's own) is always
+ *                           selected; topk - 1 others compete.
+ *              share_group  the query heads of a cache head share one
+ *                           selection, made on the sum of their scores.
+ *   scale      softmax scale; <= 0 selects 1/sqrt(d).
+ *   out        [tokens][q_heads][d] bf16 (device).
+ *   idx_out    optional int32 (device) [tokens][q_heads][topk], or
+ *              [tokens][heads][topk] with share_group: the selected blocks,
+ *              ascending, -1 after the last.
+ * topk in [1, 32]; q_heads a multiple of heads, at most 128 per cache head.
+ * Only pages that hold one of the first lens[t] keys are looked up.  One
+ * outside [0, num_pages) is reported as BSA_ERR_BAD_INDEX; its block scores
+ * -inf, and its keys are skipped if it is selected all the same.  lens
+ * outside [0, table_width * page] is clamped and reported as
+ * BSA_ERR_INVALID_ARG; a token_seq outside [0, seqs) is reported as
+ * BSA_ERR_BAD_INDEX and the token's row is zero.
+ */
+typedef struct {
+    int32_t local_block;
+    int32_t share_group;
+} bsa_decode_options;
+
+bsa_status bsa_paged_decode(bsa_cache cache, const void *q, int64_t q_stride, int64_t tokens,
+                            int32_t q_heads, const int32_t *table, int32_t table_width,
+                            int64_t seqs, const int32_t *token_seq, const int32_t *lens,
+                            int32_t topk, const bsa_decode_options *options, float scale,
+                            void *out, int32_t *idx_out, void *stream);
+
+/*
+ * Which sequence owns which page, on the host: page counts of references,
+ * copy on write, and the copies that bsa_cache_copy_pages has to make.  It
+ * touches no device memory; a handle is used by one thread at a time.
+ *   create      a pool of num_pages pages of `page` tokens, max_seqs empty
+ *               sequences with at most table_width pages each.
+ *   reserve     makes room for `tokens` more tokens of a sequence and counts
+ *               them as there.  If its partly filled last page is shared, the
+ *               sequence gets a page of its own and a copy is queued.
+ *               All or nothing: BSA_ERR_WORKSPACE when the pool or the table
+ *               is too small.
+ *   fork        the empty sequence `to` gets all of `from`'s tokens, sharing
+ *               the pages.
+ *   truncate    keeps the first `length` tokens; pages nobody holds any more
+ *               become free (length 0: all of them).
+ *   take_copies hands out the queued copies, pairs HOST int32 [capacity][2],
+ *               and empties the queue.  Run them (in stream order) before
+ *               anything is appended to the cache.  pairs NULL: only
+ *               *count is written.  A page that a queued copy reads is not
+ *               given away until then.  BSA_ERR_WORKSPACE when capacity is
+ *               too small (nothing is taken).
+ *   compact     moves the pages in use to the lowest ids; pairs as above, at
+ *               most num_pages / 2 of them.  Not while copies are queued
+ *               (BSA_ERR_INVALID_ARG).
+ *   tables      HOST int32 [max_seqs][table_width] (-1 after a sequence's
+ *               pages) and int32 [max_seqs] lengths; either may be NULL.
+ *   free_pages  pages nobody holds; -BSA_ERR_INVALID_ARG without a handle.
+ * A sequence's length is at most 2^31 - 1.
+ */
+typedef struct bsa_pages_s *bsa_pages;
+bsa_status bsa_pages_create(int64_t num_pages, int32_t page, int32_t max_seqs,
+                            int32_t table_width, bsa_pages *pages);
+bsa_status bsa_pages_destroy(bsa_pages pages);
+bsa_status bsa_pages_reserve(bsa_pages pages, int32_t seq, int64_t tokens);
+bsa_status bsa_pages_fork(bsa_pages pages, int32_t from, int32_t to);
+bsa_status bsa_pages_truncate(bsa_pages pages, int32_t seq, int64_t length);
+bsa_status bsa_pages_take_copies(bsa_pages pages, int32_t *pairs, int64_t capacity,
+                                 int64_t *count);
+bsa_status bsa_pages_compact(bsa_pages pages, int32_t *pairs, int64_t capacity, int64_t *count);
+bsa_status bsa_pages_tables(bsa_pages pages, int32_t *table, int32_t *lengths);
+int64_t bsa_pages_free_pages(bsa_pages pages);
 
 /* Number of kernel launches one bsa_forward call enqueues for this problem
  * (for launch accounting by callers); negative bsa_status on bad arguments. */
