@@ -11,26 +11,32 @@
 //               group; fp32 dot products, reduced over the lanes by an
 //               exchange that halves the number of values at each step.
 //               The scores stay in shared memory as order-preserving keys.
-//   2. top-k    each CTA's k best keys go through distributed shared memory;
-//               the k-th best of all, t, is known to every CTA.  A score is
-//               off its true value by at most e (a bound from the sums of
-//               |q| and the largest |mean|), so blocks above t + 2e are
-//               selected for certain and blocks below t - 2e are not.  Where
-//               more blocks than wanted lie between, those are scored again
-//               in fp64 (ties to the lower id).  The selection is therefore
-//               that of the exact scores, whatever the order of the sums.
+//   2. top-k    a warp sorts its share's best 32 (key, id) and each CTA gives
+//               its list to the whole cluster (distributed shared memory), so
+//               that every CTA merges all lists and knows t, the k-th best.
+//               A score is off its true value by at most e (a bound from the
+//               sums of |q| and the largest |mean|), so blocks above t + 2e
+//               are selected for certain and blocks below t - 2e are not.
+//               Where more blocks than wanted lie between, those are scored
+//               again in fp64 (ties to the lower id).  The selection is
+//               therefore that of the exact scores, whatever the order of the
+//               sums.
 //   3. attention over the union of the heads' selected blocks, each loaded
 //               once: a warp takes 16 keys at a time straight from global
 //               memory into mma fragments (no shared memory between), S^T =
 //               K Q^T and O^T += V^T P^T with the group's heads as the
 //               8-wide side; a head that did not select the block is masked.
-//               Online softmax per warp, merged over the warps and then over
-//               the cluster.
+//               K of the next keys is requested as soon as the scores of
+//               these are done, V as soon as their product is.  Online
+//               softmax per warp, merged over the warps and then over the
+//               cluster, each CTA receiving its share of the outputs.
 // Bound: memory (block means and selected K, V once); with one sequence, the
-// latency of the chain table -> means -> merge -> keys.  m16n8k16 mma.sync
-// carries it: 8 or 16 rows against 16 keys is far below a tcgen05 tile (128
-// rows), and the keys arrive at about 23 bytes a clock and SM.
+// latency of the chain table -> means -> merge -> table -> keys.  m16n8k16
+// mma.sync carries it: 8 or 16 rows against 16 keys is far below a tcgen05
+// tile (128 rows), and the keys arrive at about 23 bytes a clock and SM.
 #include <cooperative_groups.h>
+
+#include <utility>
 
 #include "bsa_device.cuh"
 #include "bsa_internal.h"
@@ -40,11 +46,12 @@ namespace cg = cooperative_groups;
 namespace bsa {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxRows = 16;        // query heads of one cluster
 constexpr int kMaxK = 32;
 constexpr int kMaxItems = kMaxRows * kMaxK;
-constexpr int kListCap = 256;       // candidates a warp holds in registers
+constexpr int kMaxWarps = 12;
+constexpr int kMaxCluster = 8;
+constexpr int kListCap = 256;       // candidates of a filtered list
 constexpr int kMaxLocal = 2048;     // blocks one CTA scores
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kNegInf = -__builtin_huge_valf();
@@ -57,23 +64,34 @@ struct Plan {
     int32_t score_rows;   // rows, or 1 when the group shares the selection
     int32_t segs;         // warps that share a row's local top-k
     int32_t nloc;         // score slots of a row
-    int32_t gath_off, main_off;
+    int32_t list_off, part_off, main_off;
+};
+
+// A CTA's best of one row, largest key first; `next` is the largest key that
+// is not in the list (0: none).
+struct List {
+    uint32_t key[kMaxK];
+    uint16_t id[kMaxK];
+    uint32_t next;
 };
 
 struct Fixed {
     double dscore[kMaxRows][kMaxK];
-    uint32_t cand[kMaxRows][kMaxK];
-    uint32_t list[kWarps][kListCap];
-    int32_t sel[kMaxRows][kMaxK];    // own blocks at or above t - 2e, the first 32
-    int32_t def[kMaxRows][kMaxK];    // own blocks above t + 2e
+    uint64_t seg[kMaxWarps][kMaxK];     // sorted lists of a row's parts
+    uint32_t seg_next[kMaxWarps];
+    uint16_t cand[kMaxWarps][kListCap];
+    int32_t def[kMaxRows][kMaxK];    // re-scoring: own blocks above t + 2e
     int32_t did[kMaxRows][kMaxK];    // own best re-scored blocks
     int32_t fin[kMaxRows][kMaxK];    // the row's selection without the forced block
-    int32_t nsel[kMaxRows], ndef[kMaxRows], nd[kMaxRows], slow[kMaxRows];
+    int32_t ndef[kMaxRows], nd[kMaxRows], slow[kMaxRows];
     uint32_t lo[kMaxRows], hi[kMaxRows];
     uint32_t bits[kDecodeMaxWidth / 32], pref[kDecodeMaxWidth / 32];
-    int32_t items[kMaxItems], pages[kMaxItems];
+    int32_t pages[kMaxItems];
     uint32_t masks[kMaxItems];
-    float wm[kWarps][kMaxRows], wl[kWarps][kMaxRows], pm[kMaxRows], pl[kMaxRows];
+    uint16_t items[kMaxItems];
+    float wm[kMaxWarps][kMaxRows], wl[kMaxWarps][kMaxRows];
+    float pm[kMaxCluster][kMaxRows], pl[kMaxCluster][kMaxRows];   // of every CTA
+    uint32_t kmaxes[kMaxCluster];
     uint32_t kmax;
     int32_t any_slow, n_items;
 };
@@ -88,63 +106,144 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-// The k-th largest of the warp's 32 N keys, known to be in [low, high]: bits
-// are settled from the highest in which the two ends differ.
-template <int N>
-__device__ __forceinline__ uint32_t kth_in_regs(const uint32_t (&x)[N], int k, uint32_t low,
-                                                uint32_t high) {
-    if (low == high) return low;
-    const int top = 31 - __clz(low ^ high);
-    uint32_t t = top == 31 ? 0u : (high >> (top + 1)) << (top + 1);
-    for (int bit = top; bit >= 0; --bit) {
-        const uint32_t c = t | (1u << bit);
-        int n = 0;
-#pragma unroll
-        for (int i = 0; i < N; ++i) n += __popc(__ballot_sync(kFull, x[i] >= c));
-        if (n >= k) t = c;
-    }
-    return t;
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
-// The k-th largest of a[0, n), 1 <= k <= min(32, n).  k of the 32 lanes'
-// maxima are at or above the k-th largest of these, so only elements from
-// there on are looked at (about 20 to 100 of 2048).
-__device__ uint32_t kth_largest(const uint32_t *a, int n, int k, uint32_t *list, int lane) {
-    uint32_t mx[1] = {0u};
-    for (int i = lane; i < n; i += 32) mx[0] = max(mx[0], a[i]);
-    const uint32_t high = __reduce_max_sync(kFull, mx[0]);
-    const uint32_t low = max(1u, kth_in_regs<1>(mx, k, 0u, high));   // 0 pads a list
-    if (n <= 32) return low;
-    int m = 0;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-        const uint32_t x = i0 + lane < n ? a[i0 + lane] : 0u;
-        const bool in = i0 + lane < n && x >= low;
-        const uint32_t b = __ballot_sync(kFull, in);
-        const int at = m + __popc(b & ((1u << lane) - 1));
-        if (in && at < kListCap) list[at] = x;
-        m += __popc(b);
-    }
-    __syncwarp();
-    if (m <= kListCap) {
-        uint32_t x[kListCap / 32];
+// Bitonic networks over the 32 lanes, largest first, B independent lists at
+// once (the exchanges of one hide the latency of the others').
+template <typename T, int B>
+__device__ __forceinline__ void sort32(T (&x)[B], int lane) {
 #pragma unroll
-        for (int i = 0; i < kListCap / 32; ++i)
-            x[i] = i * 32 + lane < m ? list[i * 32 + lane] : 0u;
-        const uint32_t t = kth_in_regs(x, k, low, high);
+    for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+        for (int j = size / 2; j > 0; j /= 2) {
+            const bool larger = ((lane & j) == 0) == ((lane & size) == 0);
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const T y = __shfl_xor_sync(kFull, x[b], j);
+                x[b] = larger == (x[b] > y) ? x[b] : y;
+            }
+        }
+}
+
+// Merges pairs of sorted lists, x[i] with x[i + N], into their best 32;
+// `low` keeps the largest of what falls out.
+template <typename T, int B, int N>
+__device__ __forceinline__ void merge32(T (&x)[B], T &low, int lane) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const T y = __shfl_sync(kFull, x[i + N], 31 - lane);
+        const T out = x[i] > y ? y : x[i];
+        x[i] = x[i] > y ? x[i] : y;
+        low = low > out ? low : out;
+    }
+#pragma unroll
+    for (int j = 16; j > 0; j /= 2)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const T y = __shfl_xor_sync(kFull, x[i], j);
+            x[i] = ((lane & j) == 0) == (x[i] > y) ? x[i] : y;
+        }
+}
+template <typename T, int B>
+__device__ __forceinline__ void merge_all(T (&x)[B], T &low, int lane) {
+    if constexpr (B >= 16) merge32<T, B, 8>(x, low, lane);
+    if constexpr (B >= 8) merge32<T, B, 4>(x, low, lane);
+    if constexpr (B >= 4) merge32<T, B, 2>(x, low, lane);
+    if constexpr (B >= 2) merge32<T, B, 1>(x, low, lane);
+}
+
+// (key, index) as one number: a larger key first, then a lower index.
+__device__ __forceinline__ uint64_t composite(uint32_t key, int i) {
+    return (uint64_t(key) << 32) | uint32_t(0xffff - i);
+}
+
+// B batches of 32 keys a[index(i)], i < m, sorted and merged.
+template <int B, typename F>
+__device__ __forceinline__ uint64_t best32(const uint32_t *a, int m, F index, uint64_t &low, int lane) {
+    uint64_t x[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+        const int i = b * 32 + lane;
+        x[b] = 0;
+        if (i < m) {
+            const int j = index(i);
+            x[b] = composite(a[j], j);
+        }
+    }
+    sort32(x, lane);
+    merge_all(x, low, lane);
+    return x[0];
+}
+
+// The best 32 of a[0, n) (lane i has the i-th) and the largest key left out.
+// For many keys only those are sorted that are at or above the k-th largest
+// of the 32 lanes' maxima: k of the keys are, and few others (some 20 to 100
+// of 2048).
+__device__ uint64_t top32(const uint32_t *a, int n, int k, uint16_t *cand, uint32_t &next, int lane) {
+    const auto same = [](int i) { return i; };
+    uint64_t low = 0, best;
+    uint32_t rest = 0;
+    if (n <= 32) {
+        best = best32<1>(a, n, same, low, lane);
+    } else if (n <= 64) {
+        best = best32<2>(a, n, same, low, lane);
+    } else if (n <= 128) {
+        best = best32<4>(a, n, same, low, lane);
+    } else {
+        uint32_t mx[1] = {0u};
+#pragma unroll 8
+        for (int i = lane; i < n; i += 32) mx[0] = max(mx[0], a[i]);
+        sort32(mx, lane);
+        const uint32_t bound = __shfl_sync(kFull, mx[0], k - 1);
+        int m = 0;
+#pragma unroll 4
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const uint32_t x = i0 + lane < n ? a[i0 + lane] : 0u;
+            const bool in = i0 + lane < n && x >= bound;
+            const uint32_t b = __ballot_sync(kFull, in);
+            const int at = m + __popc(b & ((1u << lane) - 1));
+            if (in) {
+                if (at < kListCap) cand[at] = uint16_t(i0 + lane);
+            } else {
+                rest = max(rest, x);
+            }
+            m += __popc(b);
+        }
         __syncwarp();
-        return t;
+        const auto listed = [cand](int i) { return int(cand[i]); };
+        if (m <= 32) {
+            best = best32<1>(a, m, listed, low, lane);
+        } else if (m <= 64) {
+            best = best32<2>(a, m, listed, low, lane);
+        } else if (m <= 128) {
+            best = best32<4>(a, m, listed, low, lane);
+        } else if (m <= kListCap) {
+            best = best32<8>(a, m, listed, low, lane);
+        } else {                                // many equal scores
+            rest = 0;
+            best = 0;
+            for (int i0 = 0; i0 < n; i0 += 32) {
+                uint64_t x[2] = {best, i0 + lane < n ? composite(a[i0 + lane], i0 + lane) : 0};
+                const uint64_t worst = __shfl_sync(kFull, best, 31);
+                if (!__any_sync(kFull, x[1] > worst)) {
+                    low = low > x[1] ? low : x[1];
+                    continue;
+                }
+                uint64_t y[1] = {x[1]};
+                sort32(y, lane);
+                x[1] = y[0];
+                merge32<uint64_t, 2, 1>(x, low, lane);
+                best = x[0];
+            }
+        }
+        __syncwarp();
     }
-    // many equal scores: settle the bits over the whole array
-    if (low == high) return low;
-    const int top = 31 - __clz(low ^ high);
-    uint32_t t = top == 31 ? 0u : (high >> (top + 1)) << (top + 1);
-    for (int bit = top; bit >= 0; --bit) {
-        const uint32_t c = t | (1u << bit);
-        int cnt = 0;
-        for (int i = lane; i < n; i += 32) cnt += a[i] >= c;
-        if (__reduce_add_sync(kFull, cnt) >= k) t = c;
-    }
-    return t;
+    next = __reduce_max_sync(kFull, max(rest, uint32_t(low >> 32)));
+    return best;
 }
 
 // Sums each of NV values over the LPB lanes of a lane group: at each step a
@@ -214,7 +313,7 @@ __device__ __forceinline__ double score_fp64(const DecodeArgs &a, const Job &w, 
 }
 
 // Stage 1: the keys of the CTA's n blocks from b0 on, sc[row][nloc].
-template <int D, int RP>
+template <int D, int RP, int W>
 __device__ __forceinline__ void score_blocks(const DecodeArgs &a, const Plan &p, const Job &w,
                                              Fixed &f, uint32_t *sc, int b0, int n) {
     constexpr int LPB = D / 4;          // lanes per block
@@ -251,15 +350,20 @@ __device__ __forceinline__ void score_blocks(const DecodeArgs &a, const Plan &p,
     }
     const int srows = a.share ? 1 : w.rows;
     uint32_t big = 0;
-    for (int base = warp * U * BPL; base < n; base += kWarps * U * BPL) {
+    constexpr int kStep = W * U * BPL;
+    const int ahead = lane < U * BPL ? lane : n;       // this lane's block of a batch
+    int base = warp * U * BPL;
+    int entry = base + ahead < n ? w.table[b0 + base + ahead] : 0;
+    for (; base < n; base += kStep) {
         int mine = -1;
-        if (lane < U * BPL && base + lane < n) {
-            mine = w.table[b0 + base + lane];
+        if (base + ahead < n) {
+            mine = entry;
             if (mine < 0 || mine >= a.c.num_pages) {
                 report_status(a.status, kStatusBadIndex);
                 mine = -1;
             }
         }
+        if (base + kStep + ahead < n) entry = w.table[b0 + base + kStep + ahead];
         float4 x[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -302,63 +406,85 @@ __device__ __forceinline__ void score_blocks(const DecodeArgs &a, const Plan &p,
 
 // Stage 2: fills f.fin with the kk selected ids of every score row,
 // ascending.  Every CTA of the cluster ends with the same lists.
-template <int D>
+// lists[CTA][row] is filled by the cluster.
+template <int D, int W>
 __device__ __forceinline__ void select_blocks(const DecodeArgs &a, const Plan &p, const Job &w,
-                                              Fixed &f, uint32_t *sc, uint32_t *gath, int b0,
-                                              int n) {
+                                              Fixed &f, uint32_t *sc, List *lists, int b0, int n) {
     cg::cluster_group cluster = cg::this_cluster();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int srows = a.share ? 1 : w.rows, kk = w.kk, C = p.cluster;
-    const bool alone = C * p.segs == 1;
-    // the kk best keys of each part of a row
-    for (int task = warp; task < srows * p.segs && !alone; task += kWarps) {
+    if (threadIdx.x < C) cluster.map_shared_rank(&f, threadIdx.x)->kmaxes[w.rank] = f.kmax;
+    const auto give = [&](int row, uint64_t best, uint32_t next) {
+        const int at = 0xffff - int(uint32_t(best) & 0xffffu);
+        for (int c = 0; c < C; ++c) {
+            List *l = cluster.map_shared_rank(&lists[w.rank * p.score_rows + row], c);
+            l->key[lane] = uint32_t(best >> 32);
+            l->id[lane] = uint16_t(b0 + at);
+            if (lane == 0) l->next = next;
+        }
+    };
+    for (int task = warp; task < srows * p.segs; task += W) {
         const int row = task / p.segs, seg = task - row * p.segs;
         const int per = (n + p.segs - 1) / p.segs;
         const int i0 = min(n, seg * per), m = min(n, i0 + per) - i0;
-        const uint32_t *s = sc + row * p.nloc + i0;
-        uint32_t *out = f.cand[task];
-        if (m <= kk) {
-            out[lane] = lane < m ? s[lane] : 0u;
-            continue;
+        uint32_t next;
+        uint64_t best = top32(sc + row * p.nloc + i0, m, kk, f.cand[warp], next, lane);
+        if (best != 0) best -= uint64_t(i0);            // the row's index
+        if (p.segs == 1) {
+            give(row, best, next);
+        } else {
+            f.seg[task][lane] = best;
+            if (lane == 0) f.seg_next[task] = next;
         }
-        const uint32_t t = kth_largest(s, m, kk, f.list[warp], lane);
-        int at = 0;
-        for (int j = 0; j < m; j += 32) {
-            const bool in = j + lane < m && s[j + lane] > t;
-            const uint32_t b = __ballot_sync(kFull, in);
-            if (in) out[at + __popc(b & ((1u << lane) - 1))] = s[j + lane];
-            at += __popc(b);
-        }
-        if (lane >= at) out[lane] = lane < kk ? t : 0u;
     }
-    cluster.sync();
-    const int G = C * p.segs;               // lists of a row
-    if (!alone) {
-        // rank by rank of the lists, so that a lane of kth_largest meets them all
-        for (int i = threadIdx.x; i < srows * G * kMaxK; i += kThreads) {
-            const int row = i / (G * kMaxK), j = i - row * (G * kMaxK), list = j / kMaxK;
-            const int c = list / p.segs, s = list - c * p.segs;
-            gath[row * G * kMaxK + (j % kMaxK) * G + list] =
-                cluster.map_shared_rank(&f, c)->cand[row * p.segs + s][j % kMaxK];
-        }
+    if (p.segs > 1) {
         __syncthreads();
+        for (int row = warp; row < srows; row += W) {
+            uint64_t x[8], low = 0;
+            uint32_t next = 0;
+#pragma unroll
+            for (int s = 0; s < 8; ++s) x[s] = s < p.segs ? f.seg[row * p.segs + s][lane] : 0;
+            if (lane < p.segs) next = f.seg_next[row * p.segs + lane];
+            if (p.segs > 4) merge32<uint64_t, 8, 4>(x, low, lane);
+            if (p.segs > 2) merge32<uint64_t, 8, 2>(x, low, lane);
+            merge32<uint64_t, 8, 1>(x, low, lane);
+            next = __reduce_max_sync(kFull, max(next, uint32_t(low >> 32)));
+            give(row, x[0], next);
+        }
     }
-    for (int row = warp; row < srows; row += kWarps) {
+    if (C > 1)
+        cluster.sync();
+    else
+        __syncthreads();
+    for (int row = warp; row < srows; row += W) {
         // t, the kk-th best of the whole row
-        const uint32_t t = alone ? kth_largest(sc + row * p.nloc, n, kk, f.list[warp], lane)
-                                 : kth_largest(gath + row * G * kMaxK, G * kMaxK, kk, f.list[warp],
-                                               lane);
-        uint32_t kmax = 0;
-        for (int c = 0; c < C; ++c) kmax = max(kmax, cluster.map_shared_rank(&f, c)->kmax);
+        uint32_t key[kMaxCluster], x[kMaxCluster], low = 0, kmax = 0, next = 0;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c)
+            x[c] = key[c] = c < C ? lists[c * p.score_rows + row].key[lane] : 0u;
+        if (lane < C) {
+            next = lists[lane * p.score_rows + row].next;
+            kmax = f.kmaxes[lane];
+        }
+        kmax = __reduce_max_sync(kFull, kmax);
+        if (C > 4) merge32<uint32_t, 8, 4>(x, low, lane);
+        if (C > 2) merge32<uint32_t, 8, 2>(x, low, lane);
+        if (C > 1) merge32<uint32_t, 8, 1>(x, low, lane);
+        const uint32_t t = __shfl_sync(kFull, x[0], kk - 1);
         // |computed - true| <= e: at most 4 + 5 roundings on a path of the
         // sum, 2^-24 each of sum |q||mean|, which is at most sum |q| times
         // the largest |mean|; a shared row's q is itself a sum of `group`
         // terms.  16 + group leaves room for this bound's own roundings.
         float qa = 0.f;
         const int h0 = w.head * p.group + (a.share ? 0 : w.row0 + row);
-        for (int g = 0; g < (a.share ? p.group : 1); ++g) {
-            const uint16_t *q = a.q + int64_t(w.token) * a.q_stride + int64_t(h0 + g) * D;
-            for (int e = lane; e < D; e += 32) qa += fabsf(__uint_as_float(uint32_t(q[e]) << 16));
+        const uint16_t *q = a.q + int64_t(w.token) * a.q_stride + int64_t(h0) * D;
+#pragma unroll 4
+        for (int e = lane; e < (a.share ? p.group : 1) * (D / 8); e += 32) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(q + e * 8);
+            const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                qa += fabsf(bf16_low_half(v[i])) + fabsf(bf16_high_half(v[i]));
         }
         qa = warp_sum(qa);
         const float e = (qa * __uint_as_float(kmax)) * (float(16 + p.group) * 5.9604645e-8f) + 1e-36f;
@@ -368,46 +494,49 @@ __device__ __forceinline__ void select_blocks(const DecodeArgs &a, const Plan &p
             lo = key_of(tv - 2.f * e);
             hi = key_of(tv + 2.f * e);
         }
-        int cnt = 0, ndef = 0;
-        for (int i0 = 0; i0 < n; i0 += 32) {
-            const uint32_t x = i0 + lane < n ? sc[row * p.nloc + i0 + lane] : 0u;
-            const bool in = i0 + lane < n && x >= lo, sure = i0 + lane < n && x > hi;
-            const uint32_t b = __ballot_sync(kFull, in), d = __ballot_sync(kFull, sure);
-            const int at = cnt + __popc(b & ((1u << lane) - 1));
-            const int dt = ndef + __popc(d & ((1u << lane) - 1));
-            if (in && at < kMaxK) f.sel[row][at] = b0 + i0 + lane;
-            if (sure && dt < kMaxK) f.def[row][dt] = b0 + i0 + lane;
-            cnt += __popc(b);
-            ndef += __popc(d);
-        }
+        // the blocks at or above t - 2e, if the lists hold them all
+        int total = 0;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c)
+            if (c < C) {
+                const bool in = key[c] >= lo && key[c] != 0u;
+                const uint32_t b = __ballot_sync(kFull, in);
+                const int at = total + __popc(b & ((1u << lane) - 1));
+                if (in && at < kMaxK) f.fin[row][at] = lists[c * p.score_rows + row].id[lane];
+                total += __popc(b);
+            }
+        const bool slow = total != kk || __any_sync(kFull, next >= lo && next != 0u);
+        __syncwarp();
+        // ascending ids
+        const int mine = lane < kk ? f.fin[row][lane] : 0x7fffffff;
+        int before = 0;
+#pragma unroll 8
+        for (int j = 0; j < kk; ++j) before += __shfl_sync(kFull, mine, j) < mine;
+        __syncwarp();
+        if (lane < kk && !slow) f.fin[row][before] = mine;
         if (lane == 0) {
-            f.nsel[row] = cnt;
-            f.ndef[row] = ndef;
+            f.slow[row] = slow;
             f.lo[row] = lo;
             f.hi[row] = hi;
-        }
-    }
-    cluster.sync();
-    for (int row = warp; row < srows; row += kWarps) {
-        int total = 0;
-        for (int c = 0; c < C; ++c) {
-            const Fixed *peer = cluster.map_shared_rank(&f, c);
-            const int m = peer->nsel[row];
-            if (lane < m && total + lane < kMaxK) f.fin[row][total + lane] = peer->sel[row][lane];
-            total += m;
-        }
-        if (lane == 0) {
-            f.slow[row] = total != kk;
-            if (total != kk) atomicOr(&f.any_slow, 1);
+            if (slow) atomicOr(&f.any_slow, 1);
         }
     }
     __syncthreads();
-    // the counts are the same to every CTA of the cluster, and so is this
+    // made from the same lists in every CTA of the cluster, so this is the
+    // same everywhere
     if (f.any_slow == 0) return;
-    for (int row = warp; row < srows; row += kWarps) {
+    for (int row = warp; row < srows; row += W) {
         if (!f.slow[row]) continue;
-        int need = kk;
-        for (int c = 0; c < C; ++c) need -= cluster.map_shared_rank(&f, c)->ndef[row];
+        const uint32_t lo = f.lo[row], hi = f.hi[row];
+        int ndef = 0;
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const bool sure = i0 + lane < n && sc[row * p.nloc + i0 + lane] > hi;
+            const uint32_t d = __ballot_sync(kFull, sure);
+            const int at = ndef + __popc(d & ((1u << lane) - 1));
+            if (sure && at < kMaxK) f.def[row][at] = b0 + i0 + lane;
+            ndef += __popc(d);
+        }
+        if (lane == 0) f.ndef[row] = ndef;
         double q[D / 32];
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) q[e] = 0.0;
@@ -422,7 +551,6 @@ __device__ __forceinline__ void select_blocks(const DecodeArgs &a, const Plan &p
         // an equal score goes behind those that are there
         double best = 0.0;
         int id = 0, held = 0;
-        const uint32_t lo = f.lo[row], hi = f.hi[row];
         for (int i0 = 0; i0 < n; i0 += 32) {
             const uint32_t x = i0 + lane < n ? sc[row * p.nloc + i0 + lane] : 0u;
             uint32_t open = __ballot_sync(kFull, i0 + lane < n && x >= lo && !(x > hi));
@@ -431,7 +559,7 @@ __device__ __forceinline__ void select_blocks(const DecodeArgs &a, const Plan &p
                 open &= open - 1;
                 const double s = score_fp64<D>(a, w, b, q, lane);
                 const int at = __popc(__ballot_sync(kFull, lane < held && best >= s));
-                if (at < need) {
+                if (at < kk) {
                     const double bu = __shfl_up_sync(kFull, best, 1);
                     const int iu = __shfl_up_sync(kFull, id, 1);
                     if (lane > at) {
@@ -441,7 +569,7 @@ __device__ __forceinline__ void select_blocks(const DecodeArgs &a, const Plan &p
                         best = s;
                         id = b;
                     }
-                    held = min(held + 1, need);
+                    held = min(held + 1, kk);
                 }
             }
         }
@@ -450,7 +578,7 @@ __device__ __forceinline__ void select_blocks(const DecodeArgs &a, const Plan &p
         if (lane == 0) f.nd[row] = held;
     }
     cluster.sync();
-    for (int row = warp; row < srows; row += kWarps) {
+    for (int row = warp; row < srows; row += W) {
         if (!f.slow[row]) continue;
         int have = 0;
         for (int c = 0; c < C; ++c) {
@@ -497,26 +625,33 @@ __device__ __forceinline__ void select_blocks(const DecodeArgs &a, const Plan &p
 }
 
 // The union of the rows' lists: items (ascending ids), their pages and the
-// rows that selected each.
+// rows that selected each.  f.bits and f.masks are zero.
+template <int W>
 __device__ __forceinline__ void make_items(const DecodeArgs &a, const Plan &p, const Job &w,
                                            Fixed &f) {
+    constexpr int kThreads = W * 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool all = w.ne <= w.kk;                       // every block is selected
     const int sel = all ? w.ne : w.kk;
     const int cnt = sel + (w.own >= 0 ? 1 : 0);
     const uint32_t every = (1u << w.rows) - 1;
+    const auto put = [&](int at, int id) {
+        int pid = w.table[id];
+        if (pid < 0 || pid >= a.c.num_pages) {
+            report_status(a.status, kStatusBadIndex);
+            pid = -1;
+        }
+        f.items[at] = uint16_t(id);
+        f.pages[at] = pid;
+    };
     if (all || a.share || w.rows == 1) {
         for (int i = tid; i < cnt; i += kThreads) {
-            f.items[i] = i == sel ? w.own : all ? i : f.fin[0][i];
+            put(i, i == sel ? w.own : all ? i : f.fin[0][i]);
             f.masks[i] = every;
         }
         if (tid == 0) f.n_items = cnt;
-        __syncthreads();
     } else {
         const int words = (w.nb + 31) / 32;
-        for (int i = tid; i < words; i += kThreads) f.bits[i] = 0u;
-        for (int i = tid; i < kMaxItems; i += kThreads) f.masks[i] = 0u;
-        __syncthreads();
         for (int i = tid; i < w.rows * cnt; i += kThreads) {
             const int r = i / cnt, j = i - r * cnt;
             const int id = j == sel ? w.own : f.fin[r][j];
@@ -529,6 +664,7 @@ __device__ __forceinline__ void make_items(const DecodeArgs &a, const Plan &p, c
             int sum = 0;
             for (int i = w0; i < w1; ++i) sum += __popc(f.bits[i]);
             int run = sum;
+#pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(kFull, run, o);
                 if (lane >= o) run += y;
@@ -545,18 +681,9 @@ __device__ __forceinline__ void make_items(const DecodeArgs &a, const Plan &p, c
             const int r = i / cnt, j = i - r * cnt;
             const int id = j == sel ? w.own : f.fin[r][j];
             const int at = int(f.pref[id >> 5]) + __popc(f.bits[id >> 5] & ((1u << (id & 31)) - 1));
-            f.items[at] = id;
-            atomicOr(&f.masks[at], 1u << r);
+            // the first row to come looks the page up
+            if (atomicOr(&f.masks[at], 1u << r) == 0u) put(at, id);
         }
-        __syncthreads();
-    }
-    for (int i = tid; i < f.n_items; i += kThreads) {
-        int pid = w.table[f.items[i]];
-        if (pid < 0 || pid >= a.c.num_pages) {
-            report_status(a.status, kStatusBadIndex);
-            pid = -1;
-        }
-        f.pages[i] = pid;
     }
     if (a.idx != nullptr && w.rank == 0 && (!a.share || w.part == 0)) {
         const int srows = a.share ? 1 : w.rows;
@@ -571,12 +698,14 @@ __device__ __forceinline__ void make_items(const DecodeArgs &a, const Plan &p, c
     __syncthreads();
 }
 
-// Stage 3 and the merge.
-template <int D, int NT>
+// Stage 3 and the merge.  `part` is where the cluster leaves this CTA's share
+// of the outputs, [CTA][rows * D / C].
+template <int D, int NT, int W>
 __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const Job &w, Fixed &f,
-                                       float *po) {
+                                       float *part, float *po) {
     cg::cluster_group cluster = cg::this_cluster();
-    constexpr int PS = D + 1;           // row stride of the partial outputs
+    constexpr int kThreads = W * 32;
+    constexpr int PS = D + 1;           // row stride of the warps' outputs
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n8 = lane >> 2, kq = lane & 3;
     uint4 q[NT][D / 32];
@@ -602,22 +731,34 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
     }
     const int tpp = a.c.page / 16;      // 16-key tiles of a page, a power of two
     const int shift = 31 - __clz(tpp);
-    const int units = f.n_items << shift;
-    for (int unit = w.rank * kWarps + warp; unit < units; unit += p.cluster * kWarps) {
-        const int item = unit >> shift, tile = unit & (tpp - 1);
-        const int64_t pid = f.pages[item];
-        const int64_t key0 = int64_t(f.items[item]) * a.c.page + tile * 16;
-        const int valid = int(i64min(16, w.len - key0));
-        if (pid < 0 || valid <= 0) continue;
-        const int64_t row0 = (pid * a.c.heads + w.head) * a.c.page + tile * 16;
-        uint4 kr[2][D / 32], vr[4][D / 64];
+    const int units = f.n_items << shift, step = p.cluster * W;
+    uint4 kr[2][D / 32], vr[4][D / 64];
+    // the next unit from u on that has keys: its first row in the cache
+    int64_t row0 = 0;
+    int valid = 0, item = 0;
+    const auto find = [&](int u) {
+        for (; u < units; u += step) {
+            item = u >> shift;
+            const int tile = u & (tpp - 1);
+            const int64_t pid = f.pages[item];
+            const int64_t left = w.len - (int64_t(f.items[item]) * a.c.page + tile * 16);
+            if (pid < 0 || left <= 0) continue;
+            valid = int(i64min(16, left));
+            row0 = (pid * a.c.heads + w.head) * a.c.page + tile * 16;
+            return u;
+        }
+        return units;
+    };
+    const auto load_k = [&] {
         const uint16_t *kp = a.c.k + (row0 + n8) * D + kq * 8;
-        const uint16_t *vp = a.c.v + (row0 + 2 * kq) * D + n8 * 8;
 #pragma unroll
         for (int g = 0; g < D / 32; ++g) {
             kr[0][g] = __ldg(reinterpret_cast<const uint4 *>(kp + g * 32));
             kr[1][g] = __ldg(reinterpret_cast<const uint4 *>(kp + 8 * D + g * 32));
         }
+    };
+    const auto load_v = [&](int64_t row) {
+        const uint16_t *vp = a.c.v + (row + 2 * kq) * D + n8 * 8;
 #pragma unroll
         for (int g = 0; g < D / 64; ++g) {
             vr[0][g] = __ldg(reinterpret_cast<const uint4 *>(vp + g * 64));
@@ -625,6 +766,15 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
             vr[2][g] = __ldg(reinterpret_cast<const uint4 *>(vp + 8 * D + g * 64));
             vr[3][g] = __ldg(reinterpret_cast<const uint4 *>(vp + 9 * D + g * 64));
         }
+    };
+    int unit = find(w.rank * W + warp);
+    if (unit < units) {
+        load_k();
+        load_v(row0);
+    }
+    while (unit < units) {
+        const int now_valid = valid;
+        const uint32_t mask = f.masks[item];
         float s[NT][4];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -635,16 +785,8 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
                 mma_bf16(s[t], kr[0][g].z, kr[1][g].z, kr[0][g].w, kr[1][g].w, q[t][g].z, q[t][g].w);
             }
         }
-        if (valid < 16) {
-            // rows past the end hold anything: 0 * NaN must not reach O
-            const int rows[4] = {2 * kq, 2 * kq + 1, 2 * kq + 8, 2 * kq + 9};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (rows[i] >= valid)
-#pragma unroll
-                    for (int g = 0; g < D / 64; ++g) vr[i][g] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        const uint32_t mask = f.masks[item];
+        unit = find(unit + step);
+        if (unit < units) load_k();     // in flight during the softmax and P V
         uint32_t b0[NT], b1[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -654,8 +796,8 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
             for (int e = 0; e < 2; ++e) {
                 const bool in = (mask >> (t * 8 + 2 * kq + e)) & 1u;
                 // s[e]: key n8, s[2 + e]: key n8 + 8
-                s[t][e] = in && n8 < valid ? s[t][e] * a.scale_log2 : kNegInf;
-                s[t][2 + e] = in && n8 + 8 < valid ? s[t][2 + e] * a.scale_log2 : kNegInf;
+                s[t][e] = in && n8 < now_valid ? s[t][e] * a.scale_log2 : kNegInf;
+                s[t][2 + e] = in && n8 + 8 < now_valid ? s[t][2 + e] * a.scale_log2 : kNegInf;
                 float x = fmaxf(s[t][e], s[t][2 + e]);
                 x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
                 x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
@@ -663,10 +805,10 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
                 const float mn = fmaxf(m[t][e], x);
                 const float base = mn == kNegInf ? 0.f : mn;     // nothing admitted yet
                 moved |= mn != m[t][e];
-                corr[e] = exp2f(m[t][e] - base);
+                corr[e] = exp2_fast(m[t][e] - base);
                 m[t][e] = mn;
-                s[t][e] = exp2f(s[t][e] - base);
-                s[t][2 + e] = exp2f(s[t][2 + e] - base);
+                s[t][e] = exp2_fast(s[t][e] - base);
+                s[t][2 + e] = exp2_fast(s[t][2 + e] - base);
                 l[t][e] = l[t][e] * corr[e] + (s[t][e] + s[t][2 + e]);
             }
             if (__any_sync(kFull, moved)) {
@@ -683,6 +825,15 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
             b0[t] = transpose_8x8(pack_bf16x2(s[t][0], s[t][1]));
             b1[t] = transpose_8x8(pack_bf16x2(s[t][2], s[t][3]));
         }
+        if (now_valid < 16) {
+            // rows past the end hold anything: 0 * NaN must not reach O
+            const int rows[4] = {2 * kq, 2 * kq + 1, 2 * kq + 8, 2 * kq + 9};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (rows[i] >= now_valid)
+#pragma unroll
+                    for (int g = 0; g < D / 64; ++g) vr[i][g] = make_uint4(0u, 0u, 0u, 0u);
+        }
 #pragma unroll
         for (int g = 0; g < D / 64; ++g)
 #pragma unroll
@@ -694,6 +845,7 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
 #pragma unroll
                 for (int t = 0; t < NT; ++t) mma_bf16(o[t][g * 4 + j], a0, a1, a2, a3, b0[t], b1[t]);
             }
+        if (unit < units) load_v(row0);
     }
     // merge the warps' states
 #pragma unroll
@@ -719,54 +871,76 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
             }
         }
     __syncthreads();
-    for (int i = tid; i < w.rows * D; i += kThreads) {
+    uint16_t *out = a.out + (int64_t(w.token) * a.q_heads + w.head * p.group + w.row0) * D;
+    const int C = p.cluster, share = w.rows * D / C;     // C divides D
+    for (int i = 2 * tid; i < w.rows * D; i += 2 * kThreads) {
         const int r = i / D, c = i % D;
         float mx = kNegInf;
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) mx = fmaxf(mx, f.wm[k][r]);
-        const float base = mx == kNegInf ? 0.f : mx;
-        float acc = 0.f, ls = 0.f;
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-            const float x = exp2f(f.wm[k][r] - base);
-            acc = fmaf(x, po[(k * p.rows + r) * PS + c], acc);
-            ls = fmaf(x, f.wl[k][r], ls);
-        }
-        po[r * PS + c] = acc;           // read by this thread alone until now
-        if (c == 0) {
-            f.pm[r] = mx;
-            f.pl[r] = ls;
-        }
-    }
-    cluster.sync();
-    uint16_t *out = a.out + (int64_t(w.token) * a.q_heads + w.head * p.group + w.row0) * D;
-    for (int i = w.rank * kThreads + tid; i < w.rows * D / 2; i += p.cluster * kThreads) {
-        const int r = i / (D / 2), c = i % (D / 2) * 2;
-        float mx = kNegInf;
-        for (int k = 0; k < p.cluster; ++k)
-            mx = fmaxf(mx, cluster.map_shared_rank(&f, k)->pm[r]);
+        for (int k = 0; k < W; ++k) mx = fmaxf(mx, f.wm[k][r]);
         const float base = mx == kNegInf ? 0.f : mx;
         float x0 = 0.f, x1 = 0.f, ls = 0.f;
-        for (int k = 0; k < p.cluster; ++k) {
-            const Fixed *peer = cluster.map_shared_rank(&f, k);
-            const float *pp = cluster.map_shared_rank(po, k) + r * PS + c;
-            const float x = exp2f(peer->pm[r] - base);
-            x0 = fmaf(x, pp[0], x0);
-            x1 = fmaf(x, pp[1], x1);
-            ls = fmaf(x, peer->pl[r], ls);
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            const float x = exp2_fast(f.wm[k][r] - base);
+            x0 = fmaf(x, po[(k * p.rows + r) * PS + c], x0);
+            x1 = fmaf(x, po[(k * p.rows + r) * PS + c + 1], x1);
+            ls = fmaf(x, f.wl[k][r], ls);
         }
-        const float inv = ls > 0.f || ls != ls ? __fdiv_rn(1.f, ls) : 0.f;
-        *reinterpret_cast<uint32_t *>(out + r * D + c) = pack_bf16x2(x0 * inv, x1 * inv);
+        if (C == 1) {
+            const float inv = ls > 0.f || ls != ls ? __fdiv_rn(1.f, ls) : 0.f;
+            *reinterpret_cast<uint32_t *>(out + i) = pack_bf16x2(x0 * inv, x1 * inv);
+        } else {
+            *reinterpret_cast<float2 *>(cluster.map_shared_rank(part, i / share) + w.rank * share +
+                                        i % share) = make_float2(x0, x1);
+            if (c < 2 * C) {            // one thread of the row for each CTA
+                Fixed *peer = cluster.map_shared_rank(&f, c / 2);
+                peer->pm[w.rank][r] = mx;
+                peer->pl[w.rank][r] = ls;
+            }
+        }
     }
-    cluster.sync();                     // the peers' shared memory is read until here
+    if (C == 1) return;
+    cluster.sync();
+    for (int j = 2 * tid; j < share; j += 2 * kThreads) {
+        const int i = w.rank * share + j, r = i / D;
+        float mx = kNegInf;
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k)
+            if (k < C) mx = fmaxf(mx, f.pm[k][r]);
+        const float base = mx == kNegInf ? 0.f : mx;
+        float x0 = 0.f, x1 = 0.f, ls = 0.f;
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k)
+            if (k < C) {
+                const float2 y = *reinterpret_cast<const float2 *>(part + k * share + j);
+                const float x = exp2_fast(f.pm[k][r] - base);
+                x0 = fmaf(x, y.x, x0);
+                x1 = fmaf(x, y.y, x1);
+                ls = fmaf(x, f.pl[k][r], ls);
+            }
+        const float inv = ls > 0.f || ls != ls ? __fdiv_rn(1.f, ls) : 0.f;
+        *reinterpret_cast<uint32_t *>(out + i) = pack_bf16x2(x0 * inv, x1 * inv);
+    }
 }
 
-template <int D, int RP, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kernel(DecodeArgs a, Plan p) {
+// CTAs per SM: three of four warps or one of twelve (eight with 16 rows,
+// whose accumulators take twice the registers).
+constexpr int kWarpsSmall = 4;
+constexpr int warps_large(int nt) { return nt == 1 ? 12 : 8; }
+
+template <int D, int RP, int NT, int W>
+__global__ void __launch_bounds__(W * 32, W == kWarpsSmall ? (NT == 1 ? 3 : 2) : 1)
+    decode_kernel(DecodeArgs a, Plan p) {
     extern __shared__ __align__(16) char smem[];
+    constexpr int kThreads = W * 32;
     Fixed &f = *reinterpret_cast<Fixed *>(smem);
-    uint32_t *gath = reinterpret_cast<uint32_t *>(smem + p.gath_off);
+    List *lists = reinterpret_cast<List *>(smem + p.list_off);
+    float *part = reinterpret_cast<float *>(smem + p.part_off);
     uint32_t *sc = reinterpret_cast<uint32_t *>(smem + p.main_off);
+    cg::cluster_group cluster = cg::this_cluster();
+    // peers may write to this CTA once all of the cluster have come this far
+    auto arrived = cluster.barrier_arrive();
     const int tid = threadIdx.x;
     Job w;
     w.rank = int(blockIdx.x % unsigned(p.cluster));
@@ -780,6 +954,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kernel(Decod
     w.rows = min(p.rows, p.group - w.row0);
     const int64_t seq = a.token_seq != nullptr ? a.token_seq[w.token] : w.token;
     w.len = a.lens[w.token];
+    for (int i = tid; i < kDecodeMaxWidth / 32; i += kThreads) f.bits[i] = 0u;
+    for (int i = tid; i < kMaxItems; i += kThreads) f.masks[i] = 0u;
+    if (tid == 0) {
+        f.kmax = 0u;
+        f.any_slow = 0;
+    }
     if (seq < 0 || seq >= a.seqs) {
         if (tid == 0) report_status(a.status, kStatusBadIndex);
         w.len = 0;
@@ -791,6 +971,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kernel(Decod
     }
     w.nb = int((w.len + a.c.page - 1) / a.c.page);
     if (w.nb == 0) {                    // the same for the whole cluster
+        cluster.barrier_wait(std::move(arrived));
         if (w.rank != 0) return;
         uint16_t *out = a.out + (int64_t(w.token) * a.q_heads + w.head * p.group + w.row0) * D;
         for (int i = tid; i < w.rows * D; i += kThreads) out[i] = 0;
@@ -807,30 +988,30 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) decode_kernel(Decod
     w.ne = w.nb - (a.local ? 1 : 0);
     w.kk = a.topk - (a.local ? 1 : 0);
     if (w.ne > w.kk && w.kk > 0) {
-        if (tid == 0) {
-            f.kmax = 0u;
-            f.any_slow = 0;
-        }
         __syncthreads();
         const int each = (w.ne + p.cluster - 1) / p.cluster;
         const int b0 = min(w.ne, w.rank * each), n = min(w.ne, b0 + each) - b0;
-        score_blocks<D, RP>(a, p, w, f, sc, b0, n);
+        score_blocks<D, RP, W>(a, p, w, f, sc, b0, n);
         __syncthreads();
-        select_blocks<D>(a, p, w, f, sc, gath, b0, n);
+        cluster.barrier_wait(std::move(arrived));
+        select_blocks<D, W>(a, p, w, f, sc, lists, b0, n);
+    } else {
+        cluster.barrier_wait(std::move(arrived));
+        __syncthreads();
     }
-    make_items(a, p, w, f);
-    attend<D, NT>(a, p, w, f, reinterpret_cast<float *>(sc));
+    make_items<W>(a, p, w, f);
+    attend<D, NT, W>(a, p, w, f, part, reinterpret_cast<float *>(sc));
 }
 
-template <int D, int RP, int NT>
+template <int D, int RP, int NT, int W>
 cudaError_t launch(const DecodeArgs &a, const Plan &p, size_t smem, int64_t items, cudaStream_t st) {
-    auto kernel = decode_kernel<D, RP, NT>;
+    auto kernel = decode_kernel<D, RP, NT, W>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          int(smem));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(items * p.cluster));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(W * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -842,17 +1023,24 @@ cudaError_t launch(const DecodeArgs &a, const Plan &p, size_t smem, int64_t item
     return cudaLaunchKernelEx(&cfg, kernel, a, p);
 }
 
+template <int D, int RP, int NT>
+cudaError_t pick(const DecodeArgs &a, const Plan &p, bool large, size_t smem, int64_t items,
+                 cudaStream_t st) {
+    if (large) return launch<D, RP, NT, warps_large(NT)>(a, p, smem, items, st);
+    return launch<D, RP, NT, kWarpsSmall>(a, p, smem, items, st);
+}
+
 template <int D>
-cudaError_t dispatch(const DecodeArgs &a, const Plan &p, size_t smem, int64_t items,
+cudaError_t dispatch(const DecodeArgs &a, const Plan &p, bool large, size_t smem, int64_t items,
                      cudaStream_t st) {
     if (p.score_rows == 1) {
-        if (p.rows > 8) return launch<D, 1, 2>(a, p, smem, items, st);
-        return launch<D, 1, 1>(a, p, smem, items, st);
+        if (p.rows > 8) return pick<D, 1, 2>(a, p, large, smem, items, st);
+        return pick<D, 1, 1>(a, p, large, smem, items, st);
     }
-    if (p.rows <= 2) return launch<D, 2, 1>(a, p, smem, items, st);
-    if (p.rows <= 4) return launch<D, 4, 1>(a, p, smem, items, st);
-    if (p.rows <= 8) return launch<D, 8, 1>(a, p, smem, items, st);
-    return launch<D, 16, 2>(a, p, smem, items, st);
+    if (p.rows <= 2) return pick<D, 2, 1>(a, p, large, smem, items, st);
+    if (p.rows <= 4) return pick<D, 4, 1>(a, p, large, smem, items, st);
+    if (p.rows <= 8) return pick<D, 8, 1>(a, p, large, smem, items, st);
+    return pick<D, 16, 2>(a, p, large, smem, items, st);
 }
 
 }  // namespace
@@ -863,25 +1051,32 @@ cudaError_t launch_paged_decode(const DecodeArgs &a, cudaStream_t st) {
     p.parts = (p.group + kMaxRows - 1) / kMaxRows;
     p.rows = (p.group + p.parts - 1) / p.parts;
     p.score_rows = a.share ? 1 : p.rows;
-    p.segs = p.score_rows >= kWarps ? 1 : kWarps / p.score_rows;
     const int64_t items = a.tokens * a.c.heads * p.parts;
-    // CTAs per cluster: enough to cover the card twice, and to hold the
-    // sequence's scores
+    // Few items: large CTAs, clusters of up to eight of them.  Many: small
+    // CTAs, three to an SM, so that some load while others select.
+    const bool large = items * kMaxCluster < 3 * 152;
+    const int64_t want = large ? 152 : 3 * 152;
     p.cluster = 1;
-    while (p.cluster < 8 &&
-           (items * p.cluster < 2 * 152 || (a.width + p.cluster - 1) / p.cluster > kMaxLocal))
+    while (p.cluster < kMaxCluster &&
+           (items * p.cluster < want || (a.width + p.cluster - 1) / p.cluster > kMaxLocal))
         p.cluster *= 2;
     if (items * p.cluster > 0x7fffffff) return cudaErrorInvalidConfiguration;
     p.nloc = (a.width + p.cluster - 1) / p.cluster;
+    const int warps = large ? warps_large(p.rows > 8 ? 2 : 1) : kWarpsSmall;
+    p.segs = p.score_rows >= warps ? 1 : warps / p.score_rows;
+    if (p.segs > 8) p.segs = 8;
     const auto up = [](size_t x) { return (x + 15) / 16 * 16; };
     size_t off = up(sizeof(Fixed));
-    p.gath_off = int32_t(off);
-    off = up(off + size_t(p.cluster) * p.score_rows * p.segs * kMaxK * 4);
+    p.list_off = int32_t(off);
+    off = up(off + size_t(p.cluster) * p.score_rows * sizeof(List));
+    p.part_off = int32_t(off);
+    if (p.cluster > 1) off = up(off + size_t(p.rows) * a.c.d * 4);
     p.main_off = int32_t(off);
     const size_t scores = size_t(p.score_rows) * p.nloc * 4;
-    const size_t merge = size_t(kWarps) * p.rows * (a.c.d + 1) * 4;
+    const size_t merge = size_t(warps) * p.rows * (a.c.d + 1) * 4;
     const size_t smem = off + up(scores > merge ? scores : merge);
-    return a.c.d == 64 ? dispatch<64>(a, p, smem, items, st) : dispatch<128>(a, p, smem, items, st);
+    return a.c.d == 64 ? dispatch<64>(a, p, large, smem, items, st)
+                       : dispatch<128>(a, p, large, smem, items, st);
 }
 
 }  // namespace bsa
