@@ -492,48 +492,53 @@ class Rope:
         self.rotation = Rotation(self.table.data_ptr(), rot, int(interleaved), attention_factor)
 
 
-def _one_device(*tensors):
-    """All on one CUDA device, and that the current one: pointers of another
-    device would be launched on this one's stream."""
+def _here(*tensors) -> int:
+    """The current device's stream, all tensors being on that device: pointers
+    of another one would be launched on this one's stream."""
     torch = _torch()
-    here = torch.cuda.current_device() if any(t is not None and t.is_cuda for t in tensors) else None
+    here = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != here):
+        if t is not None and t.get_device() != here:
             raise ValueError("tensors must be on the current CUDA device")
+    return torch._C._cuda_getCurrentRawStream(here)
 
 
 def _i32(t, name: str, shape):
-    torch = _torch()
-    if t.dtype != torch.int32 or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+    if t.dtype != _torch().int32 or t.shape != shape or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous int32 tensor {list(shape)}")
-    return t
+    return t.data_ptr()
 
 
 def _rope(fn, x, rope: Rope, positions, out):
     torch = _torch()
-    if x.dim() not in (3, 4) or x.stride(-1) != 1:
+    dims = x.dim()
+    if dims not in (3, 4) or x.stride(-1) != 1:
         raise ValueError("x must be [batch, heads, n, d] or [heads, n, d] with contiguous channels")
-    if x.dtype not in (torch.bfloat16, torch.float32):
+    if x.dtype == torch.bfloat16:
+        dt = BF16
+    elif x.dtype == torch.float32:
+        dt = FP32
+    else:
         raise TypeError(f"unsupported dtype {x.dtype}")
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     elif out.shape != x.shape or out.dtype != x.dtype or out.stride(-1) != 1:
         raise ValueError("out must have x's shape and dtype and contiguous channels")
-    batch = x.shape[0] if x.dim() == 4 else 1
+    batch = x.shape[0] if dims == 4 else 1
     heads, n, d = x.shape[-3:]
-    first = 0
     if isinstance(positions, torch.Tensor):
-        shape = (batch, n) if positions.dim() == 2 else (n,)
         if positions.dim() == 1 and batch != 1:
             raise TypeError("positions must be [batch, n]")
-        _i32(positions, "positions", shape)
-        _one_device(x, out, rope.table, positions)
+        first, pos = 0, _i32(positions, "positions", (batch, n) if positions.dim() == 2 else (n,))
+        stream = _here(x, out, rope.table, positions)
     else:
-        first, positions = int(positions), None
-        _one_device(x, out, rope.table)
-    s = Heads(batch, n, heads, d, BF16 if x.dtype == torch.bfloat16 else FP32)
-    st = [Strides(t.stride(0) if t.dim() == 4 else 0, t.stride(-3), t.stride(-2)) for t in (x, out)]
-    _check(fn(s, _ptr(x), st[0], _ptr(positions), first, rope.rotation, _ptr(out), st[1], _stream()))
+        first, pos = int(positions), None
+        stream = _here(x, out, rope.table)
+    xs, os_ = x.stride(), out.stride()
+    if dims == 3:
+        xs, os_ = (0, *xs), (0, *os_)
+    _check(fn(Heads(batch, n, heads, d, dt), x.data_ptr(), Strides(*xs[:3]), pos, first,
+              rope.rotation, out.data_ptr(), Strides(*os_[:3]), stream))
     return out
 
 
@@ -563,7 +568,7 @@ class PagedCache:
         if kbar.dtype != torch.float32 or not kbar.is_contiguous() \
                 or tuple(kbar.shape) != (k.shape[0], k.shape[1], k.shape[3]):
             raise ValueError("kbar must be contiguous float32 [pages, heads, d]")
-        _one_device(k, v, kbar)
+        _here(k, v, kbar)
         self.k, self.v, self.kbar = k, v, kbar
         self.num_pages, self.heads, self.page, self.d = k.shape
         self.struct = Cache(k.data_ptr(), v.data_ptr(), kbar.data_ptr(), self.num_pages,
@@ -577,9 +582,9 @@ class PagedCache:
         return cls(k, v, torch.zeros((num_pages, heads, d), dtype=torch.float32, device=device))
 
 
-def _token_rows(t, name: str, heads: int, d: int):
-    torch = _torch()
-    if t.dim() != 3 or t.dtype != torch.bfloat16 or t.shape[1:] != (heads, d) \
+def _token_rows(t, name: str, heads: int, d: int) -> int:
+    """The stride from a token's rows to the next's."""
+    if t.dim() != 3 or t.dtype != _torch().bfloat16 or t.shape[1] != heads or t.shape[2] != d \
             or t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
         raise ValueError(f"{name} must be bfloat16 [tokens, {heads}, {d}] with contiguous rows")
     return t.stride(0) if t.shape[0] > 1 else heads * d
@@ -591,16 +596,15 @@ def cache_append(cache: PagedCache, k, v, table, start, *, cu_tokens=None):
     width], ``start`` int32 [seqs] (lengths before); ``cu_tokens`` int32
     [seqs + 1], None: as many tokens for each.  See bsa_cache_append."""
     seqs, width = table.shape
-    ks, vs = (_token_rows(t, n, cache.heads, cache.d) for t, n in ((k, "k"), (v, "v")))
+    ks = _token_rows(k, "k", cache.heads, cache.d)
+    vs = _token_rows(v, "v", cache.heads, cache.d)
     if k.shape != v.shape:
         raise ValueError("k and v must have one shape")
-    _i32(table, "table", (seqs, width))
-    _i32(start, "start", (seqs,))
-    if cu_tokens is not None:
-        _i32(cu_tokens, "cu_tokens", (seqs + 1,))
-    _one_device(cache.k, k, v, table, start, cu_tokens)
-    _check(lib().bsa_cache_append(cache.struct, _ptr(k), ks, _ptr(v), vs, k.shape[0], seqs,
-                                  _ptr(cu_tokens), _ptr(start), _ptr(table), width, _stream()))
+    cu = None if cu_tokens is None else _i32(cu_tokens, "cu_tokens", (seqs + 1,))
+    _check(lib().bsa_cache_append(
+        cache.struct, k.data_ptr(), ks, v.data_ptr(), vs, k.shape[0], seqs, cu,
+        _i32(start, "start", (seqs,)), _i32(table, "table", (seqs, width)), width,
+        _here(cache.k, k, v, table, start, cu_tokens)))
 
 
 def copy_pages(cache: PagedCache, pairs):
@@ -609,9 +613,9 @@ def copy_pages(cache: PagedCache, pairs):
     torch = _torch()
     if not isinstance(pairs, torch.Tensor):
         pairs = torch.from_numpy(np.ascontiguousarray(pairs, dtype=np.int32)).to(cache.k.device)
-    _i32(pairs, "pairs", (pairs.shape[0], 2))
-    _one_device(cache.k, pairs)
-    _check(lib().bsa_cache_copy_pages(cache.struct, _ptr(pairs), pairs.shape[0], _stream()))
+    count = pairs.shape[0]
+    _check(lib().bsa_cache_copy_pages(cache.struct, _i32(pairs, "pairs", (count, 2)), count,
+                                      _here(cache.k, pairs)))
 
 
 def paged_decode(cache: PagedCache, q, table, lens, topk: int, *, token_seq=None,
@@ -625,22 +629,18 @@ def paged_decode(cache: PagedCache, q, table, lens, topk: int, *, token_seq=None
     seqs, width = table.shape
     tokens, q_heads = q.shape[0], q.shape[1]
     qs = _token_rows(q, "q", q_heads, cache.d)
-    _i32(table, "table", (seqs, width))
-    _i32(lens, "lens", (tokens,))
-    if token_seq is not None:
-        _i32(token_seq, "token_seq", (tokens,))
+    seq = None if token_seq is None else _i32(token_seq, "token_seq", (tokens,))
     if out is None:
         out = torch.empty((tokens, q_heads, cache.d), dtype=q.dtype, device=q.device)
-    elif out.dtype != q.dtype or not out.is_contiguous() \
-            or tuple(out.shape) != (tokens, q_heads, cache.d):
+    elif out.dtype != q.dtype or out.shape != (tokens, q_heads, cache.d) or not out.is_contiguous():
         raise ValueError("out must be contiguous bfloat16 [tokens, q_heads, d]")
-    _one_device(cache.k, q, table, lens, token_seq, out)
     idx = torch.empty((tokens, cache.heads if share_group else q_heads, topk), dtype=torch.int32,
                       device=q.device)
-    opts = DecodeOptions(int(local_block), int(share_group))
-    _check(lib().bsa_paged_decode(cache.struct, _ptr(q), qs, tokens, q_heads, _ptr(table), width,
-                                  seqs, _ptr(token_seq), _ptr(lens), topk, ctypes.byref(opts),
-                                  float(scale), _ptr(out), _ptr(idx), _stream()))
+    _check(lib().bsa_paged_decode(
+        cache.struct, q.data_ptr(), qs, tokens, q_heads, _i32(table, "table", (seqs, width)), width,
+        seqs, seq, _i32(lens, "lens", (tokens,)), topk,
+        ctypes.byref(DecodeOptions(int(local_block), int(share_group))), scale, out.data_ptr(),
+        idx.data_ptr(), _here(cache.k, q, table, lens, token_seq, out)))
     return out, idx
 
 

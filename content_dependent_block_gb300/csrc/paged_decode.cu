@@ -11,9 +11,11 @@
 //               group; fp32 dot products, reduced over the lanes by an
 //               exchange that halves the number of values at each step.
 //               The scores stay in shared memory as order-preserving keys.
-//   2. top-k    a warp sorts its share's best 32 (key, id) and each CTA gives
-//               its list to the whole cluster (distributed shared memory), so
-//               that every CTA merges all lists and knows t, the k-th best.
+//   2. top-k    each row's scores gather in the shared memory of one CTA of the
+//               cluster, whose warps find t, the k-th best, with a histogram
+//               between the smallest and the largest score (256 equal
+//               intervals, so that about one of the scores near t falls into
+//               each) and hand the selection back to the cluster.
 //               A score is off its true value by at most e (a bound from the
 //               sums of |q| and the largest |mean|), so blocks above t + 2e
 //               are selected for certain and blocks below t - 2e are not.
@@ -36,10 +38,12 @@
 // tile (128 rows), and the keys arrive at about 23 bytes a clock and SM.
 #include <cooperative_groups.h>
 
-#include <utility>
+#include <atomic>
+#include <cstddef>
 
 #include "bsa_device.cuh"
 #include "bsa_internal.h"
+#include "tc.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -50,9 +54,11 @@ constexpr int kMaxRows = 16;        // query heads of one cluster
 constexpr int kMaxK = 32;
 constexpr int kMaxItems = kMaxRows * kMaxK;
 constexpr int kMaxWarps = 12;
-constexpr int kMaxCluster = 8;
-constexpr int kListCap = 256;       // candidates of a filtered list
-constexpr int kMaxLocal = 2048;     // blocks one CTA scores
+constexpr int kMaxCluster = 16;
+constexpr int kBins = 256;
+constexpr int kListCap = 256;       // candidates a team lists
+constexpr int kMaxKeys = 32768;     // scores one CTA holds
+constexpr int kMaxSmem = 227 * 1024;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kNegInf = -__builtin_huge_valf();
 
@@ -62,38 +68,30 @@ struct Plan {
     int32_t parts;        // clusters a group is dealt to
     int32_t rows;         // query heads per cluster
     int32_t score_rows;   // rows, or 1 when the group shares the selection
-    int32_t segs;         // warps that share a row's local top-k
-    int32_t nloc;         // score slots of a row
-    int32_t list_off, part_off, main_off;
+    int32_t part_off, main_off;
 };
 
-// A CTA's best of one row, largest key first; `next` is the largest key that
-// is not in the list (0: none).
-struct List {
-    uint32_t key[kMaxK];
-    uint16_t id[kMaxK];
-    uint32_t next;
+// Scratch of the warps that select for one row.
+struct Team {
+    uint32_t hist[kBins];
+    uint16_t list[kListCap];
+    uint32_t low, high;       // smallest and largest key looked at
+    int32_t count, found;
 };
 
 struct Fixed {
-    double dscore[kMaxRows][kMaxK];
-    uint64_t seg[kMaxWarps][kMaxK];     // sorted lists of a row's parts
-    uint32_t seg_next[kMaxWarps];
-    uint16_t cand[kMaxWarps][kListCap];
-    int32_t def[kMaxRows][kMaxK];    // re-scoring: own blocks above t + 2e
-    int32_t did[kMaxRows][kMaxK];    // own best re-scored blocks
     int32_t fin[kMaxRows][kMaxK];    // the row's selection without the forced block
-    int32_t ndef[kMaxRows], nd[kMaxRows], slow[kMaxRows];
-    uint32_t lo[kMaxRows], hi[kMaxRows];
+    int32_t fin_page[kMaxRows][kMaxK];
+    float qabs[kMaxRows];            // sum of |q| over a row's channels and heads
     uint32_t bits[kDecodeMaxWidth / 32], pref[kDecodeMaxWidth / 32];
     int32_t pages[kMaxItems];
     uint32_t masks[kMaxItems];
     uint16_t items[kMaxItems];
     float wm[kMaxWarps][kMaxRows], wl[kMaxWarps][kMaxRows];
     float pm[kMaxCluster][kMaxRows], pl[kMaxCluster][kMaxRows];   // of every CTA
-    uint32_t kmaxes[kMaxCluster];
-    uint32_t kmax;
-    int32_t any_slow, n_items;
+    uint32_t kmax;                   // bits of the largest |mean| of all blocks
+    int32_t n_items;
+    Team teams[kMaxWarps];           // as many as the CTA has warps
 };
 
 // Order-preserving image of a float (NaN as -inf, -0 as +0); 0 is below all.
@@ -110,140 +108,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
-}
-
-// Bitonic networks over the 32 lanes, largest first, B independent lists at
-// once (the exchanges of one hide the latency of the others').
-template <typename T, int B>
-__device__ __forceinline__ void sort32(T (&x)[B], int lane) {
-#pragma unroll
-    for (int size = 2; size <= 32; size *= 2)
-#pragma unroll
-        for (int j = size / 2; j > 0; j /= 2) {
-            const bool larger = ((lane & j) == 0) == ((lane & size) == 0);
-#pragma unroll
-            for (int b = 0; b < B; ++b) {
-                const T y = __shfl_xor_sync(kFull, x[b], j);
-                x[b] = larger == (x[b] > y) ? x[b] : y;
-            }
-        }
-}
-
-// Merges pairs of sorted lists, x[i] with x[i + N], into their best 32;
-// `low` keeps the largest of what falls out.
-template <typename T, int B, int N>
-__device__ __forceinline__ void merge32(T (&x)[B], T &low, int lane) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const T y = __shfl_sync(kFull, x[i + N], 31 - lane);
-        const T out = x[i] > y ? y : x[i];
-        x[i] = x[i] > y ? x[i] : y;
-        low = low > out ? low : out;
-    }
-#pragma unroll
-    for (int j = 16; j > 0; j /= 2)
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const T y = __shfl_xor_sync(kFull, x[i], j);
-            x[i] = ((lane & j) == 0) == (x[i] > y) ? x[i] : y;
-        }
-}
-template <typename T, int B>
-__device__ __forceinline__ void merge_all(T (&x)[B], T &low, int lane) {
-    if constexpr (B >= 16) merge32<T, B, 8>(x, low, lane);
-    if constexpr (B >= 8) merge32<T, B, 4>(x, low, lane);
-    if constexpr (B >= 4) merge32<T, B, 2>(x, low, lane);
-    if constexpr (B >= 2) merge32<T, B, 1>(x, low, lane);
-}
-
-// (key, index) as one number: a larger key first, then a lower index.
-__device__ __forceinline__ uint64_t composite(uint32_t key, int i) {
-    return (uint64_t(key) << 32) | uint32_t(0xffff - i);
-}
-
-// B batches of 32 keys a[index(i)], i < m, sorted and merged.
-template <int B, typename F>
-__device__ __forceinline__ uint64_t best32(const uint32_t *a, int m, F index, uint64_t &low, int lane) {
-    uint64_t x[B];
-#pragma unroll
-    for (int b = 0; b < B; ++b) {
-        const int i = b * 32 + lane;
-        x[b] = 0;
-        if (i < m) {
-            const int j = index(i);
-            x[b] = composite(a[j], j);
-        }
-    }
-    sort32(x, lane);
-    merge_all(x, low, lane);
-    return x[0];
-}
-
-// The best 32 of a[0, n) (lane i has the i-th) and the largest key left out.
-// For many keys only those are sorted that are at or above the k-th largest
-// of the 32 lanes' maxima: k of the keys are, and few others (some 20 to 100
-// of 2048).
-__device__ uint64_t top32(const uint32_t *a, int n, int k, uint16_t *cand, uint32_t &next, int lane) {
-    const auto same = [](int i) { return i; };
-    uint64_t low = 0, best;
-    uint32_t rest = 0;
-    if (n <= 32) {
-        best = best32<1>(a, n, same, low, lane);
-    } else if (n <= 64) {
-        best = best32<2>(a, n, same, low, lane);
-    } else if (n <= 128) {
-        best = best32<4>(a, n, same, low, lane);
-    } else {
-        uint32_t mx[1] = {0u};
-#pragma unroll 8
-        for (int i = lane; i < n; i += 32) mx[0] = max(mx[0], a[i]);
-        sort32(mx, lane);
-        const uint32_t bound = __shfl_sync(kFull, mx[0], k - 1);
-        int m = 0;
-#pragma unroll 4
-        for (int i0 = 0; i0 < n; i0 += 32) {
-            const uint32_t x = i0 + lane < n ? a[i0 + lane] : 0u;
-            const bool in = i0 + lane < n && x >= bound;
-            const uint32_t b = __ballot_sync(kFull, in);
-            const int at = m + __popc(b & ((1u << lane) - 1));
-            if (in) {
-                if (at < kListCap) cand[at] = uint16_t(i0 + lane);
-            } else {
-                rest = max(rest, x);
-            }
-            m += __popc(b);
-        }
-        __syncwarp();
-        const auto listed = [cand](int i) { return int(cand[i]); };
-        if (m <= 32) {
-            best = best32<1>(a, m, listed, low, lane);
-        } else if (m <= 64) {
-            best = best32<2>(a, m, listed, low, lane);
-        } else if (m <= 128) {
-            best = best32<4>(a, m, listed, low, lane);
-        } else if (m <= kListCap) {
-            best = best32<8>(a, m, listed, low, lane);
-        } else {                                // many equal scores
-            rest = 0;
-            best = 0;
-            for (int i0 = 0; i0 < n; i0 += 32) {
-                uint64_t x[2] = {best, i0 + lane < n ? composite(a[i0 + lane], i0 + lane) : 0};
-                const uint64_t worst = __shfl_sync(kFull, best, 31);
-                if (!__any_sync(kFull, x[1] > worst)) {
-                    low = low > x[1] ? low : x[1];
-                    continue;
-                }
-                uint64_t y[1] = {x[1]};
-                sort32(y, lane);
-                x[1] = y[0];
-                merge32<uint64_t, 2, 1>(x, low, lane);
-                best = x[0];
-            }
-        }
-        __syncwarp();
-    }
-    next = __reduce_max_sync(kFull, max(rest, uint32_t(low >> 32)));
-    return best;
 }
 
 // Sums each of NV values over the LPB lanes of a lane group: at each step a
@@ -291,31 +155,68 @@ __device__ __forceinline__ uint32_t word(const uint4 &u, int j) {
 
 // Everything a CTA of the cluster knows about its share of the work.
 struct Job {
-    int32_t token, head, part, row0, rows, rank, nb, own, ne, kk;
+    int32_t token, head, part, row0, rows, rank, nb, own, own_page, ne, kk;
     int64_t len;
     const int32_t *table;     // the sequence's page ids
 };
 
-// q . mean of one block in fp64; lanes hold D / 32 channels of q (summed over
-// the group when it shares the selection).
+// q . mean in fp64 for up to four blocks (their loads in flight together);
+// lanes hold D / 32 channels of q (summed over the group when it shares the
+// selection).
 template <int D>
-__device__ __forceinline__ double score_fp64(const DecodeArgs &a, const Job &w, int block,
-                                             const double (&q)[D / 32], int lane) {
-    const int64_t pid = w.table[block];
-    if (pid < 0 || pid >= a.c.num_pages) return double(kNegInf);
-    const float *m = a.c.kbar + (pid * a.c.heads + w.head) * D + lane * (D / 32);
-    double s = 0.0;
+__device__ __forceinline__ void score_fp64(const DecodeArgs &a, const Job &w, const int (&block)[4],
+                                           int count, const double (&q)[D / 32], double (&s)[4],
+                                           int lane) {
+    float m[4][D / 32];
+    bool good[4];
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) s += q[e] * double(__ldg(m + e));
+    for (int i = 0; i < 4; ++i) {
+        const int64_t pid = i < count ? w.table[block[i]] : -1;
+        good[i] = pid >= 0 && pid < a.c.num_pages;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-    return s == s ? s : double(kNegInf);
+        for (int e = 0; e < D / 32; ++e)
+            m[i][e] = good[i] ? __ldg(a.c.kbar + (pid * a.c.heads + w.head) * D + lane * (D / 32) + e)
+                              : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s[i] = 0.0;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) s[i] += q[e] * double(m[i][e]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s[i] += __shfl_xor_sync(kFull, s[i], o);
+        if (!good[i] || s[i] != s[i]) s[i] = double(kNegInf);
+    }
 }
 
-// Stage 1: the keys of the CTA's n blocks from b0 on, sc[row][nloc].
+// A row's q in fp64, summed over the group when it shares the selection.
+template <int D>
+__device__ __forceinline__ void load_fp64(const DecodeArgs &a, const Plan &p, const Job &w, int row,
+                                          double (&q)[D / 32], int lane) {
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) q[e] = 0.0;
+    const int h0 = w.head * p.group + (a.share ? 0 : w.row0 + row);
+    const uint16_t *src = a.q + int64_t(w.token) * a.q_stride + int64_t(h0) * D + lane * (D / 32);
+    for (int g = 0; g < (a.share ? p.group : 1); ++g)
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e)
+            q[e] += double(__uint_as_float(uint32_t(src[g * D + e]) << 16));
+}
+
+// Puts (x, b) in front of lane `at`'s entry; the last entry falls out.
+__device__ __forceinline__ void insert_at(double &best, int &id, int at, double x, int b, int lane) {
+    const double bu = __shfl_up_sync(kFull, best, 1);
+    const int iu = __shfl_up_sync(kFull, id, 1);
+    best = lane > at ? bu : lane == at ? x : best;
+    id = lane > at ? iu : lane == at ? b : id;
+}
+
+// Stage 1: the keys of the CTA's n blocks from b0 on, each put into keys[row /
+// C][block] of CTA row % C.
 template <int D, int RP, int W>
 __device__ __forceinline__ void score_blocks(const DecodeArgs &a, const Plan &p, const Job &w,
-                                             Fixed &f, uint32_t *sc, int b0, int n) {
+                                             Fixed &f, uint32_t *keys, int b0, int n) {
+    cg::cluster_group cluster = cg::this_cluster();
     constexpr int LPB = D / 4;          // lanes per block
     constexpr int BPL = 32 / LPB;       // blocks per load instruction
     constexpr int U = 8;                // loads in flight
@@ -323,6 +224,10 @@ __device__ __forceinline__ void score_blocks(const DecodeArgs &a, const Plan &p,
     constexpr int NV = J * RP;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int ch = (lane % LPB) * 4;
+    constexpr int kStep = W * U * BPL;
+    const int ahead = lane < U * BPL ? lane : n;       // this lane's block of a batch
+    int base = warp * U * BPL;
+    int entry = base + ahead < n ? w.table[b0 + base + ahead] : 0;
     float q[RP][4];
 #pragma unroll
     for (int r = 0; r < RP; ++r)
@@ -330,12 +235,22 @@ __device__ __forceinline__ void score_blocks(const DecodeArgs &a, const Plan &p,
         for (int e = 0; e < 4; ++e) q[r][e] = 0.f;
     const uint16_t *qt = a.q + int64_t(w.token) * a.q_stride + int64_t(w.head) * p.group * D + ch;
     if (RP == 1 && a.share) {
+        float qa = 0.f;
+#pragma unroll 4
         for (int g = 0; g < p.group; ++g) {
             const uint2 x = *reinterpret_cast<const uint2 *>(qt + g * D);
-            q[0][0] += bf16_low_half(x.x);
-            q[0][1] += bf16_high_half(x.x);
-            q[0][2] += bf16_low_half(x.y);
-            q[0][3] += bf16_high_half(x.y);
+            const float v[4] = {bf16_low_half(x.x), bf16_high_half(x.x), bf16_low_half(x.y),
+                                bf16_high_half(x.y)};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                q[0][e] += v[e];
+                qa += fabsf(v[e]);
+            }
+        }
+        if (warp == 0) {
+#pragma unroll
+            for (int o = LPB / 2; o > 0; o /= 2) qa += __shfl_xor_sync(kFull, qa, o);
+            if (lane == 0) f.qabs[0] = qa;
         }
     } else {
 #pragma unroll
@@ -349,11 +264,17 @@ __device__ __forceinline__ void score_blocks(const DecodeArgs &a, const Plan &p,
             }
     }
     const int srows = a.share ? 1 : w.rows;
+    if (!(RP == 1 && a.share)) {
+#pragma unroll
+        for (int r = 0; r < RP; ++r)
+            if (r % W == warp && r < w.rows) {
+                float qa = fabsf(q[r][0]) + fabsf(q[r][1]) + fabsf(q[r][2]) + fabsf(q[r][3]);
+#pragma unroll
+                for (int o = LPB / 2; o > 0; o /= 2) qa += __shfl_xor_sync(kFull, qa, o);
+                if (lane == 0) f.qabs[r] = qa;
+            }
+    }
     uint32_t big = 0;
-    constexpr int kStep = W * U * BPL;
-    const int ahead = lane < U * BPL ? lane : n;       // this lane's block of a batch
-    int base = warp * U * BPL;
-    int entry = base + ahead < n ? w.table[b0 + base + ahead] : 0;
     for (; base < n; base += kStep) {
         int mine = -1;
         if (base + ahead < n) {
@@ -397,231 +318,240 @@ __device__ __forceinline__ void score_blocks(const DecodeArgs &a, const Plan &p,
             const int slot = (j0 + at / RP) * BPL + lane / LPB, row = at % RP;
             const bool good = __shfl_sync(kFull, mine, slot) >= 0;
             if (lane % (LPB / NV) == 0 && row < srows && base + slot < n)
-                sc[row * p.nloc + base + slot] = key_of(good ? s : kNegInf);
+                cluster.map_shared_rank(keys, row % p.cluster)[
+                    row / p.cluster * a.width + b0 + base + slot] = key_of(good ? s : kNegInf);
         }
     }
     big = __reduce_max_sync(kFull, big);
-    if (lane == 0) atomicMax(&f.kmax, big);
+    if (lane < p.cluster) atomicMax(&cluster.map_shared_rank(&f, lane)->kmax, big);
+}
+
+// The key that is the kk-th largest of keys[0, n), kk < n, found by the `team`
+// of `size` threads (whole warps; `me` is this one's index): a histogram
+// narrows the keys down to the interval that holds it, again if more than 32
+// share that.  Intervals are equal in value, or in the keys where values are
+// not finite; either way the smallest and the largest key part, so it ends.
+template <typename Sync>
+__device__ __forceinline__ uint32_t kth_largest(const uint32_t *keys, int n, int kk, Team &t, int me,
+                                                int size, Sync sync) {
+    const int lane = me & 31;
+    uint32_t from = 0u, to = kFull;     // the keys still in question
+    int above = 0;                      // how many lie above those
+    for (;;) {
+        for (int i = me; i < kBins; i += size) t.hist[i] = 0u;
+        if (me == 0) {
+            t.low = kFull;
+            t.high = 0u;
+            t.count = 0;
+        }
+        uint32_t lo = kFull, hi = 0u;
+#pragma unroll 4
+        for (int i = me; i < n; i += size) {
+            const uint32_t x = keys[i];
+            if (x >= from && x <= to) {
+                lo = min(lo, x);
+                hi = max(hi, x);
+            }
+        }
+        lo = __reduce_min_sync(kFull, lo);
+        hi = __reduce_max_sync(kFull, hi);
+        sync();
+        if (lane == 0) {
+            atomicMin(&t.low, lo);
+            atomicMax(&t.high, hi);
+        }
+        sync();
+        from = t.low;
+        to = t.high;
+        if (from == to) return from;
+        const float base = key_value(from), width = key_value(to) - base;
+        const float scale = __fdiv_rn(255.99f, width);
+        const bool linear = width < -kNegInf && scale < -kNegInf;
+        const int shift = max(0, 24 - __clz(to - from));
+        const auto bin = [&](uint32_t x) {
+            return linear ? int((key_value(x) - base) * scale) : int((x - from) >> shift);
+        };
+#pragma unroll 4
+        for (int i = me; i < n; i += size) {
+            const uint32_t x = keys[i];
+            if (x >= from && x <= to) atomicAdd(&t.hist[bin(x)], 1u);
+        }
+        sync();
+        // every warp for itself: lane l has the eight bins from 255 - 8 l down
+        uint32_t cnt[8], sum = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum += cnt[j] = t.hist[kBins - 1 - 8 * lane - j];
+        uint32_t run = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(kFull, run, o);
+            if (lane >= o) run += y;
+        }
+        const int who = __ffs(__ballot_sync(kFull, above + int(run) >= kk)) - 1;
+        int over = above + int(run - sum), pivot = 0, in = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (in == 0) {
+                if (over + int(cnt[j]) >= kk) {
+                    pivot = kBins - 1 - 8 * lane - j;
+                    in = int(cnt[j]);
+                } else {
+                    over += int(cnt[j]);
+                }
+            }
+        above = __shfl_sync(kFull, over, who);
+        pivot = __shfl_sync(kFull, pivot, who);
+        in = __shfl_sync(kFull, in, who);
+        const bool few = in <= 32;
+        if (few) {
+            // the interval's keys, through the histogram's space
+            sync();
+#pragma unroll 4
+            for (int i = me; i < n; i += size) {
+                const uint32_t x = keys[i];
+                if (x >= from && x <= to && bin(x) == pivot) t.hist[atomicAdd(&t.count, 1)] = x;
+            }
+            sync();
+            const uint32_t x = lane < in ? t.hist[lane] : 0u;
+            int rank = 0;               // keys above this one, or equal and before it
+            for (int j = 0; j < in; ++j) {
+                const uint32_t y = __shfl_sync(kFull, x, j);
+                rank += y > x || (y == x && j < lane);
+            }
+            const uint32_t b = __ballot_sync(kFull, lane < in && above + rank == kk - 1);
+            return __shfl_sync(kFull, x, __ffs(b) - 1);
+        }
+        lo = kFull;
+        hi = 0u;
+        for (int i = me; i < n; i += size) {
+            const uint32_t x = keys[i];
+            if (x >= from && x <= to && bin(x) == pivot) {
+                lo = min(lo, x);
+                hi = max(hi, x);
+            }
+        }
+        // intervals are in order, so no other key lies between its ends
+        lo = __reduce_min_sync(kFull, lo);
+        hi = __reduce_max_sync(kFull, hi);
+        sync();
+        if (me == 0) {
+            t.low = kFull;
+            t.high = 0u;
+        }
+        sync();
+        if (lane == 0) {
+            atomicMin(&t.low, lo);
+            atomicMax(&t.high, hi);
+        }
+        sync();
+        from = t.low;
+        to = t.high;
+        sync();
+    }
 }
 
 // Stage 2: fills f.fin with the kk selected ids of every score row,
-// ascending.  Every CTA of the cluster ends with the same lists.
-// lists[CTA][row] is filled by the cluster.
+// ascending, and f.fin_page with their pages, in every CTA of the cluster.
+// Row r is selected by CTA r % C, whose keys[r / C] has all its scores.
 template <int D, int W>
 __device__ __forceinline__ void select_blocks(const DecodeArgs &a, const Plan &p, const Job &w,
-                                              Fixed &f, uint32_t *sc, List *lists, int b0, int n) {
+                                              Fixed &f, const uint32_t *own_keys) {
     cg::cluster_group cluster = cg::this_cluster();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int srows = a.share ? 1 : w.rows, kk = w.kk, C = p.cluster;
-    if (threadIdx.x < C) cluster.map_shared_rank(&f, threadIdx.x)->kmaxes[w.rank] = f.kmax;
-    const auto give = [&](int row, uint64_t best, uint32_t next) {
-        const int at = 0xffff - int(uint32_t(best) & 0xffffu);
-        for (int c = 0; c < C; ++c) {
-            List *l = cluster.map_shared_rank(&lists[w.rank * p.score_rows + row], c);
-            l->key[lane] = uint32_t(best >> 32);
-            l->id[lane] = uint16_t(b0 + at);
-            if (lane == 0) l->next = next;
-        }
+    const int srows = a.share ? 1 : w.rows, kk = w.kk, C = p.cluster, n = w.ne;
+    const int mine = w.rank < srows ? (srows - w.rank + C - 1) / C : 0;
+    // the warps are dealt to the rows in teams
+    const int per = mine == 0 ? W : max(1, W / mine), size = per * 32;
+    const int team = warp / per, me = threadIdx.x - team * size;
+    const auto sync = [&] {
+        if (per == 1)
+            __syncwarp();
+        else
+            tc::named_bar_sync(1 + team, size);
     };
-    for (int task = warp; task < srows * p.segs; task += W) {
-        const int row = task / p.segs, seg = task - row * p.segs;
-        const int per = (n + p.segs - 1) / p.segs;
-        const int i0 = min(n, seg * per), m = min(n, i0 + per) - i0;
-        uint32_t next;
-        uint64_t best = top32(sc + row * p.nloc + i0, m, kk, f.cand[warp], next, lane);
-        if (best != 0) best -= uint64_t(i0);            // the row's index
-        if (p.segs == 1) {
-            give(row, best, next);
-        } else {
-            f.seg[task][lane] = best;
-            if (lane == 0) f.seg_next[task] = next;
-        }
-    }
-    if (p.segs > 1) {
-        __syncthreads();
-        for (int row = warp; row < srows; row += W) {
-            uint64_t x[8], low = 0;
-            uint32_t next = 0;
-#pragma unroll
-            for (int s = 0; s < 8; ++s) x[s] = s < p.segs ? f.seg[row * p.segs + s][lane] : 0;
-            if (lane < p.segs) next = f.seg_next[row * p.segs + lane];
-            if (p.segs > 4) merge32<uint64_t, 8, 4>(x, low, lane);
-            if (p.segs > 2) merge32<uint64_t, 8, 2>(x, low, lane);
-            merge32<uint64_t, 8, 1>(x, low, lane);
-            next = __reduce_max_sync(kFull, max(next, uint32_t(low >> 32)));
-            give(row, x[0], next);
-        }
-    }
-    if (C > 1)
-        cluster.sync();
-    else
-        __syncthreads();
-    for (int row = warp; row < srows; row += W) {
-        // t, the kk-th best of the whole row
-        uint32_t key[kMaxCluster], x[kMaxCluster], low = 0, kmax = 0, next = 0;
-#pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c)
-            x[c] = key[c] = c < C ? lists[c * p.score_rows + row].key[lane] : 0u;
-        if (lane < C) {
-            next = lists[lane * p.score_rows + row].next;
-            kmax = f.kmaxes[lane];
-        }
-        kmax = __reduce_max_sync(kFull, kmax);
-        if (C > 4) merge32<uint32_t, 8, 4>(x, low, lane);
-        if (C > 2) merge32<uint32_t, 8, 2>(x, low, lane);
-        if (C > 1) merge32<uint32_t, 8, 1>(x, low, lane);
-        const uint32_t t = __shfl_sync(kFull, x[0], kk - 1);
+    for (int k = team; k < mine && team < W / per; k += W / per) {
+        const int row = w.rank + k * C;
+        const uint32_t *keys = own_keys + k * a.width;
+        Team &t = f.teams[team];
+        const uint32_t kth = kth_largest(keys, n, kk, t, me, size, sync);
         // |computed - true| <= e: at most 4 + 5 roundings on a path of the
         // sum, 2^-24 each of sum |q||mean|, which is at most sum |q| times
         // the largest |mean|; a shared row's q is itself a sum of `group`
-        // terms.  16 + group leaves room for this bound's own roundings.
-        float qa = 0.f;
-        const int h0 = w.head * p.group + (a.share ? 0 : w.row0 + row);
-        const uint16_t *q = a.q + int64_t(w.token) * a.q_stride + int64_t(h0) * D;
-#pragma unroll 4
-        for (int e = lane; e < (a.share ? p.group : 1) * (D / 8); e += 32) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(q + e * 8);
-            const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                qa += fabsf(bf16_low_half(v[i])) + fabsf(bf16_high_half(v[i]));
-        }
-        qa = warp_sum(qa);
-        const float e = (qa * __uint_as_float(kmax)) * (float(16 + p.group) * 5.9604645e-8f) + 1e-36f;
-        const float tv = key_value(t);
+        // terms.  The last unit leaves room for this bound's own roundings.
+        const float e = (f.qabs[row] * __uint_as_float(f.kmax)) *
+                            (float(10 + (a.share ? p.group : 0)) * 5.9604645e-8f) + 1e-36f;
         uint32_t lo = 0u, hi = kFull;           // unknown: every block is open
         if (e < -kNegInf) {
-            lo = key_of(tv - 2.f * e);
-            hi = key_of(tv + 2.f * e);
+            lo = key_of(key_value(kth) - 2.f * e);
+            hi = key_of(key_value(kth) + 2.f * e);
         }
-        // the blocks at or above t - 2e, if the lists hold them all
-        int total = 0;
-#pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c)
-            if (c < C) {
-                const bool in = key[c] >= lo && key[c] != 0u;
-                const uint32_t b = __ballot_sync(kFull, in);
-                const int at = total + __popc(b & ((1u << lane) - 1));
-                if (in && at < kMaxK) f.fin[row][at] = lists[c * p.score_rows + row].id[lane];
-                total += __popc(b);
+        sync();                                 // the scratch has been read
+        if (me == 0) t.found = 0;
+        sync();
+#pragma unroll 4
+        for (int i = me; i < n; i += size)
+            if (keys[i] >= lo) {
+                const int at = atomicAdd(&t.found, 1);
+                if (at < kListCap) t.list[at] = uint16_t(i);
             }
-        const bool slow = total != kk || __any_sync(kFull, next >= lo && next != 0u);
-        __syncwarp();
-        // ascending ids
-        const int mine = lane < kk ? f.fin[row][lane] : 0x7fffffff;
-        int before = 0;
-#pragma unroll 8
-        for (int j = 0; j < kk; ++j) before += __shfl_sync(kFull, mine, j) < mine;
-        __syncwarp();
-        if (lane < kk && !slow) f.fin[row][before] = mine;
-        if (lane == 0) {
-            f.slow[row] = slow;
-            f.lo[row] = lo;
-            f.hi[row] = hi;
-            if (slow) atomicOr(&f.any_slow, 1);
-        }
-    }
-    __syncthreads();
-    // made from the same lists in every CTA of the cluster, so this is the
-    // same everywhere
-    if (f.any_slow == 0) return;
-    for (int row = warp; row < srows; row += W) {
-        if (!f.slow[row]) continue;
-        const uint32_t lo = f.lo[row], hi = f.hi[row];
-        int ndef = 0;
-        for (int i0 = 0; i0 < n; i0 += 32) {
-            const bool sure = i0 + lane < n && sc[row * p.nloc + i0 + lane] > hi;
-            const uint32_t d = __ballot_sync(kFull, sure);
-            const int at = ndef + __popc(d & ((1u << lane) - 1));
-            if (sure && at < kMaxK) f.def[row][at] = b0 + i0 + lane;
-            ndef += __popc(d);
-        }
-        if (lane == 0) f.ndef[row] = ndef;
-        double q[D / 32];
+        sync();
+        if (me >= 32) continue;                 // the next row's first sync comes before reuse
+        const int found = t.found;
+        int id = 0x7fffffff;
+        if (found == kk) {
+            if (lane < kk) id = t.list[lane];
+        } else {
+            // more than wanted: those above t + 2e, then the best of the
+            // others by their fp64 scores, lane i holding the i-th of these
+            double q[D / 32], best = 0.0;
+            load_fp64<D>(a, p, w, row, q, lane);
+            int have = 0, held = 0, open_id = 0;
+            const bool listed = found <= kListCap;
+            const int m = listed ? found : n;
+            for (int i0 = 0; i0 < m; i0 += 32) {
+                const int b = i0 + lane < m ? (listed ? int(t.list[i0 + lane]) : i0 + lane) : 0;
+                const uint32_t x = i0 + lane < m ? keys[b] : 0u;
+                uint32_t sure = __ballot_sync(kFull, i0 + lane < m && x > hi);
+                uint32_t open = __ballot_sync(kFull, i0 + lane < m && x >= lo && !(x > hi));
+                for (; sure != 0; sure &= sure - 1) {
+                    const int y = __shfl_sync(kFull, b, __ffs(sure) - 1);
+                    if (lane == have++) id = y;
+                }
+                while (open != 0) {
+                    int y[4] = {}, cnt = 0;
+                    double v[4];
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) q[e] = 0.0;
-        const int h0 = w.head * p.group + (a.share ? 0 : w.row0 + row);
-        for (int g = 0; g < (a.share ? p.group : 1); ++g) {
-            const uint16_t *src =
-                a.q + int64_t(w.token) * a.q_stride + int64_t(h0 + g) * D + lane * (D / 32);
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e) q[e] += double(__uint_as_float(uint32_t(src[e]) << 16));
-        }
-        // lane i holds the i-th best so far; ids come in ascending order, so
-        // an equal score goes behind those that are there
-        double best = 0.0;
-        int id = 0, held = 0;
-        for (int i0 = 0; i0 < n; i0 += 32) {
-            const uint32_t x = i0 + lane < n ? sc[row * p.nloc + i0 + lane] : 0u;
-            uint32_t open = __ballot_sync(kFull, i0 + lane < n && x >= lo && !(x > hi));
-            while (open != 0) {
-                const int b = b0 + i0 + __ffs(open) - 1;
-                open &= open - 1;
-                const double s = score_fp64<D>(a, w, b, q, lane);
-                const int at = __popc(__ballot_sync(kFull, lane < held && best >= s));
-                if (at < kk) {
-                    const double bu = __shfl_up_sync(kFull, best, 1);
-                    const int iu = __shfl_up_sync(kFull, id, 1);
-                    if (lane > at) {
-                        best = bu;
-                        id = iu;
-                    } else if (lane == at) {
-                        best = s;
-                        id = b;
+                    for (int j = 0; j < 4; ++j) {
+                        y[j] = __shfl_sync(kFull, b, open != 0 ? __ffs(open) - 1 : 0);
+                        cnt += open != 0;
+                        open &= open - 1;
                     }
-                    held = min(held + 1, kk);
+                    score_fp64<D>(a, w, y, cnt, q, v, lane);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j < cnt) {
+                            const int at = __popc(__ballot_sync(
+                                kFull, lane < held &&
+                                           (best > v[j] || (best == v[j] && open_id < y[j]))));
+                            insert_at(best, open_id, at, v[j], y[j], lane);
+                            held = min(held + 1, kMaxK);
+                        }
                 }
             }
+            const int y = __shfl_sync(kFull, open_id, (lane - have) & 31);
+            if (lane >= have && lane < kk) id = y;
         }
-        f.dscore[row][lane] = best;
-        f.did[row][lane] = id;
-        if (lane == 0) f.nd[row] = held;
-    }
-    cluster.sync();
-    for (int row = warp; row < srows; row += W) {
-        if (!f.slow[row]) continue;
-        int have = 0;
-        for (int c = 0; c < C; ++c) {
-            const Fixed *peer = cluster.map_shared_rank(&f, c);
-            const int m = peer->ndef[row];
-            if (lane < m && have + lane < kMaxK) f.fin[row][have + lane] = peer->def[row][lane];
-            have += m;
-        }
-        // merge the CTAs' lists; lane c walks over CTA c's, whose ids are
-        // below those of CTA c + 1
-        const Fixed *peer = cluster.map_shared_rank(&f, min(lane, C - 1));
-        const int m = lane < C ? peer->nd[row] : 0;
-        int at = 0;
-        while (have < kk) {
-            const bool there = at < m;
-            const double s = there ? peer->dscore[row][at] : 0.0;
-            const int b = there ? peer->did[row][at] : -1;
-            double bs = s;
-            int bc = there ? lane : 64;
-            for (int o = 16; o > 0; o >>= 1) {
-                const double os = __shfl_xor_sync(kFull, bs, o);
-                const int oc = __shfl_xor_sync(kFull, bc, o);
-                if (oc < 64 && (bc == 64 || os > bs || (os == bs && oc < bc))) {
-                    bs = os;
-                    bc = oc;
-                }
+        const int page = lane < kk ? w.table[id] : 0;
+        int before = 0;                         // ascending ids
+#pragma unroll 8
+        for (int j = 0; j < kMaxK; ++j) before += __shfl_sync(kFull, id, j) < id;
+        if (lane < kk)
+            for (int c = 0; c < C; ++c) {
+                Fixed *peer = cluster.map_shared_rank(&f, c);
+                peer->fin[row][before] = id;
+                peer->fin_page[row][before] = page;
             }
-            if (bc == 64) break;
-            if (lane == bc) {
-                f.fin[row][have] = b;
-                ++at;
-            }
-            ++have;
-        }
-        __syncwarp();
-        // ascending ids
-        const int mine = lane < kk ? f.fin[row][lane] : 0x7fffffff;
-        int before = 0;
-        for (int j = 0; j < kk; ++j) before += __shfl_sync(kFull, mine, j) < mine;
-        __syncwarp();
-        if (lane < kk) f.fin[row][before] = mine;
     }
-    __syncthreads();
 }
 
 // The union of the rows' lists: items (ascending ids), their pages and the
@@ -635,8 +565,7 @@ __device__ __forceinline__ void make_items(const DecodeArgs &a, const Plan &p, c
     const int sel = all ? w.ne : w.kk;
     const int cnt = sel + (w.own >= 0 ? 1 : 0);
     const uint32_t every = (1u << w.rows) - 1;
-    const auto put = [&](int at, int id) {
-        int pid = w.table[id];
+    const auto put = [&](int at, int id, int pid) {
         if (pid < 0 || pid >= a.c.num_pages) {
             report_status(a.status, kStatusBadIndex);
             pid = -1;
@@ -646,7 +575,8 @@ __device__ __forceinline__ void make_items(const DecodeArgs &a, const Plan &p, c
     };
     if (all || a.share || w.rows == 1) {
         for (int i = tid; i < cnt; i += kThreads) {
-            put(i, i == sel ? w.own : all ? i : f.fin[0][i]);
+            put(i, i == sel ? w.own : all ? i : f.fin[0][i],
+                i == sel ? w.own_page : all ? w.table[i] : f.fin_page[0][i]);
             f.masks[i] = every;
         }
         if (tid == 0) f.n_items = cnt;
@@ -681,8 +611,8 @@ __device__ __forceinline__ void make_items(const DecodeArgs &a, const Plan &p, c
             const int r = i / cnt, j = i - r * cnt;
             const int id = j == sel ? w.own : f.fin[r][j];
             const int at = int(f.pref[id >> 5]) + __popc(f.bits[id >> 5] & ((1u << (id & 31)) - 1));
-            // the first row to come looks the page up
-            if (atomicOr(&f.masks[at], 1u << r) == 0u) put(at, id);
+            if (atomicOr(&f.masks[at], 1u << r) == 0u)       // the first row to come
+                put(at, id, j == sel ? w.own_page : f.fin_page[r][j]);
         }
     }
     if (a.idx != nullptr && w.rank == 0 && (!a.share || w.part == 0)) {
@@ -905,20 +835,18 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
     for (int j = 2 * tid; j < share; j += 2 * kThreads) {
         const int i = w.rank * share + j, r = i / D;
         float mx = kNegInf;
-#pragma unroll
-        for (int k = 0; k < kMaxCluster; ++k)
-            if (k < C) mx = fmaxf(mx, f.pm[k][r]);
+#pragma unroll 4
+        for (int k = 0; k < C; ++k) mx = fmaxf(mx, f.pm[k][r]);
         const float base = mx == kNegInf ? 0.f : mx;
         float x0 = 0.f, x1 = 0.f, ls = 0.f;
-#pragma unroll
-        for (int k = 0; k < kMaxCluster; ++k)
-            if (k < C) {
-                const float2 y = *reinterpret_cast<const float2 *>(part + k * share + j);
-                const float x = exp2_fast(f.pm[k][r] - base);
-                x0 = fmaf(x, y.x, x0);
-                x1 = fmaf(x, y.y, x1);
-                ls = fmaf(x, f.pl[k][r], ls);
-            }
+#pragma unroll 4
+        for (int k = 0; k < C; ++k) {
+            const float2 y = *reinterpret_cast<const float2 *>(part + k * share + j);
+            const float x = exp2_fast(f.pm[k][r] - base);
+            x0 = fmaf(x, y.x, x0);
+            x1 = fmaf(x, y.y, x1);
+            ls = fmaf(x, f.pl[k][r], ls);
+        }
         const float inv = ls > 0.f || ls != ls ? __fdiv_rn(1.f, ls) : 0.f;
         *reinterpret_cast<uint32_t *>(out + i) = pack_bf16x2(x0 * inv, x1 * inv);
     }
@@ -928,19 +856,17 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
 // whose accumulators take twice the registers).
 constexpr int kWarpsSmall = 4;
 constexpr int warps_large(int nt) { return nt == 1 ? 12 : 8; }
+constexpr int ctas_per_sm(int d, int nt) { return nt == 2 ? 2 : d == 64 ? 4 : 3; }
 
 template <int D, int RP, int NT, int W>
-__global__ void __launch_bounds__(W * 32, W == kWarpsSmall ? (NT == 1 ? 3 : 2) : 1)
+__global__ void __launch_bounds__(W * 32, W == kWarpsSmall ? ctas_per_sm(D, NT) : 1)
     decode_kernel(DecodeArgs a, Plan p) {
     extern __shared__ __align__(16) char smem[];
     constexpr int kThreads = W * 32;
     Fixed &f = *reinterpret_cast<Fixed *>(smem);
-    List *lists = reinterpret_cast<List *>(smem + p.list_off);
     float *part = reinterpret_cast<float *>(smem + p.part_off);
-    uint32_t *sc = reinterpret_cast<uint32_t *>(smem + p.main_off);
+    uint32_t *keys = reinterpret_cast<uint32_t *>(smem + p.main_off);
     cg::cluster_group cluster = cg::this_cluster();
-    // peers may write to this CTA once all of the cluster have come this far
-    auto arrived = cluster.barrier_arrive();
     const int tid = threadIdx.x;
     Job w;
     w.rank = int(blockIdx.x % unsigned(p.cluster));
@@ -956,10 +882,7 @@ __global__ void __launch_bounds__(W * 32, W == kWarpsSmall ? (NT == 1 ? 3 : 2) :
     w.len = a.lens[w.token];
     for (int i = tid; i < kDecodeMaxWidth / 32; i += kThreads) f.bits[i] = 0u;
     for (int i = tid; i < kMaxItems; i += kThreads) f.masks[i] = 0u;
-    if (tid == 0) {
-        f.kmax = 0u;
-        f.any_slow = 0;
-    }
+    if (tid == 0) f.kmax = 0u;
     if (seq < 0 || seq >= a.seqs) {
         if (tid == 0) report_status(a.status, kStatusBadIndex);
         w.len = 0;
@@ -971,7 +894,6 @@ __global__ void __launch_bounds__(W * 32, W == kWarpsSmall ? (NT == 1 ? 3 : 2) :
     }
     w.nb = int((w.len + a.c.page - 1) / a.c.page);
     if (w.nb == 0) {                    // the same for the whole cluster
-        cluster.barrier_wait(std::move(arrived));
         if (w.rank != 0) return;
         uint16_t *out = a.out + (int64_t(w.token) * a.q_heads + w.head * p.group + w.row0) * D;
         for (int i = tid; i < w.rows * D; i += kThreads) out[i] = 0;
@@ -985,30 +907,38 @@ __global__ void __launch_bounds__(W * 32, W == kWarpsSmall ? (NT == 1 ? 3 : 2) :
     }
     w.table = a.table + seq * a.width;
     w.own = a.local ? w.nb - 1 : -1;
+    w.own_page = a.local ? w.table[w.own] : -1;
     w.ne = w.nb - (a.local ? 1 : 0);
     w.kk = a.topk - (a.local ? 1 : 0);
+    // peers may write to this CTA's shared memory from here on
+    p.cluster > 1 ? cluster.sync() : __syncthreads();
     if (w.ne > w.kk && w.kk > 0) {
-        __syncthreads();
         const int each = (w.ne + p.cluster - 1) / p.cluster;
         const int b0 = min(w.ne, w.rank * each), n = min(w.ne, b0 + each) - b0;
-        score_blocks<D, RP, W>(a, p, w, f, sc, b0, n);
-        __syncthreads();
-        cluster.barrier_wait(std::move(arrived));
-        select_blocks<D, W>(a, p, w, f, sc, lists, b0, n);
-    } else {
-        cluster.barrier_wait(std::move(arrived));
-        __syncthreads();
+        score_blocks<D, RP, W>(a, p, w, f, keys, b0, n);
+        p.cluster > 1 ? cluster.sync() : __syncthreads();
+        select_blocks<D, W>(a, p, w, f, keys);
+        p.cluster > 1 ? cluster.sync() : __syncthreads();
     }
     make_items<W>(a, p, w, f);
-    attend<D, NT, W>(a, p, w, f, part, reinterpret_cast<float *>(sc));
+    attend<D, NT, W>(a, p, w, f, part, reinterpret_cast<float *>(keys));
 }
 
 template <int D, int RP, int NT, int W>
 cudaError_t launch(const DecodeArgs &a, const Plan &p, size_t smem, int64_t items, cudaStream_t st) {
     auto kernel = decode_kernel<D, RP, NT, W>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         int(smem));
+    // once per device: calls on other threads set the same values
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev >= 64 || ((ready.load() >> dev) & 1u) == 0u) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(uint64_t(1) << dev);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(items * p.cluster));
     cfg.blockDim = dim3(W * 32);
@@ -1052,27 +982,28 @@ cudaError_t launch_paged_decode(const DecodeArgs &a, cudaStream_t st) {
     p.rows = (p.group + p.parts - 1) / p.parts;
     p.score_rows = a.share ? 1 : p.rows;
     const int64_t items = a.tokens * a.c.heads * p.parts;
-    // Few items: large CTAs, clusters of up to eight of them.  Many: small
-    // CTAs, three to an SM, so that some load while others select.
-    const bool large = items * kMaxCluster < 3 * 152;
-    const int64_t want = large ? 152 : 3 * 152;
-    p.cluster = 1;
-    while (p.cluster < kMaxCluster &&
-           (items * p.cluster < want || (a.width + p.cluster - 1) / p.cluster > kMaxLocal))
-        p.cluster *= 2;
-    if (items * p.cluster > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    p.nloc = (a.width + p.cluster - 1) / p.cluster;
+    // Few items: large CTAs, one to an SM, in clusters that fill the card.
+    // Many: small CTAs, three or four to an SM, so that some load while
+    // others select.  No more warps than there are 16-key tiles to attend to.
+    const bool large = items * 8 <= 152;
     const int warps = large ? warps_large(p.rows > 8 ? 2 : 1) : kWarpsSmall;
-    p.segs = p.score_rows >= warps ? 1 : warps / p.score_rows;
-    if (p.segs > 8) p.segs = 8;
+    const int64_t picked = int64_t(p.score_rows) * a.topk;
+    const int64_t tiles = (picked < a.width ? picked : a.width) * (a.c.page / 16);
+    p.cluster = 1;
+    while (p.cluster < (large ? kMaxCluster : 8) && p.cluster * warps < tiles &&
+           (large ? items * p.cluster * 2 <= 152 : items * p.cluster < 3 * 152))
+        p.cluster *= 2;
+    const auto kept = [&] {         // scores a CTA holds
+        return int64_t((p.score_rows + p.cluster - 1) / p.cluster) * a.width;
+    };
+    while (kept() > kMaxKeys) p.cluster *= 2;
+    if (items * p.cluster > 0x7fffffff) return cudaErrorInvalidConfiguration;
     const auto up = [](size_t x) { return (x + 15) / 16 * 16; };
-    size_t off = up(sizeof(Fixed));
-    p.list_off = int32_t(off);
-    off = up(off + size_t(p.cluster) * p.score_rows * sizeof(List));
+    size_t off = up(offsetof(Fixed, teams) + warps * sizeof(Team));
     p.part_off = int32_t(off);
     if (p.cluster > 1) off = up(off + size_t(p.rows) * a.c.d * 4);
     p.main_off = int32_t(off);
-    const size_t scores = size_t(p.score_rows) * p.nloc * 4;
+    const size_t scores = size_t(kept()) * 4;
     const size_t merge = size_t(warps) * p.rows * (a.c.d + 1) * 4;
     const size_t smem = off + up(scores > merge ? scores : merge);
     return a.c.d == 64 ? dispatch<64>(a, p, large, smem, items, st)
