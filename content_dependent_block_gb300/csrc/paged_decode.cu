@@ -13,9 +13,8 @@
 //               The scores stay in shared memory as order-preserving keys.
 //   2. top-k    each row's scores gather in the shared memory of one CTA of the
 //               cluster, whose warps find t, the k-th best, with a histogram
-//               between the smallest and the largest score (256 equal
-//               intervals, so that about one of the scores near t falls into
-//               each) and hand the selection back to the cluster.
+//               between the smallest and the largest score (64 equal
+//               intervals, so that only a few scores share the one of t) and hand the selection back to the cluster.
 //               A score is off its true value by at most e (a bound from the
 //               sums of |q| and the largest |mean|), so blocks above t + 2e
 //               are selected for certain and blocks below t - 2e are not.
@@ -53,9 +52,9 @@ namespace {
 constexpr int kMaxRows = 16;        // query heads of one cluster
 constexpr int kMaxK = 32;
 constexpr int kMaxItems = kMaxRows * kMaxK;
-constexpr int kMaxWarps = 12;
+constexpr int kMaxWarps = 8;
 constexpr int kMaxCluster = 16;
-constexpr int kBins = 256;
+constexpr int kBins = 64;
 constexpr int kListCap = 256;       // candidates a team lists
 constexpr int kMaxKeys = 32768;     // scores one CTA holds
 constexpr int kMaxSmem = 227 * 1024;
@@ -74,9 +73,11 @@ struct Plan {
 // Scratch of the warps that select for one row.
 struct Team {
     uint32_t hist[kBins];
-    uint16_t list[kListCap];
-    uint32_t low, high;       // smallest and largest key looked at
-    int32_t count, found;
+    uint32_t near[32];        // the keys of t's interval
+    uint32_t low[kMaxWarps], high[kMaxWarps], floor[kMaxWarps];
+    uint16_t list[kListCap];  // blocks of the intervals from just below t's up
+    uint16_t sel[kMaxK];
+    int32_t count, near_count;
 };
 
 struct Fixed {
@@ -132,6 +133,14 @@ __device__ __forceinline__ float reduce_exchange(float (&v)[NV], int lane) {
 #pragma unroll
     for (; o > 0; o /= 2) r += __shfl_xor_sync(kFull, r, o);
     return r;
+}
+
+// The cluster's barrier in two halves.
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -274,6 +283,7 @@ __device__ __forceinline__ void score_blocks(const DecodeArgs &a, const Plan &p,
                 if (lane == 0) f.qabs[r] = qa;
             }
     }
+    if (p.cluster > 1) cluster_wait();
     uint32_t big = 0;
     for (; base < n; base += kStep) {
         int mine = -1;
@@ -326,24 +336,29 @@ __device__ __forceinline__ void score_blocks(const DecodeArgs &a, const Plan &p,
     if (lane < p.cluster) atomicMax(&cluster.map_shared_rank(&f, lane)->kmax, big);
 }
 
-// The key that is the kk-th largest of keys[0, n), kk < n, found by the `team`
-// of `size` threads (whole warps; `me` is this one's index): a histogram
-// narrows the keys down to the interval that holds it, again if more than 32
-// share that.  Intervals are equal in value, or in the keys where values are
-// not finite; either way the smallest and the largest key part, so it ends.
+// Where a row's kk-th largest key lies.
+struct Found {
+    int in, above;            // keys in its interval, keys above that
+    bool listed;              // t.list has every key from `floor` up
+    uint32_t floor;
+};
+
+// Narrows keys[0, n), kk < n, down to an interval with the kk-th largest and
+// at most 32 keys (or equal ones only), which go to t.near, and lists the
+// blocks of that interval, the one below it and all above.  Done by the team
+// of `size` threads (whole warps; `me` is this one's index).  Intervals are
+// equal in value, or in the keys where values are not finite; either way the
+// smallest and the largest key part, so the loop ends.
 template <typename Sync>
-__device__ __forceinline__ uint32_t kth_largest(const uint32_t *keys, int n, int kk, Team &t, int me,
-                                                int size, Sync sync) {
-    const int lane = me & 31;
+__device__ __forceinline__ Found narrow(const uint32_t *keys, int n, int kk, Team &t, int me, int size,
+                                        Sync sync) {
+    const int lane = me & 31, warps = size >> 5;
     uint32_t from = 0u, to = kFull;     // the keys still in question
     int above = 0;                      // how many lie above those
+    bool first = true;
     for (;;) {
         for (int i = me; i < kBins; i += size) t.hist[i] = 0u;
-        if (me == 0) {
-            t.low = kFull;
-            t.high = 0u;
-            t.count = 0;
-        }
+        if (me == 0) t.count = t.near_count = 0;
         uint32_t lo = kFull, hi = 0u;
 #pragma unroll 4
         for (int i = me; i < n; i += size) {
@@ -355,19 +370,23 @@ __device__ __forceinline__ uint32_t kth_largest(const uint32_t *keys, int n, int
         }
         lo = __reduce_min_sync(kFull, lo);
         hi = __reduce_max_sync(kFull, hi);
-        sync();
-        if (lane == 0) {
-            atomicMin(&t.low, lo);
-            atomicMax(&t.high, hi);
+        if (warps > 1) {
+            if (lane == 0) {
+                t.low[me >> 5] = lo;
+                t.high[me >> 5] = hi;
+            }
+            sync();
+            lo = __reduce_min_sync(kFull, lane < warps ? t.low[lane] : kFull);
+            hi = __reduce_max_sync(kFull, lane < warps ? t.high[lane] : 0u);
+        } else {
+            sync();
         }
-        sync();
-        from = t.low;
-        to = t.high;
-        if (from == to) return from;
+        from = lo;
+        to = hi;
         const float base = key_value(from), width = key_value(to) - base;
-        const float scale = __fdiv_rn(255.99f, width);
-        const bool linear = width < -kNegInf && scale < -kNegInf;
-        const int shift = max(0, 24 - __clz(to - from));
+        const float scale = __fdividef(float(kBins) - 0.01f, width);
+        const bool linear = width < 1e30f && width > 1e-30f;
+        const int shift = max(0, 26 - __clz(to - from));
         const auto bin = [&](uint32_t x) {
             return linear ? int((key_value(x) - base) * scale) : int((x - from) >> shift);
         };
@@ -377,76 +396,80 @@ __device__ __forceinline__ uint32_t kth_largest(const uint32_t *keys, int n, int
             if (x >= from && x <= to) atomicAdd(&t.hist[bin(x)], 1u);
         }
         sync();
-        // every warp for itself: lane l has the eight bins from 255 - 8 l down
-        uint32_t cnt[8], sum = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum += cnt[j] = t.hist[kBins - 1 - 8 * lane - j];
-        uint32_t run = sum;
+        // every warp for itself: lane l has the l-th pair of bins from the top
+        const int top = kBins - 1 - 2 * lane;
+        const int c0 = int(t.hist[top]), c1 = int(t.hist[top - 1]);
+        int run = c0 + c1;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(kFull, run, o);
+            const int y = __shfl_up_sync(kFull, run, o);
             if (lane >= o) run += y;
         }
-        const int who = __ffs(__ballot_sync(kFull, above + int(run) >= kk)) - 1;
-        int over = above + int(run - sum), pivot = 0, in = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (in == 0) {
-                if (over + int(cnt[j]) >= kk) {
-                    pivot = kBins - 1 - 8 * lane - j;
-                    in = int(cnt[j]);
-                } else {
-                    over += int(cnt[j]);
-                }
-            }
-        above = __shfl_sync(kFull, over, who);
-        pivot = __shfl_sync(kFull, pivot, who);
-        in = __shfl_sync(kFull, in, who);
-        const bool few = in <= 32;
-        if (few) {
-            // the interval's keys, through the histogram's space
-            sync();
-#pragma unroll 4
+        const int who = __ffs(__ballot_sync(kFull, above + run >= kk)) - 1;
+        const int over = above + run - c0 - c1;         // above this lane's bins
+        const bool upper = over + c0 >= kk;
+        above = __shfl_sync(kFull, upper ? over : over + c0, who);
+        const int pivot = __shfl_sync(kFull, upper ? top : top - 1, who);
+        const int in = __shfl_sync(kFull, upper ? c0 : c1, who);
+        const int below = pivot > 0 ? int(t.hist[pivot - 1]) : 0;
+        if (in > 32 && from != to) {
+            // again within the interval; intervals are in order, so no other
+            // key lies between its ends
+            lo = kFull;
+            hi = 0u;
             for (int i = me; i < n; i += size) {
                 const uint32_t x = keys[i];
-                if (x >= from && x <= to && bin(x) == pivot) t.hist[atomicAdd(&t.count, 1)] = x;
+                if (x >= from && x <= to && bin(x) == pivot) {
+                    lo = min(lo, x);
+                    hi = max(hi, x);
+                }
+            }
+            lo = __reduce_min_sync(kFull, lo);
+            hi = __reduce_max_sync(kFull, hi);
+            sync();
+            if (lane == 0) {
+                t.low[me >> 5] = lo;
+                t.high[me >> 5] = hi;
             }
             sync();
-            const uint32_t x = lane < in ? t.hist[lane] : 0u;
-            int rank = 0;               // keys above this one, or equal and before it
-            for (int j = 0; j < in; ++j) {
-                const uint32_t y = __shfl_sync(kFull, x, j);
-                rank += y > x || (y == x && j < lane);
-            }
-            const uint32_t b = __ballot_sync(kFull, lane < in && above + rank == kk - 1);
-            return __shfl_sync(kFull, x, __ffs(b) - 1);
+            from = __reduce_min_sync(kFull, lane < warps ? t.low[lane] : kFull);
+            to = __reduce_max_sync(kFull, lane < warps ? t.high[lane] : 0u);
+            sync();
+            first = false;
+            continue;
         }
-        lo = kFull;
-        hi = 0u;
+        Found r;
+        r.in = min(in, 32);             // more only if all are equal
+        r.above = above;
+        r.listed = first && above + in + below <= kListCap;
+        const int least = r.listed ? max(0, pivot - 1) : pivot;
+        uint32_t floor = 0u;            // the largest key that is not listed
+#pragma unroll 4
         for (int i = me; i < n; i += size) {
             const uint32_t x = keys[i];
-            if (x >= from && x <= to && bin(x) == pivot) {
-                lo = min(lo, x);
-                hi = max(hi, x);
+            if (x >= from && x <= to) {
+                const int b = bin(x);
+                if (b < least) {
+                    floor = max(floor, x);
+                    continue;
+                }
+                if (b == pivot) {
+                    const int at = atomicAdd(&t.near_count, 1);
+                    if (at < 32) t.near[at] = x;
+                }
+                if (r.listed) t.list[atomicAdd(&t.count, 1)] = uint16_t(i);
             }
         }
-        // intervals are in order, so no other key lies between its ends
-        lo = __reduce_min_sync(kFull, lo);
-        hi = __reduce_max_sync(kFull, hi);
-        sync();
-        if (me == 0) {
-            t.low = kFull;
-            t.high = 0u;
+        floor = __reduce_max_sync(kFull, floor);
+        if (warps > 1) {
+            if (lane == 0) t.floor[me >> 5] = floor;
+            sync();
+            floor = __reduce_max_sync(kFull, lane < warps ? t.floor[lane] : 0u);
+        } else {
+            sync();
         }
-        sync();
-        if (lane == 0) {
-            atomicMin(&t.low, lo);
-            atomicMax(&t.high, hi);
-        }
-        sync();
-        from = t.low;
-        to = t.high;
-        sync();
+        r.floor = floor + 1u;
+        return r;
     }
 }
 
@@ -459,21 +482,46 @@ __device__ __forceinline__ void select_blocks(const DecodeArgs &a, const Plan &p
     cg::cluster_group cluster = cg::this_cluster();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int srows = a.share ? 1 : w.rows, kk = w.kk, C = p.cluster, n = w.ne;
-    const int mine = w.rank < srows ? (srows - w.rank + C - 1) / C : 0;
-    // the warps are dealt to the rows in teams
-    const int per = mine == 0 ? W : max(1, W / mine), size = per * 32;
-    const int team = warp / per, me = threadIdx.x - team * size;
+    // the warps are dealt to the rows in teams of `per`: as large as still
+    // leave a team for each row
+    const int mine = (srows - w.rank + C - 1) / C;
+    int per = 1, team = warp, teams = W;
+    if (mine <= 1) {
+        per = W;
+        team = 0;
+        teams = 1;
+    } else if (mine == 2) {
+        per = W / 2;
+        team = warp / (W / 2);
+        teams = 2;
+    } else if (mine <= W / 2) {
+        per = 2;
+        team = warp / 2;
+        teams = W / 2;
+    }
+    const int size = per * 32, me = threadIdx.x - team * size;
     const auto sync = [&] {
         if (per == 1)
             __syncwarp();
         else
             tc::named_bar_sync(1 + team, size);
     };
-    for (int k = team; k < mine && team < W / per; k += W / per) {
+    for (int k = team; k < mine; k += teams) {
         const int row = w.rank + k * C;
         const uint32_t *keys = own_keys + k * a.width;
         Team &t = f.teams[team];
-        const uint32_t kth = kth_largest(keys, n, kk, t, me, size, sync);
+        const Found r = narrow(keys, n, kk, t, me, size, sync);
+        if (me >= 32) continue;     // the next row's syncs come before the scratch is reused
+        // t, the kk-th largest: rank r.above + (keys above it in the interval,
+        // or equal and before it)
+        const uint32_t x = lane < r.in ? t.near[lane] : 0u;
+        int rank = r.above;
+        for (int j = 0; j < r.in; ++j) {
+            const uint32_t y = __shfl_sync(kFull, x, j);
+            rank += y > x || (y == x && j < lane);
+        }
+        const uint32_t hit = __ballot_sync(kFull, lane < r.in && rank == kk - 1);
+        const uint32_t kth = __shfl_sync(kFull, x, hit != 0 ? __ffs(hit) - 1 : 0);
         // |computed - true| <= e: at most 4 + 5 roundings on a path of the
         // sum, 2^-24 each of sum |q||mean|, which is at most sum |q| times
         // the largest |mean|; a shared row's q is itself a sum of `group`
@@ -485,34 +533,32 @@ __device__ __forceinline__ void select_blocks(const DecodeArgs &a, const Plan &p
             lo = key_of(key_value(kth) - 2.f * e);
             hi = key_of(key_value(kth) + 2.f * e);
         }
-        sync();                                 // the scratch has been read
-        if (me == 0) t.found = 0;
-        sync();
-#pragma unroll 4
-        for (int i = me; i < n; i += size)
-            if (keys[i] >= lo) {
-                const int at = atomicAdd(&t.found, 1);
-                if (at < kListCap) t.list[at] = uint16_t(i);
-            }
-        sync();
-        if (me >= 32) continue;                 // the next row's first sync comes before reuse
-        const int found = t.found;
+        const bool listed = r.listed && lo >= r.floor;
+        const int m = listed ? t.count : n;
+        int found = 0;
+        for (int i0 = 0; i0 < m; i0 += 32) {
+            const int b = i0 + lane < m ? (listed ? int(t.list[i0 + lane]) : i0 + lane) : 0;
+            const bool in = i0 + lane < m && keys[b] >= lo;
+            const uint32_t v = __ballot_sync(kFull, in);
+            const int at = found + __popc(v & ((1u << lane) - 1));
+            if (in && at < kMaxK) t.sel[at] = uint16_t(b);
+            found += __popc(v);
+        }
+        __syncwarp();
         int id = 0x7fffffff;
         if (found == kk) {
-            if (lane < kk) id = t.list[lane];
+            if (lane < kk) id = t.sel[lane];
         } else {
             // more than wanted: those above t + 2e, then the best of the
             // others by their fp64 scores, lane i holding the i-th of these
             double q[D / 32], best = 0.0;
             load_fp64<D>(a, p, w, row, q, lane);
             int have = 0, held = 0, open_id = 0;
-            const bool listed = found <= kListCap;
-            const int m = listed ? found : n;
             for (int i0 = 0; i0 < m; i0 += 32) {
                 const int b = i0 + lane < m ? (listed ? int(t.list[i0 + lane]) : i0 + lane) : 0;
-                const uint32_t x = i0 + lane < m ? keys[b] : 0u;
-                uint32_t sure = __ballot_sync(kFull, i0 + lane < m && x > hi);
-                uint32_t open = __ballot_sync(kFull, i0 + lane < m && x >= lo && !(x > hi));
+                const uint32_t y0 = i0 + lane < m ? keys[b] : 0u;
+                uint32_t sure = __ballot_sync(kFull, i0 + lane < m && y0 > hi);
+                uint32_t open = __ballot_sync(kFull, i0 + lane < m && y0 >= lo && !(y0 > hi));
                 for (; sure != 0; sure &= sure - 1) {
                     const int y = __shfl_sync(kFull, b, __ffs(sure) - 1);
                     if (lane == have++) id = y;
@@ -527,15 +573,15 @@ __device__ __forceinline__ void select_blocks(const DecodeArgs &a, const Plan &p
                         open &= open - 1;
                     }
                     score_fp64<D>(a, w, y, cnt, q, v, lane);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (j < cnt) {
-                            const int at = __popc(__ballot_sync(
-                                kFull, lane < held &&
-                                           (best > v[j] || (best == v[j] && open_id < y[j]))));
-                            insert_at(best, open_id, at, v[j], y[j], lane);
-                            held = min(held + 1, kMaxK);
-                        }
+#pragma unroll 1
+                    for (int j = 0; j < cnt; ++j) {
+                        const double vj = j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[2] : v[3];
+                        const int yj = j == 0 ? y[0] : j == 1 ? y[1] : j == 2 ? y[2] : y[3];
+                        const int at = __popc(__ballot_sync(
+                            kFull, lane < held && (best > vj || (best == vj && open_id < yj))));
+                        insert_at(best, open_id, at, vj, yj, lane);
+                        held = min(held + 1, kMaxK);
+                    }
                 }
             }
             const int y = __shfl_sync(kFull, open_id, (lane - have) & 31);
@@ -629,7 +675,7 @@ __device__ __forceinline__ void make_items(const DecodeArgs &a, const Plan &p, c
 }
 
 // Stage 3 and the merge.  `part` is where the cluster leaves this CTA's share
-// of the outputs, [CTA][rows * D / C].
+// of the outputs, [CTA][rows][D / C].
 template <int D, int NT, int W>
 __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const Job &w, Fixed &f,
                                        float *part, float *po) {
@@ -802,7 +848,8 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
         }
     __syncthreads();
     uint16_t *out = a.out + (int64_t(w.token) * a.q_heads + w.head * p.group + w.row0) * D;
-    const int C = p.cluster, share = w.rows * D / C;     // C divides D
+    const int C = p.cluster, share = D / C;     // channels of each CTA
+    const int shift_c = 31 - __clz(share);
     for (int i = 2 * tid; i < w.rows * D; i += 2 * kThreads) {
         const int r = i / D, c = i % D;
         float mx = kNegInf;
@@ -821,8 +868,9 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
             const float inv = ls > 0.f || ls != ls ? __fdiv_rn(1.f, ls) : 0.f;
             *reinterpret_cast<uint32_t *>(out + i) = pack_bf16x2(x0 * inv, x1 * inv);
         } else {
-            *reinterpret_cast<float2 *>(cluster.map_shared_rank(part, i / share) + w.rank * share +
-                                        i % share) = make_float2(x0, x1);
+            float *dst = cluster.map_shared_rank(part, c >> shift_c);
+            *reinterpret_cast<float2 *>(dst + ((w.rank * w.rows + r) << shift_c) + (c & (share - 1))) =
+                make_float2(x0, x1);
             if (c < 2 * C) {            // one thread of the row for each CTA
                 Fixed *peer = cluster.map_shared_rank(&f, c / 2);
                 peer->pm[w.rank][r] = mx;
@@ -832,8 +880,8 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
     }
     if (C == 1) return;
     cluster.sync();
-    for (int j = 2 * tid; j < share; j += 2 * kThreads) {
-        const int i = w.rank * share + j, r = i / D;
+    for (int j = 2 * tid; j < w.rows * share; j += 2 * kThreads) {
+        const int r = j >> shift_c, i = r * D + w.rank * share + (j & (share - 1));
         float mx = kNegInf;
 #pragma unroll 4
         for (int k = 0; k < C; ++k) mx = fmaxf(mx, f.pm[k][r]);
@@ -841,7 +889,7 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
         float x0 = 0.f, x1 = 0.f, ls = 0.f;
 #pragma unroll 4
         for (int k = 0; k < C; ++k) {
-            const float2 y = *reinterpret_cast<const float2 *>(part + k * share + j);
+            const float2 y = *reinterpret_cast<const float2 *>(part + k * w.rows * share + j);
             const float x = exp2_fast(f.pm[k][r] - base);
             x0 = fmaf(x, y.x, x0);
             x1 = fmaf(x, y.y, x1);
@@ -852,14 +900,16 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
     }
 }
 
-// CTAs per SM: three of four warps or one of twelve (eight with 16 rows,
-// whose accumulators take twice the registers).
+// Warps of a CTA, and CTAs an SM holds by their registers.  Large CTAs have six
+// warps, two to an SM: a cluster of sixteen takes sixteen SMs of one group, and
+// with one CTA to an SM only seven clusters fit the card at once.  (Sixteen
+// heads' accumulators take twice the registers.)
 constexpr int kWarpsSmall = 4;
-constexpr int warps_large(int nt) { return nt == 1 ? 12 : 8; }
+constexpr int warps_large(int nt) { return nt == 1 ? 6 : 8; }
 constexpr int ctas_per_sm(int d, int nt) { return nt == 2 ? 2 : d == 64 ? 4 : 3; }
 
 template <int D, int RP, int NT, int W>
-__global__ void __launch_bounds__(W * 32, W == kWarpsSmall ? ctas_per_sm(D, NT) : 1)
+__global__ void __launch_bounds__(W * 32, W == kWarpsSmall ? ctas_per_sm(D, NT) : W == 6 ? 2 : 1)
     decode_kernel(DecodeArgs a, Plan p) {
     extern __shared__ __align__(16) char smem[];
     constexpr int kThreads = W * 32;
@@ -910,8 +960,9 @@ __global__ void __launch_bounds__(W * 32, W == kWarpsSmall ? ctas_per_sm(D, NT) 
     w.own_page = a.local ? w.table[w.own] : -1;
     w.ne = w.nb - (a.local ? 1 : 0);
     w.kk = a.topk - (a.local ? 1 : 0);
-    // peers may write to this CTA's shared memory from here on
-    p.cluster > 1 ? cluster.sync() : __syncthreads();
+    // peers may write to this CTA's shared memory once all have come this far
+    if (p.cluster > 1) cluster_arrive();
+    __syncthreads();
     if (w.ne > w.kk && w.kk > 0) {
         const int each = (w.ne + p.cluster - 1) / p.cluster;
         const int b0 = min(w.ne, w.rank * each), n = min(w.ne, b0 + each) - b0;
@@ -919,6 +970,8 @@ __global__ void __launch_bounds__(W * 32, W == kWarpsSmall ? ctas_per_sm(D, NT) 
         p.cluster > 1 ? cluster.sync() : __syncthreads();
         select_blocks<D, W>(a, p, w, f, keys);
         p.cluster > 1 ? cluster.sync() : __syncthreads();
+    } else if (p.cluster > 1) {
+        cluster_wait();
     }
     make_items<W>(a, p, w, f);
     attend<D, NT, W>(a, p, w, f, part, reinterpret_cast<float *>(keys));
