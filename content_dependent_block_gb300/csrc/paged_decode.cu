@@ -63,6 +63,7 @@ constexpr float kNegInf = -__builtin_huge_valf();
 
 struct Plan {
     int32_t cluster;      // CTAs per (token, cache head, part of the group)
+    int32_t shift;        // log2 of that
     int32_t group;        // query heads per cache head
     int32_t parts;        // clusters a group is dealt to
     int32_t rows;         // query heads per cluster
@@ -76,7 +77,7 @@ struct Team {
     uint32_t near[32];        // the keys of t's interval
     uint32_t low[kMaxWarps], high[kMaxWarps], floor[kMaxWarps];
     uint16_t list[kListCap];  // blocks of the intervals from just below t's up
-    uint16_t sel[kMaxK];
+    uint16_t sel[kMaxK], sure[kMaxK];
     int32_t count, near_count;
 };
 
@@ -169,17 +170,17 @@ struct Job {
     const int32_t *table;     // the sequence's page ids
 };
 
-// q . mean in fp64 for up to four blocks (their loads in flight together);
+// q . mean in fp64 for one or two blocks (their loads in flight together);
 // lanes hold D / 32 channels of q (summed over the group when it shares the
 // selection).
 template <int D>
-__device__ __forceinline__ void score_fp64(const DecodeArgs &a, const Job &w, const int (&block)[4],
-                                           int count, const double (&q)[D / 32], double (&s)[4],
+__device__ __forceinline__ void score_fp64(const DecodeArgs &a, const Job &w, const int (&block)[2],
+                                           int count, const double (&q)[D / 32], double (&s)[2],
                                            int lane) {
-    float m[4][D / 32];
-    bool good[4];
+    float m[2][D / 32];
+    bool good[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
         const int64_t pid = i < count ? w.table[block[i]] : -1;
         good[i] = pid >= 0 && pid < a.c.num_pages;
 #pragma unroll
@@ -188,7 +189,7 @@ __device__ __forceinline__ void score_fp64(const DecodeArgs &a, const Job &w, co
                               : 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
         s[i] = 0.0;
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) s[i] += q[e] * double(m[i][e]);
@@ -206,6 +207,7 @@ __device__ __forceinline__ void load_fp64(const DecodeArgs &a, const Plan &p, co
     for (int e = 0; e < D / 32; ++e) q[e] = 0.0;
     const int h0 = w.head * p.group + (a.share ? 0 : w.row0 + row);
     const uint16_t *src = a.q + int64_t(w.token) * a.q_stride + int64_t(h0) * D + lane * (D / 32);
+#pragma unroll 4
     for (int g = 0; g < (a.share ? p.group : 1); ++g)
 #pragma unroll
         for (int e = 0; e < D / 32; ++e)
@@ -221,70 +223,79 @@ __device__ __forceinline__ void insert_at(double &best, int &id, int at, double 
 }
 
 // Stage 1: the keys of the CTA's n blocks from b0 on, each put into keys[row /
-// C][block] of CTA row % C.
+// C][block] of CTA row % C.  With up to four rows a lane takes eight channels of
+// a block, in two loads: half the lanes share a block's sums, which halves the
+// exchanges (96 sequences that share selections: 167 -> 160 us; with eight rows
+// the registers run out and nothing is gained).
 template <int D, int RP, int W>
 __device__ __forceinline__ void score_blocks(const DecodeArgs &a, const Plan &p, const Job &w,
                                              Fixed &f, uint32_t *keys, int b0, int n) {
     cg::cluster_group cluster = cg::this_cluster();
-    constexpr int LPB = D / 4;          // lanes per block
-    constexpr int BPL = 32 / LPB;       // blocks per load instruction
-    constexpr int U = 8;                // loads in flight
+    constexpr int L = RP <= 4 ? 2 : 1;  // 16-byte loads of a lane for a block
+    constexpr int LPB = D / 4 / L;      // lanes per block
+    constexpr int BPL = 32 / LPB;       // blocks a warp takes at a time
+    constexpr int U = 8 / L;            // such steps in flight
     constexpr int J = U < LPB / RP ? U : LPB / RP;
     constexpr int NV = J * RP;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int ch = (lane % LPB) * 4;
+    const int ch = (lane % LPB) * 4;    // and, for l > 0, 4 l LPB further
     constexpr int kStep = W * U * BPL;
     const int ahead = lane < U * BPL ? lane : n;       // this lane's block of a batch
     int base = warp * U * BPL;
     int entry = base + ahead < n ? w.table[b0 + base + ahead] : 0;
-    float q[RP][4];
+    float q[RP][L][4];
 #pragma unroll
     for (int r = 0; r < RP; ++r)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) q[r][e] = 0.f;
+        for (int l = 0; l < L; ++l)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) q[r][l][e] = 0.f;
     const uint16_t *qt = a.q + int64_t(w.token) * a.q_stride + int64_t(w.head) * p.group * D + ch;
+    const auto row_sum = [&](float x, int row) {       // over the block's lanes
+#pragma unroll
+        for (int o = LPB / 2; o > 0; o /= 2) x += __shfl_xor_sync(kFull, x, o);
+        if (lane == 0) f.qabs[row] = x;
+    };
     if (RP == 1 && a.share) {
         float qa = 0.f;
 #pragma unroll 4
-        for (int g = 0; g < p.group; ++g) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(qt + g * D);
-            const float v[4] = {bf16_low_half(x.x), bf16_high_half(x.x), bf16_low_half(x.y),
-                                bf16_high_half(x.y)};
+        for (int g = 0; g < p.group; ++g)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                q[0][e] += v[e];
-                qa += fabsf(v[e]);
+            for (int l = 0; l < L; ++l) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(qt + g * D + l * LPB * 4);
+                const float v[4] = {bf16_low_half(x.x), bf16_high_half(x.x), bf16_low_half(x.y),
+                                    bf16_high_half(x.y)};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    q[0][l][e] += v[e];
+                    qa += fabsf(v[e]);
+                }
             }
-        }
-        if (warp == 0) {
-#pragma unroll
-            for (int o = LPB / 2; o > 0; o /= 2) qa += __shfl_xor_sync(kFull, qa, o);
-            if (lane == 0) f.qabs[0] = qa;
-        }
+        if (warp == 0) row_sum(qa, 0);
     } else {
 #pragma unroll
         for (int r = 0; r < RP; ++r)
             if (r < w.rows) {
-                const uint2 x = *reinterpret_cast<const uint2 *>(qt + (w.row0 + r) * D);
-                q[r][0] = bf16_low_half(x.x);
-                q[r][1] = bf16_high_half(x.x);
-                q[r][2] = bf16_low_half(x.y);
-                q[r][3] = bf16_high_half(x.y);
+                float qa = 0.f;
+#pragma unroll
+                for (int l = 0; l < L; ++l) {
+                    const uint2 x =
+                        *reinterpret_cast<const uint2 *>(qt + (w.row0 + r) * D + l * LPB * 4);
+                    const float v[4] = {bf16_low_half(x.x), bf16_high_half(x.x),
+                                        bf16_low_half(x.y), bf16_high_half(x.y)};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        q[r][l][e] = v[e];
+                        qa += fabsf(v[e]);
+                    }
+                }
+                if (r % W == warp) row_sum(qa, r);
             }
     }
     const int srows = a.share ? 1 : w.rows;
-    if (!(RP == 1 && a.share)) {
-#pragma unroll
-        for (int r = 0; r < RP; ++r)
-            if (r % W == warp && r < w.rows) {
-                float qa = fabsf(q[r][0]) + fabsf(q[r][1]) + fabsf(q[r][2]) + fabsf(q[r][3]);
-#pragma unroll
-                for (int o = LPB / 2; o > 0; o /= 2) qa += __shfl_xor_sync(kFull, qa, o);
-                if (lane == 0) f.qabs[r] = qa;
-            }
-    }
     if (p.cluster > 1) cluster_wait();
-    uint32_t big = 0;
+    float big = 0.f;
+    bool unknown = false;
     for (; base < n; base += kStep) {
         int mine = -1;
         if (base + ahead < n) {
@@ -295,22 +306,22 @@ __device__ __forceinline__ void score_blocks(const DecodeArgs &a, const Plan &p,
             }
         }
         if (base + kStep + ahead < n) entry = w.table[b0 + base + kStep + ahead];
-        float4 x[U];
+        float4 x[U][L];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t pid = __shfl_sync(kFull, mine, u * BPL + lane / LPB);
-            x[u] = pid >= 0 ? __ldg(reinterpret_cast<const float4 *>(
-                                  a.c.kbar + (pid * a.c.heads + w.head) * D + ch))
-                            : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float *m = a.c.kbar + (pid * a.c.heads + w.head) * D + ch;
+#pragma unroll
+            for (int l = 0; l < L; ++l)
+                x[u][l] = pid >= 0 ? __ldg(reinterpret_cast<const float4 *>(m + l * LPB * 4))
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            // as integers, so that a NaN counts as larger than everything
-            big = max(big, __float_as_uint(x[u].x) & 0x7fffffffu);
-            big = max(big, __float_as_uint(x[u].y) & 0x7fffffffu);
-            big = max(big, __float_as_uint(x[u].z) & 0x7fffffffu);
-            big = max(big, __float_as_uint(x[u].w) & 0x7fffffffu);
-        }
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int l = 0; l < L; ++l)
+                big = fmaxf(fmaxf(fmaxf(big, fabsf(x[u][l].x)), fmaxf(fabsf(x[u][l].y), fabsf(x[u][l].z))),
+                            fabsf(x[u][l].w));
 #pragma unroll
         for (int j0 = 0; j0 < U; j0 += J) {
             float v[NV];
@@ -318,22 +329,30 @@ __device__ __forceinline__ void score_blocks(const DecodeArgs &a, const Plan &p,
             for (int j = 0; j < J; ++j)
 #pragma unroll
                 for (int r = 0; r < RP; ++r) {
-                    float s = q[r][0] * x[j0 + j].x;
-                    s = fmaf(q[r][1], x[j0 + j].y, s);
-                    s = fmaf(q[r][2], x[j0 + j].z, s);
-                    v[j * RP + r] = fmaf(q[r][3], x[j0 + j].w, s);
+                    float s = 0.f;
+#pragma unroll
+                    for (int l = 0; l < L; ++l) {
+                        const float4 y = x[j0 + j][l];
+                        s = fmaf(q[r][l][0], y.x, s);
+                        s = fmaf(q[r][l][1], y.y, s);
+                        s = fmaf(q[r][l][2], y.z, s);
+                        s = fmaf(q[r][l][3], y.w, s);
+                    }
+                    v[j * RP + r] = s;
                 }
             const float s = reduce_exchange<NV, LPB>(v, lane);
             const int at = (lane % LPB) / (LPB / NV);
             const int slot = (j0 + at / RP) * BPL + lane / LPB, row = at % RP;
             const bool good = __shfl_sync(kFull, mine, slot) >= 0;
+            unknown |= s != s;
             if (lane % (LPB / NV) == 0 && row < srows && base + slot < n)
-                cluster.map_shared_rank(keys, row % p.cluster)[
-                    row / p.cluster * a.width + b0 + base + slot] = key_of(good ? s : kNegInf);
+                cluster.map_shared_rank(keys, row & (p.cluster - 1))[
+                    (row >> p.shift) * a.width + b0 + base + slot] = key_of(good ? s : kNegInf);
         }
     }
-    big = __reduce_max_sync(kFull, big);
-    if (lane < p.cluster) atomicMax(&cluster.map_shared_rank(&f, lane)->kmax, big);
+    // a NaN score (from means that are not finite) leaves the bound unknown
+    const uint32_t most = __reduce_max_sync(kFull, unknown ? 0x7fffffffu : __float_as_uint(big));
+    if (lane < p.cluster) atomicMax(&cluster.map_shared_rank(&f, lane)->kmax, most);
 }
 
 // Where a row's kk-th largest key lies.
@@ -522,12 +541,12 @@ __device__ __forceinline__ void select_blocks(const DecodeArgs &a, const Plan &p
         }
         const uint32_t hit = __ballot_sync(kFull, lane < r.in && rank == kk - 1);
         const uint32_t kth = __shfl_sync(kFull, x, hit != 0 ? __ffs(hit) - 1 : 0);
-        // |computed - true| <= e: at most 4 + 5 roundings on a path of the
-        // sum, 2^-24 each of sum |q||mean|, which is at most sum |q| times
+        // |computed - true| <= e: at most 8 + 4 roundings on a path of the sum
+        // (4 + 5 with a lane's four channels), 2^-24 each of sum |q||mean|, which is at most sum |q| times
         // the largest |mean|; a shared row's q is itself a sum of `group`
         // terms.  The last unit leaves room for this bound's own roundings.
         const float e = (f.qabs[row] * __uint_as_float(f.kmax)) *
-                            (float(10 + (a.share ? p.group : 0)) * 5.9604645e-8f) + 1e-36f;
+                            (float(13 + (a.share ? p.group : 0)) * 5.9604645e-8f) + 1e-36f;
         uint32_t lo = 0u, hi = kFull;           // unknown: every block is open
         if (e < -kNegInf) {
             lo = key_of(key_value(kth) - 2.f * e);
@@ -535,14 +554,18 @@ __device__ __forceinline__ void select_blocks(const DecodeArgs &a, const Plan &p
         }
         const bool listed = r.listed && lo >= r.floor;
         const int m = listed ? t.count : n;
-        int found = 0;
+        int found = 0, have = 0;                // at or above lo, above hi
         for (int i0 = 0; i0 < m; i0 += 32) {
             const int b = i0 + lane < m ? (listed ? int(t.list[i0 + lane]) : i0 + lane) : 0;
-            const bool in = i0 + lane < m && keys[b] >= lo;
-            const uint32_t v = __ballot_sync(kFull, in);
+            const uint32_t y = i0 + lane < m ? keys[b] : 0u;
+            const uint32_t v = __ballot_sync(kFull, y >= lo && y != 0u);
+            const uint32_t u = __ballot_sync(kFull, y > hi);
             const int at = found + __popc(v & ((1u << lane) - 1));
-            if (in && at < kMaxK) t.sel[at] = uint16_t(b);
+            const int ut = have + __popc(u & ((1u << lane) - 1));
+            if (y >= lo && y != 0u && at < kMaxK) t.sel[at] = uint16_t(b);
+            if (y > hi && ut < kMaxK) t.sure[ut] = uint16_t(b);
             found += __popc(v);
+            have += __popc(u);
         }
         __syncwarp();
         int id = 0x7fffffff;
@@ -553,21 +576,17 @@ __device__ __forceinline__ void select_blocks(const DecodeArgs &a, const Plan &p
             // others by their fp64 scores, lane i holding the i-th of these
             double q[D / 32], best = 0.0;
             load_fp64<D>(a, p, w, row, q, lane);
-            int have = 0, held = 0, open_id = 0;
+            int held = 0, open_id = 0;
+            if (lane < have) id = t.sure[lane];
             for (int i0 = 0; i0 < m; i0 += 32) {
                 const int b = i0 + lane < m ? (listed ? int(t.list[i0 + lane]) : i0 + lane) : 0;
                 const uint32_t y0 = i0 + lane < m ? keys[b] : 0u;
-                uint32_t sure = __ballot_sync(kFull, i0 + lane < m && y0 > hi);
-                uint32_t open = __ballot_sync(kFull, i0 + lane < m && y0 >= lo && !(y0 > hi));
-                for (; sure != 0; sure &= sure - 1) {
-                    const int y = __shfl_sync(kFull, b, __ffs(sure) - 1);
-                    if (lane == have++) id = y;
-                }
+                uint32_t open = __ballot_sync(kFull, y0 != 0u && y0 >= lo && !(y0 > hi));
                 while (open != 0) {
-                    int y[4] = {}, cnt = 0;
-                    double v[4];
+                    int y[2], cnt = 0;
+                    double v[2];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < 2; ++j) {
                         y[j] = __shfl_sync(kFull, b, open != 0 ? __ffs(open) - 1 : 0);
                         cnt += open != 0;
                         open &= open - 1;
@@ -575,8 +594,8 @@ __device__ __forceinline__ void select_blocks(const DecodeArgs &a, const Plan &p
                     score_fp64<D>(a, w, y, cnt, q, v, lane);
 #pragma unroll 1
                     for (int j = 0; j < cnt; ++j) {
-                        const double vj = j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[2] : v[3];
-                        const int yj = j == 0 ? y[0] : j == 1 ? y[1] : j == 2 ? y[2] : y[3];
+                        const double vj = j == 0 ? v[0] : v[1];
+                        const int yj = j == 0 ? y[0] : y[1];
                         const int at = __popc(__ballot_sync(
                             kFull, lane < held && (best > vj || (best == vj && open_id < yj))));
                         insert_at(best, open_id, at, vj, yj, lane);
@@ -1035,22 +1054,27 @@ cudaError_t launch_paged_decode(const DecodeArgs &a, cudaStream_t st) {
     p.rows = (p.group + p.parts - 1) / p.parts;
     p.score_rows = a.share ? 1 : p.rows;
     const int64_t items = a.tokens * a.c.heads * p.parts;
-    // Few items: large CTAs, one to an SM, in clusters that fill the card.
-    // Many: small CTAs, three or four to an SM, so that some load while
-    // others select.  No more warps than there are 16-key tiles to attend to.
+    // Few items: large CTAs, one for each SM, in clusters (one sequence of
+    // 131072 tokens, 8 heads: 35 us; with small ones 38).  Many: small CTAs,
+    // three or four to an SM, so that some load while others select.  Clusters
+    // as large as leave all CTAs on the card at once (52 drafted tokens, 4
+    // heads: 64 us in pairs; 71 in fours, which take two turns; 90 alone).  No
+    // more warps than there are 16-key tiles to attend to.
     const bool large = items * 8 <= 152;
     const int warps = large ? warps_large(p.rows > 8 ? 2 : 1) : kWarpsSmall;
     const int64_t picked = int64_t(p.score_rows) * a.topk;
     const int64_t tiles = (picked < a.width ? picked : a.width) * (a.c.page / 16);
     p.cluster = 1;
     while (p.cluster < (large ? kMaxCluster : 8) && p.cluster * warps < tiles &&
-           (large ? items * p.cluster * 2 <= 152 : items * p.cluster < 3 * 152))
+           items * p.cluster * 2 <= 152 * (large ? 1 : ctas_per_sm(a.c.d, p.rows > 8 ? 2 : 1)))
         p.cluster *= 2;
     const auto kept = [&] {         // scores a CTA holds
         return int64_t((p.score_rows + p.cluster - 1) / p.cluster) * a.width;
     };
     while (kept() > kMaxKeys) p.cluster *= 2;
     if (items * p.cluster > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    p.shift = 0;
+    while ((1 << p.shift) < p.cluster) ++p.shift;
     const auto up = [](size_t x) { return (x + 15) / 16 * 16; };
     size_t off = up(offsetof(Fixed, teams) + warps * sizeof(Team));
     p.part_off = int32_t(off);
