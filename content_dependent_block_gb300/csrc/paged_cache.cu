@@ -14,7 +14,7 @@ constexpr int kThreads = 128;
 // sequence s owns the work items [cu[s] / B + 2 s, cu[s + 1] / B + 2 (s + 1)):
 // no item list has to be made, and spare items return at once.
 __device__ __forceinline__ int64_t first_item(const int32_t *cu, int64_t s, int32_t page) {
-    return int64_t(cu[s]) / page + 2 * s;
+    return int64_t(cu[s] / page) + 2 * s;
 }
 
 // One CTA per (touched page, head).  The new rows are copied into the page
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, int64_t 
     if (hi == lo) return;
     const int64_t start = a.start[seq];
     const int64_t end = start + (hi - lo);  // length afterwards
-    const int64_t block = start / page + item;
+    const int64_t block = int32_t(start) / page + item;
     if (start < 0 || end > int64_t(a.width) * page) {
         if (threadIdx.x == 0) report_status(a.status, kStatusInvalidArg);
         return;

@@ -234,12 +234,13 @@ __device__ __forceinline__ void score_blocks(const DecodeArgs &a, const Plan &p,
     constexpr int L = RP <= 4 ? 2 : 1;  // 16-byte loads of a lane for a block
     constexpr int LPB = D / 4 / L;      // lanes per block
     constexpr int BPL = 32 / LPB;       // blocks a warp takes at a time
-    constexpr int U = 8 / L;            // such steps in flight
+    constexpr int U = (RP <= 2 ? 16 : 8) / L;          // such steps in flight
     constexpr int J = U < LPB / RP ? U : LPB / RP;
     constexpr int NV = J * RP;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int ch = (lane % LPB) * 4;    // and, for l > 0, 4 l LPB further
     constexpr int kStep = W * U * BPL;
+    static_assert(U * BPL <= 32, "a lane looks up one page");
     const int ahead = lane < U * BPL ? lane : n;       // this lane's block of a batch
     int base = warp * U * BPL;
     int entry = base + ahead < n ? w.table[b0 + base + ahead] : 0;
@@ -939,10 +940,10 @@ __global__ void __launch_bounds__(W * 32, W == kWarpsSmall ? ctas_per_sm(D, NT) 
     const int tid = threadIdx.x;
     Job w;
     w.rank = int(blockIdx.x % unsigned(p.cluster));
-    const int64_t item = blockIdx.x / unsigned(p.cluster);
-    const int per = a.c.heads * p.parts;
+    const unsigned item = blockIdx.x / unsigned(p.cluster);
+    const unsigned per = unsigned(a.c.heads * p.parts);
     w.token = int32_t(item / per);
-    const int hp = int(item - int64_t(w.token) * per);
+    const int hp = int(item - unsigned(w.token) * per);
     w.head = hp / p.parts;
     w.part = hp - w.head * p.parts;
     w.row0 = w.part * p.rows;
@@ -961,7 +962,7 @@ __global__ void __launch_bounds__(W * 32, W == kWarpsSmall ? ctas_per_sm(D, NT) 
         if (tid == 0) report_status(a.status, kStatusInvalidArg);
         w.len = w.len < 0 ? 0 : most;
     }
-    w.nb = int((w.len + a.c.page - 1) / a.c.page);
+    w.nb = int((w.len + a.c.page - 1) >> (31 - __clz(a.c.page)));      // a power of two
     if (w.nb == 0) {                    // the same for the whole cluster
         if (w.rank != 0) return;
         uint16_t *out = a.out + (int64_t(w.token) * a.q_heads + w.head * p.group + w.row0) * D;
