@@ -612,6 +612,9 @@ def copy_pages(cache: PagedCache, pairs):
     device, or a host array as PageTable hands them out."""
     torch = _torch()
     if not isinstance(pairs, torch.Tensor):
+        pairs = np.asarray(pairs).reshape(-1, 2)
+        if len(np.unique(pairs[:, 1])) < len(pairs) or np.isin(pairs[:, 1], pairs[:, 0]).any():
+            raise ValueError("a page is the target of two pairs, or of one and the source of another")
         pairs = torch.from_numpy(np.ascontiguousarray(pairs, dtype=np.int32)).to(cache.k.device)
     count = pairs.shape[0]
     _check(lib().bsa_cache_copy_pages(cache.struct, _i32(pairs, "pairs", (count, 2)), count,

@@ -905,6 +905,17 @@ static bsa_status check_i32(const int32_t *p, const char *name) {
     return BSA_OK;
 }
 
+// Whether [a, a + na) and [b, b + nb) share a byte.
+static bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + uintptr_t(nb) && y < x + uintptr_t(na);
+}
+
+static bool in_cache(const bsa_cache &c, const void *p, int64_t bytes) {
+    const int64_t means = c.num_pages * c.heads * c.d * 4, kv = means / 2 * c.page;
+    return overlap(c.k, kv, p, bytes) || overlap(c.v, kv, p, bytes) || overlap(c.kbar, means, p, bytes);
+}
+
 static bsa_status check_token_stride(int64_t stride, int64_t row, const char *name) {
     if (stride < row) return fail(BSA_ERR_INVALID_ARG, "%s must be >= heads * d", name);
     if (stride % 8 != 0) return fail(BSA_ERR_ALIGNMENT, "%s must be a multiple of 8", name);
@@ -932,6 +943,10 @@ bsa_status bsa_cache_append(bsa_cache cache, const void *k, int64_t k_stride, co
     if (cu_tokens != nullptr) BSA_TRY(check_i32(cu_tokens, "cu_tokens"));
     BSA_TRY(check_i32(start, "start"));
     BSA_TRY(check_i32(table, "table"));
+    const int64_t row = int64_t(cache.heads) * cache.d;
+    if (in_cache(cache, k, ((tokens - 1) * k_stride + row) * 2) ||
+        in_cache(cache, v, ((tokens - 1) * v_stride + row) * 2))
+        return fail(BSA_ERR_INVALID_ARG, "k or v overlaps the cache");
     a.k = static_cast<const uint16_t *>(k);
     a.v = static_cast<const uint16_t *>(v);
     a.k_stride = k_stride;
@@ -966,8 +981,8 @@ bsa_status bsa_paged_decode(bsa_cache cache, const void *q, int64_t q_stride, in
                             void *out, int32_t *idx_out, void *stream) {
     bsa::DecodeArgs a = {};
     BSA_TRY(cache_view(cache, &a.c));
-    if (tokens < 1 || seqs < 1 || table_width < 1)
-        return fail(BSA_ERR_INVALID_ARG, "tokens, seqs and table_width must be >= 1");
+    if (tokens < 0 || seqs < 1 || table_width < 1)
+        return fail(BSA_ERR_INVALID_ARG, "tokens must be >= 0, seqs and table_width >= 1");
     if (tokens > 0x7fffffff || seqs > 0x7fffffff)
         return fail(BSA_ERR_UNSUPPORTED, "tokens and seqs must fit in int32");
     if (q_heads < 1 || q_heads % cache.heads != 0)
@@ -979,6 +994,7 @@ bsa_status bsa_paged_decode(bsa_cache cache, const void *q, int64_t q_stride, in
         return fail(BSA_ERR_UNSUPPORTED, "table_width must be <= %d", bsa::kDecodeMaxWidth);
     if (token_seq == nullptr && seqs < tokens)
         return fail(BSA_ERR_INVALID_ARG, "without token_seq there must be a sequence per token");
+    if (tokens == 0) return ok();           // q and out may be empty then
     BSA_TRY(check_ptr(q, "q"));
     BSA_TRY(check_ptr(out, "out"));
     BSA_TRY(check_token_stride(q_stride, int64_t(q_heads) * cache.d, "q_stride"));
@@ -987,6 +1003,10 @@ bsa_status bsa_paged_decode(bsa_cache cache, const void *q, int64_t q_stride, in
     if (token_seq != nullptr) BSA_TRY(check_i32(token_seq, "token_seq"));
     if (idx_out != nullptr) BSA_TRY(check_i32(idx_out, "idx_out"));
     if (std::isnan(scale)) return fail(BSA_ERR_INVALID_ARG, "scale is NaN");
+    const int64_t row = int64_t(q_heads) * cache.d, out_bytes = tokens * row * 2;
+    if (overlap(q, ((tokens - 1) * q_stride + row) * 2, out, out_bytes) ||
+        in_cache(cache, out, out_bytes))
+        return fail(BSA_ERR_INVALID_ARG, "out overlaps q or the cache");
     a.q = static_cast<const uint16_t *>(q);
     a.q_stride = q_stride;
     a.tokens = tokens;

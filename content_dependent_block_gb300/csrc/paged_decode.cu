@@ -93,6 +93,8 @@ struct Fixed {
     float pm[kMaxCluster][kMaxRows], pl[kMaxCluster][kMaxRows];   // of every CTA
     uint32_t kmax;                   // bits of the largest |mean| of all blocks
     int32_t n_items;
+    uint32_t redo;                   // rows whose output is not finite
+    float redo_m[kMaxRows], redo_inv[kMaxRows];
     Team teams[kMaxWarps];           // as many as the CTA has warps
 };
 
@@ -572,6 +574,20 @@ __device__ __forceinline__ void select_blocks(const DecodeArgs &a, const Plan &p
         int id = 0x7fffffff;
         if (found == kk) {
             if (lane < kk) id = t.sel[lane];
+        } else if (!(f.qabs[row] > 0.f) || f.kmax == 0u) {
+            // q or all means zero, or a NaN in q: the scores are exact (0, or
+            // -inf for a page that is not there and for NaN), so the ids decide
+            int got = 0;
+            for (int pass = 0; pass < 2; ++pass)        // above the kk-th, then equal to it
+                for (int i0 = 0; i0 < n && got < kk; i0 += 32) {
+                    const uint32_t y = i0 + lane < n ? keys[i0 + lane] : 0u;
+                    const uint32_t v = __ballot_sync(kFull, pass == 0 ? y > kth : y == kth);
+                    const int at = got + __popc(v & ((1u << lane) - 1));
+                    if ((v >> lane & 1u) && at < kk) t.sel[at] = uint16_t(i0 + lane);
+                    got += __popc(v);
+                }
+            __syncwarp();
+            if (lane < kk) id = t.sel[lane];
         } else {
             // more than wanted: those above t + 2e, then the best of the
             // others by their fp64 scores, lane i holding the i-th of these
@@ -690,6 +706,50 @@ __device__ __forceinline__ void make_items(const DecodeArgs &a, const Plan &p, c
                                         : int64_t(w.token) * a.q_heads + w.head * p.group + w.row0 + r;
             a.idx[row * a.topk + j] = id;
         }
+    }
+    __syncthreads();
+}
+
+// A row whose output is not finite, again and alone: the shared tiles multiply
+// a masked key's weight 0 with its value, which must not count where that is
+// infinite or NaN.  Every warp takes keys of the row's own blocks; `sum` has
+// W + 1 rows of D.
+template <int D, int W>
+__device__ __noinline__ void attend_alone(const DecodeArgs &a, const Plan &p, const Job &w,
+                                          const Fixed &f, int row, float mx, float *sum) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint16_t *qr = a.q + int64_t(w.token) * a.q_stride +
+                         int64_t(w.head * p.group + w.row0 + row) * D + lane * E;
+    float q[E], acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        q[e] = __uint_as_float(uint32_t(qr[e]) << 16);
+        acc[e] = 0.f;
+    }
+    for (int i = 0; i < f.n_items; ++i) {
+        const int64_t pid = f.pages[i];
+        if (!(f.masks[i] >> row & 1u) || pid < 0) continue;
+        const int keys = int(i64min(a.c.page, w.len - int64_t(f.items[i]) * a.c.page));
+        for (int j = warp; j < keys; j += W) {
+            const int64_t at = ((pid * a.c.heads + w.head) * a.c.page + j) * D + lane * E;
+            float s = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) s = fmaf(q[e], __uint_as_float(uint32_t(a.c.k[at + e]) << 16), s);
+            const float x = exp2_fast(warp_sum(s) * a.scale_log2 - (mx == kNegInf ? 0.f : mx));
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                acc[e] = fmaf(x, __uint_as_float(uint32_t(a.c.v[at + e]) << 16), acc[e]);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[warp * D + lane * E + e] = acc[e];
+    __syncthreads();
+    for (int c = threadIdx.x; c < D; c += W * 32) {
+        float x = 0.f;
+        for (int k = 0; k < W; ++k) x += sum[k * D + c];
+        sum[W * D + c] = x;
     }
     __syncthreads();
 }
@@ -870,6 +930,18 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
     uint16_t *out = a.out + (int64_t(w.token) * a.q_heads + w.head * p.group + w.row0) * D;
     const int C = p.cluster, share = D / C;     // channels of each CTA
     const int shift_c = 31 - __clz(share);
+    // a row with no key to attend to is zero
+    const auto put = [&](int i, int r, float mx, float ls, float x0, float x1) {
+        const float inv = ls > 0.f || ls != ls ? __fdiv_rn(1.f, ls) : 0.f;
+        x0 *= inv;
+        x1 *= inv;
+        *reinterpret_cast<uint32_t *>(out + i) = pack_bf16x2(x0, x1);
+        if (!(fabsf(x0) < -kNegInf && fabsf(x1) < -kNegInf)) {
+            f.redo_m[r] = mx;
+            f.redo_inv[r] = inv;
+            atomicOr(&f.redo, 1u << r);
+        }
+    };
     for (int i = 2 * tid; i < w.rows * D; i += 2 * kThreads) {
         const int r = i / D, c = i % D;
         float mx = kNegInf;
@@ -885,8 +957,7 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
             ls = fmaf(x, f.wl[k][r], ls);
         }
         if (C == 1) {
-            const float inv = ls > 0.f || ls != ls ? __fdiv_rn(1.f, ls) : 0.f;
-            *reinterpret_cast<uint32_t *>(out + i) = pack_bf16x2(x0 * inv, x1 * inv);
+            put(i, r, mx, ls, x0, x1);
         } else {
             float *dst = cluster.map_shared_rank(part, c >> shift_c);
             *reinterpret_cast<float2 *>(dst + ((w.rank * w.rows + r) << shift_c) + (c & (share - 1))) =
@@ -898,25 +969,36 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
             }
         }
     }
-    if (C == 1) return;
-    cluster.sync();
-    for (int j = 2 * tid; j < w.rows * share; j += 2 * kThreads) {
-        const int r = j >> shift_c, i = r * D + w.rank * share + (j & (share - 1));
-        float mx = kNegInf;
+    if (C > 1) {
+        cluster.sync();
+        for (int j = 2 * tid; j < w.rows * share; j += 2 * kThreads) {
+            const int r = j >> shift_c, i = r * D + w.rank * share + (j & (share - 1));
+            float mx = kNegInf;
 #pragma unroll 4
-        for (int k = 0; k < C; ++k) mx = fmaxf(mx, f.pm[k][r]);
-        const float base = mx == kNegInf ? 0.f : mx;
-        float x0 = 0.f, x1 = 0.f, ls = 0.f;
+            for (int k = 0; k < C; ++k) mx = fmaxf(mx, f.pm[k][r]);
+            const float base = mx == kNegInf ? 0.f : mx;
+            float x0 = 0.f, x1 = 0.f, ls = 0.f;
 #pragma unroll 4
-        for (int k = 0; k < C; ++k) {
-            const float2 y = *reinterpret_cast<const float2 *>(part + k * w.rows * share + j);
-            const float x = exp2_fast(f.pm[k][r] - base);
-            x0 = fmaf(x, y.x, x0);
-            x1 = fmaf(x, y.y, x1);
-            ls = fmaf(x, f.pl[k][r], ls);
+            for (int k = 0; k < C; ++k) {
+                const float2 y = *reinterpret_cast<const float2 *>(part + k * w.rows * share + j);
+                const float x = exp2_fast(f.pm[k][r] - base);
+                x0 = fmaf(x, y.x, x0);
+                x1 = fmaf(x, y.y, x1);
+                ls = fmaf(x, f.pl[k][r], ls);
+            }
+            put(i, r, mx, ls, x0, x1);
         }
-        const float inv = ls > 0.f || ls != ls ? __fdiv_rn(1.f, ls) : 0.f;
-        *reinterpret_cast<uint32_t *>(out + i) = pack_bf16x2(x0 * inv, x1 * inv);
+    }
+    __syncthreads();
+    // one list for all rows has no masked key
+    if (f.redo == 0u || a.share || w.rows == 1) return;
+    for (int r = 0; r < w.rows; ++r) {
+        if (!(f.redo >> r & 1u)) continue;
+        attend_alone<D, W>(a, p, w, f, r, f.redo_m[r], po);
+        for (int c = tid; c < share; c += kThreads) {
+            const float x = po[W * D + w.rank * share + c] * f.redo_inv[r];
+            out[r * D + w.rank * share + c] = f32_to_bf16_bits(x);
+        }
     }
 }
 
@@ -952,7 +1034,7 @@ __global__ void __launch_bounds__(W * 32, W == kWarpsSmall ? ctas_per_sm(D, NT) 
     w.len = a.lens[w.token];
     for (int i = tid; i < kDecodeMaxWidth / 32; i += kThreads) f.bits[i] = 0u;
     for (int i = tid; i < kMaxItems; i += kThreads) f.masks[i] = 0u;
-    if (tid == 0) f.kmax = 0u;
+    if (tid == 0) f.kmax = f.redo = 0u;
     if (seq < 0 || seq >= a.seqs) {
         if (tid == 0) report_status(a.status, kStatusBadIndex);
         w.len = 0;

@@ -32,8 +32,11 @@
  *     bounded wait that ran out) never trap: the kernel skips the offending
  *     work, records the first such code in a device status word and
  *     returns.  bsa_get_device_status() reads and clears that word.
+ *   - The first call of an entry point on a device loads its kernels; make
+ *     it before capturing a stream.
  *   - Supported: d in {64, 128}; key_block B in {16, 32, 64, 128};
- *     dtype bf16 everywhere, fp32 for the fine stage.
+ *     dtype bf16 everywhere, fp32 for the fine stage and the rotary
+ *     positions.
  */
 #ifndef BSA_H_
 #define BSA_H_
@@ -525,7 +528,7 @@ bsa_status bsa_cache_copy_pages(bsa_cache cache, const int32_t *pairs, int64_t c
  *              share_group  the query heads of a cache head share one
  *                           selection, made on the sum of their scores.
  *   scale      softmax scale; <= 0 selects 1/sqrt(d).
- *   out        [tokens][q_heads][d] bf16 (device).
+ *   out        [tokens][q_heads][d] bf16 (device); not q, nor in the cache.
  *   idx_out    optional int32 (device) [tokens][q_heads][topk], or
  *              [tokens][heads][topk] with share_group: the selected blocks,
  *              ascending, -1 after the last.

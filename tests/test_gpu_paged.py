@@ -311,6 +311,122 @@ def test_decode_means_that_are_not_finite(value):
     _check(k, v, kbar, q, table, lens, 4)
 
 
+@pytest.mark.parametrize("seqs", [1, 2, 70])
+def test_decode_keeps_other_rows_from_values_that_are_not_finite(seqs):
+    """Heads of a group share the tiles of their blocks; an infinite or NaN
+    value counts for the heads that selected its block, and for no other."""
+    g = torch.Generator().manual_seed(30)
+    lens = [60 * 16 + 5] * seqs
+    k, v, kbar, q, table = _problem(g, lens, 6, 1, 64, 16)
+    _, _, sel = ref.decode(k, v, kbar, q, table, lens, 4)
+    v = torch.where(torch.isfinite(v), v, 0)               # the rows behind the end, too
+    bad = []
+    for s in range(seqs):
+        only = [b for b in sel[s, 0].tolist() if b not in sel[s, 1:].flatten().tolist()]
+        bad.append(bool(only))
+        if only:
+            v[table[s, only[0]], 0, 3, 7] = float("inf") if s % 2 else float("nan")
+    assert any(bad)
+    want, tol, widx = ref.decode(k, v, kbar, q, table, lens, 4)
+    out, idx = bsa.paged_decode(_cache(k, v, kbar), q.cuda(), table.cuda(), _i32(lens), 4)
+    out = out.cpu()
+    assert torch.equal(idx.cpu(), widx)
+    ref.assert_within(out[:, 1:], want[:, 1:], tol[:, 1:], "the other heads")
+    for s in range(seqs):
+        rest = [c for c in range(64) if c != 7]
+        ref.assert_within(out[s, 0, rest], want[s, 0, rest], tol[s, 0, rest], "the head's other channels")
+        assert torch.isfinite(out[s, 0, 7]) == torch.tensor(not bad[s])
+
+
+@pytest.mark.parametrize("what", ["q zero", "q nan", "q inf", "means zero", "a page missing"])
+@pytest.mark.parametrize("width", [80, 3000])
+def test_decode_scores_that_decide_nothing(what, width):
+    """No score differs (or none is a number): the lowest ids, and in time."""
+    g = torch.Generator().manual_seed(31)
+    n = width * 16 - 3
+    k, v, kbar, q, table = _problem(g, [n], 3, 1, 64, 16)
+    fill = {"q zero": 0.0, "q nan": float("nan"), "q inf": float("inf")}.get(what)
+    if fill is not None:
+        q[:, 1] = fill
+    if what in ("means zero", "a page missing"):
+        kbar[:] = 0
+    bad = table.clone()
+    if what == "a page missing":
+        bad[0, 2] = -5
+    c = _cache(k, v, kbar)
+    out, idx = bsa.paged_decode(c, q.cuda(), bad.cuda(), _i32([n]), 4, local_block=False)
+    torch.cuda.synchronize()
+    assert bsa.device_status() == (3 if what == "a page missing" else 0)
+    if what in ("q zero", "means zero"):
+        assert idx[0, 1].tolist() == [0, 1, 2, 3]
+    if what == "a page missing":
+        assert idx[0].tolist() == [[0, 1, 3, 4]] * 3
+    if what == "q nan":
+        assert idx[0, 1].tolist() == [0, 1, 2, 3] and out[0, 1].isnan().all()
+    if what == "q inf":              # every score is NaN or infinite
+        assert (idx[0, 1].diff() > 0).all() and not torch.isfinite(out[0, 1]).any()
+    others = [0, 2] if fill is not None else [0, 1, 2] if what == "means zero" else []
+    want, tol, widx = ref.decode(k, v, kbar, q, table, [n], 4, local=False)
+    for h in others:
+        assert torch.equal(idx[0, h].cpu(), widx[0, h])
+        ref.assert_within(out[0, h], want[0, h], tol[0, h], "the other heads")
+
+
+def test_pages_past_32_bit_offsets():
+    """A cache of more than 2^32 elements: pages at its end are appended to,
+    copied and read at their own places."""
+    g = torch.Generator().manual_seed(32)
+    heads, page, d = 8, 128, 128
+    pool = (1 << 32) // (heads * page * d) + 40
+    k, v = (torch.empty((pool, heads, page, d), dtype=BF16, device="cuda") for _ in range(2))
+    kbar = torch.zeros((pool, heads, d), device="cuda")
+    c = bsa.PagedCache(k, v, kbar)
+    ids = [pool - 1, 3, pool - 2, pool - 7, 5]
+    n = 5 * page - 11
+    nk, nv = _randn(g, n, heads, d), _randn(g, n, heads, d)
+    bsa.cache_append(c, nk.cuda(), nv.cuda(), _i32([ids]), _i32([0]))
+    moved = [pool - 20, 3, pool - 2, pool - 21, 5]
+    bsa.copy_pages(c, np.array([[pool - 1, pool - 20], [pool - 7, pool - 21]], dtype=np.int32))
+    q = _randn(g, 1, 2 * heads, d)
+    out, idx = bsa.paged_decode(c, q.cuda(), _i32([moved]), _i32([n]), 3)
+    small = [torch.stack([t[i] for i in moved]).cpu() for t in (k, v, kbar)]
+    rows = torch.cat([nk, torch.zeros(11, heads, d, dtype=BF16)]).view(5, page, heads, d).transpose(1, 2)
+    assert torch.equal(small[0][:4], rows[:4]) and torch.equal(small[0][4, :, :page - 11], rows[4, :, :page - 11])
+    want, tol, widx = ref.decode(*small, q, torch.arange(5)[None], [n], 3)
+    assert torch.equal(idx.cpu(), widx)
+    ref.assert_within(out, want, tol, "decode")
+    assert bsa.device_status() == 0
+
+
+def test_two_calls_at_once():
+    """Calls on two streams share nothing but the status word."""
+    g = torch.Generator().manual_seed(33)
+    calls = []
+    for i in range(2):
+        lens = torch.randint(1, 3000, (20,), generator=g).tolist()
+        k, v, kbar, q, table = _problem(g, lens, 8, 2, 64, 16)
+        calls.append((_cache(k, v, kbar), q.cuda(), table.cuda(), _i32(lens)))
+    want = [bsa.paged_decode(*c, 8)[0] for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(bsa.paged_decode(*calls[i], 8)[0])
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        assert all(torch.equal(w, x) for x in runs)
+
+
+def test_no_tokens():
+    c = bsa.PagedCache.empty(4, 2, 16, 64)
+    q = torch.zeros(0, 4, 64, dtype=BF16, device="cuda")
+    out, idx = bsa.paged_decode(c, q, _i32([[0]]), _i32([]), 2)
+    assert out.shape == (0, 4, 64) and idx.shape == (0, 4, 2)
+
+
 def test_decode_reads_no_page_behind_the_end():
     g = torch.Generator().manual_seed(15)
     lens = [33, 1]

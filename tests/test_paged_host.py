@@ -142,7 +142,8 @@ def test_copy_refusals(L):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(q=None), 1), (dict(q=MISALIGNED), 7), (dict(qs=192), 1), (dict(qs=258), 7),
-    (dict(tokens=0), 1), (dict(heads=5), 1), (dict(heads=0), 1), (dict(heads=2 * 129), 2),
+    (dict(tokens=0), 0), (dict(tokens=-1), 1), (dict(heads=5), 1), (dict(heads=0), 1),
+    (dict(heads=2 * 129), 2),
     (dict(topk=0), 2), (dict(topk=33), 2), (dict(width=16385), 2), (dict(width=0), 1),
     (dict(seqs=3), 1), (dict(seqs=0, ts=FAKE), 1), (dict(table=None), 1), (dict(lens=None), 1),
     (dict(ts=ODD), 7), (dict(idx=ODD), 7), (dict(out=None), 1), (dict(scale=math.nan), 1),
@@ -156,6 +157,31 @@ def test_decode_refusals(L, kw, code):
     assert L.bsa_paged_decode(_cache(), a["q"], a["qs"], a["tokens"], a["heads"], a["table"], a["width"],
                               a["seqs"], a["ts"], a["lens"], a["topk"], None, a["scale"], a["out"],
                               a["idx"], None) == code, L.bsa_last_error()
+
+
+def test_tensors_that_overlap_are_refused(L):
+    """New rows inside the cache, an output on its queries or inside the cache."""
+    c = _cache()
+    inside = [c.k, c.k + 8 * 2 * 64 * 64 * 2 - 16, c.v, c.kbar + 8 * 2 * 64 * 4 - 16]
+    for p in inside:
+        p = ctypes.c_void_p(p)
+        assert L.bsa_cache_append(c, p, 128, OTHER, 128, 4, 4, None, FAKE, FAKE, 4, None) == 1
+        assert L.bsa_cache_append(c, OTHER, 128, p, 128, 4, 4, None, FAKE, FAKE, 4, None) == 1
+        assert L.bsa_paged_decode(c, OTHER, 256, 4, 4, FAKE, 4, 4, None, FAKE, 2, None, 0.0, p, None,
+                                  None) == 1
+        assert b"overlap" in L.bsa_last_error()
+    for shift in (0, 16, 4 * 256 * 2 - 16):
+        out = ctypes.c_void_p(OTHER.value + shift)
+        assert L.bsa_paged_decode(c, OTHER, 256, 4, 4, FAKE, 4, 4, None, FAKE, 2, None, 0.0, out, None,
+                                  None) == 1
+
+
+def test_copies_from_the_host_must_not_chain():
+    import torch
+    c = type("C", (), {"k": torch.zeros(1)})()
+    for pairs in ([[0, 1], [2, 1]], [[0, 1], [1, 2]], [[3, 3]]):
+        with pytest.raises(ValueError):
+            bsa.copy_pages(c, np.array(pairs, dtype=np.int32))
 
 
 # ------------------------------------------------------------- page manager
