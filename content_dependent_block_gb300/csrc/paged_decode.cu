@@ -52,7 +52,7 @@ namespace {
 constexpr int kMaxRows = 16;        // query heads of one cluster
 constexpr int kMaxK = 32;
 constexpr int kMaxItems = kMaxRows * kMaxK;
-constexpr int kMaxWarps = 8;
+constexpr int kMaxWarps = 12;
 constexpr int kMaxCluster = 16;
 constexpr int kBins = 64;
 constexpr int kListCap = 256;       // candidates a team lists
@@ -63,7 +63,7 @@ constexpr float kNegInf = -__builtin_huge_valf();
 
 struct Plan {
     int32_t cluster;      // CTAs per (token, cache head, part of the group)
-    int32_t shift;        // log2 of that
+    int32_t takers;       // CTAs that write outputs: a power of two
     int32_t group;        // query heads per cache head
     int32_t parts;        // clusters a group is dealt to
     int32_t rows;         // query heads per cluster
@@ -297,6 +297,11 @@ __device__ __forceinline__ void score_blocks(const DecodeArgs &a, const Plan &p,
     }
     const int srows = a.share ? 1 : w.rows;
     if (p.cluster > 1) cluster_wait();
+    // where this lane's sums go: block `sub` of a step's J * BPL, one row
+    const int at = (lane % LPB) / (LPB / NV), row = at % RP;
+    const int sub = at / RP * BPL + lane / LPB;
+    const bool writes = lane % (LPB / NV) == 0 && row < srows;
+    uint32_t *dst = cluster.map_shared_rank(keys, row % p.cluster) + row / p.cluster * a.width + b0 + sub;
     float big = 0.f;
     bool unknown = false;
     for (; base < n; base += kStep) {
@@ -344,13 +349,9 @@ __device__ __forceinline__ void score_blocks(const DecodeArgs &a, const Plan &p,
                     v[j * RP + r] = s;
                 }
             const float s = reduce_exchange<NV, LPB>(v, lane);
-            const int at = (lane % LPB) / (LPB / NV);
-            const int slot = (j0 + at / RP) * BPL + lane / LPB, row = at % RP;
-            const bool good = __shfl_sync(kFull, mine, slot) >= 0;
+            const bool good = __shfl_sync(kFull, mine, j0 * BPL + sub) >= 0;
             unknown |= s != s;
-            if (lane % (LPB / NV) == 0 && row < srows && base + slot < n)
-                cluster.map_shared_rank(keys, row & (p.cluster - 1))[
-                    (row >> p.shift) * a.width + b0 + base + slot] = key_of(good ? s : kNegInf);
+            if (writes && base + j0 * BPL + sub < n) dst[base + j0 * BPL] = key_of(good ? s : kNegInf);
         }
     }
     // a NaN score (from means that are not finite) leaves the bound unknown
@@ -715,7 +716,7 @@ __device__ __forceinline__ void make_items(const DecodeArgs &a, const Plan &p, c
 // infinite or NaN.  Every warp takes keys of the row's own blocks; `sum` has
 // W + 1 rows of D.
 template <int D, int W>
-__device__ __noinline__ void attend_alone(const DecodeArgs &a, const Plan &p, const Job &w,
+__device__ __forceinline__ void attend_alone(const DecodeArgs &a, const Plan &p, const Job &w,
                                           const Fixed &f, int row, float mx, float *sum) {
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -755,7 +756,7 @@ __device__ __noinline__ void attend_alone(const DecodeArgs &a, const Plan &p, co
 }
 
 // Stage 3 and the merge.  `part` is where the cluster leaves this CTA's share
-// of the outputs, [CTA][rows][D / C].
+// of the outputs, [CTA][rows][D / takers].
 template <int D, int NT, int W>
 __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const Job &w, Fixed &f,
                                        float *part, float *po) {
@@ -928,7 +929,7 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
         }
     __syncthreads();
     uint16_t *out = a.out + (int64_t(w.token) * a.q_heads + w.head * p.group + w.row0) * D;
-    const int C = p.cluster, share = D / C;     // channels of each CTA
+    const int C = p.cluster, share = D / p.takers;      // channels of each that writes
     const int shift_c = 31 - __clz(share);
     // a row with no key to attend to is zero
     const auto put = [&](int i, int r, float mx, float ls, float x0, float x1) {
@@ -962,7 +963,7 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
             float *dst = cluster.map_shared_rank(part, c >> shift_c);
             *reinterpret_cast<float2 *>(dst + ((w.rank * w.rows + r) << shift_c) + (c & (share - 1))) =
                 make_float2(x0, x1);
-            if (c < 2 * C) {            // one thread of the row for each CTA
+            if (c < 2 * p.takers) {     // one thread of the row for each
                 Fixed *peer = cluster.map_shared_rank(&f, c / 2);
                 peer->pm[w.rank][r] = mx;
                 peer->pl[w.rank][r] = ls;
@@ -971,6 +972,7 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
     }
     if (C > 1) {
         cluster.sync();
+        if (w.rank >= p.takers) return;
         for (int j = 2 * tid; j < w.rows * share; j += 2 * kThreads) {
             const int r = j >> shift_c, i = r * D + w.rank * share + (j & (share - 1));
             float mx = kNegInf;
@@ -1002,16 +1004,19 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
     }
 }
 
-// Warps of a CTA, and CTAs an SM holds by their registers.  Large CTAs have six
-// warps, two to an SM: a cluster of sixteen takes sixteen SMs of one group, and
-// with one CTA to an SM only seven clusters fit the card at once.  (Sixteen
-// heads' accumulators take twice the registers.)
+// Warps of a CTA, and CTAs an SM holds by their registers (sixteen heads'
+// accumulators take twice the registers).
 constexpr int kWarpsSmall = 4;
-constexpr int warps_large(int nt) { return nt == 1 ? 6 : 8; }
+constexpr int warps_large(int nt) { return nt == 1 ? 12 : 8; }
 constexpr int ctas_per_sm(int d, int nt) { return nt == 2 ? 2 : d == 64 ? 4 : 3; }
 
+// Clusters of 5 to 16 CTAs the card holds with one CTA to an SM (its SMs come
+// in groups of unequal size, and a cluster lies within one).
+constexpr int kFewItems = 28;
+constexpr int8_t kClustersFit[kMaxCluster + 1] = {0, 0, 0, 0, 0, 28, 23, 15, 15, 15, 13, 8, 8, 7, 7, 7, 7};
+
 template <int D, int RP, int NT, int W>
-__global__ void __launch_bounds__(W * 32, W == kWarpsSmall ? ctas_per_sm(D, NT) : W == 6 ? 2 : 1)
+__global__ void __launch_bounds__(W * 32, W == kWarpsSmall ? ctas_per_sm(D, NT) : 1)
     decode_kernel(DecodeArgs a, Plan p) {
     extern __shared__ __align__(16) char smem[];
     constexpr int kThreads = W * 32;
@@ -1137,31 +1142,36 @@ cudaError_t launch_paged_decode(const DecodeArgs &a, cudaStream_t st) {
     p.rows = (p.group + p.parts - 1) / p.parts;
     p.score_rows = a.share ? 1 : p.rows;
     const int64_t items = a.tokens * a.c.heads * p.parts;
-    // Few items: large CTAs, one for each SM, in clusters (one sequence of
-    // 131072 tokens, 8 heads: 35 us; with small ones 38).  Many: small CTAs,
-    // three or four to an SM, so that some load while others select.  Clusters
-    // as large as leave all CTAs on the card at once (52 drafted tokens, 4
-    // heads: 64 us in pairs; 71 in fours, which take two turns; 90 alone).  No
-    // more warps than there are 16-key tiles to attend to.
-    const bool large = items * 8 <= 152;
+    // Few items: large CTAs, one to an SM, in the largest clusters that fit the
+    // card all at once.  Many: small CTAs, three or four to an SM, so that some
+    // load while others select, in clusters as large as leave all CTAs on the
+    // card at once (52 drafted tokens, 4 heads: 64 us in pairs; 71 in fours,
+    // which take two turns; 90 alone).  No more warps than there are 16-key
+    // tiles to attend to.
+    const bool large = items <= kFewItems;
     const int warps = large ? warps_large(p.rows > 8 ? 2 : 1) : kWarpsSmall;
     const int64_t picked = int64_t(p.score_rows) * a.topk;
     const int64_t tiles = (picked < a.width ? picked : a.width) * (a.c.page / 16);
-    p.cluster = 1;
-    while (p.cluster < (large ? kMaxCluster : 8) && p.cluster * warps < tiles &&
-           items * p.cluster * 2 <= 152 * (large ? 1 : ctas_per_sm(a.c.d, p.rows > 8 ? 2 : 1)))
-        p.cluster *= 2;
+    if (large) {
+        p.cluster = kMaxCluster;
+        while (kClustersFit[p.cluster] < items) --p.cluster;
+        while (p.cluster > 1 && (p.cluster - 1) * warps >= tiles) --p.cluster;
+    } else {
+        p.cluster = 1;
+        while (p.cluster < 8 && p.cluster * warps < tiles &&
+               items * p.cluster * 2 <= 152 * ctas_per_sm(a.c.d, p.rows > 8 ? 2 : 1))
+            p.cluster *= 2;
+    }
     const auto kept = [&] {         // scores a CTA holds
         return int64_t((p.score_rows + p.cluster - 1) / p.cluster) * a.width;
     };
     while (kept() > kMaxKeys) p.cluster *= 2;
     if (items * p.cluster > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    p.shift = 0;
-    while ((1 << p.shift) < p.cluster) ++p.shift;
+    p.takers = p.cluster >= 8 ? 8 : p.cluster >= 4 ? 4 : p.cluster >= 2 ? 2 : 1;
     const auto up = [](size_t x) { return (x + 15) / 16 * 16; };
     size_t off = up(offsetof(Fixed, teams) + warps * sizeof(Team));
     p.part_off = int32_t(off);
-    if (p.cluster > 1) off = up(off + size_t(p.rows) * a.c.d * 4);
+    if (p.cluster > 1) off = up(off + size_t(p.cluster) * p.rows * (a.c.d / p.takers) * 4);
     p.main_off = int32_t(off);
     const size_t scores = size_t(kept()) * 4;
     const size_t merge = size_t(warps) * p.rows * (a.c.d + 1) * 4;
