@@ -1,4 +1,5 @@
-"""GB300-native content-dependent block-sparse attention (forward).
+"""GB300-native content-dependent block-sparse attention: forward, backward,
+rotary positions, and decoding over a paged cache.
 
 The compute path is the C-ABI library ``libbsa.so`` (hand-written sm_103a
 CUDA kernels, built in-tree by ``content_dependent_block_gb300._build``).

@@ -32,9 +32,16 @@
 //               softmax per warp, merged over the warps and then over the
 //               cluster, each CTA receiving its share of the outputs.
 // Bound: memory (block means and selected K, V once); with one sequence, the
-// latency of the chain table -> means -> merge -> table -> keys.  m16n8k16
-// mma.sync carries it: 8 or 16 rows against 16 keys is far below a tcgen05
-// tile (128 rows), and the keys arrive at about 23 bytes a clock and SM.
+// latency of the chain table -> means -> k-th best -> keys.  m16n8k16 mma.sync
+// carries it: 8 or 16 rows against 16 keys is far below a tcgen05 tile (128
+// rows), and the keys arrive at about 23 bytes a clock and SM, for which the
+// tensor pipe is busy 5 to 7 % of the time.
+// Measured, device time: 96 sequences up to 32768 tokens, 64 heads over 8
+// sharing selections, d 128, top-32: 157 us, 5.9 TB/s (87 % of a plain copy's
+// rate); 32 such sequences, 32 heads over 8, d 64, top-16, each head for
+// itself: 57 us, 4.6 TB/s (the CTAs run in step, so memory idles while they
+// select: a fifth of a CTA's time); one sequence of 131072 tokens, 64 heads
+// over 8, top-32: 33 us against 11 us of traffic.
 #include <cooperative_groups.h>
 
 #include <atomic>
