@@ -496,7 +496,7 @@ def _here(*tensors) -> int:
     """The current device's stream, all tensors being on that device: pointers
     of another one would be launched on this one's stream."""
     torch = _torch()
-    here = torch.cuda.current_device()
+    here = torch._C._cuda_getDevice()
     for t in tensors:
         if t is not None and t.get_device() != here:
             raise ValueError("tensors must be on the current CUDA device")

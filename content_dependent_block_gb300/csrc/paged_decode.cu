@@ -540,11 +540,13 @@ __device__ __forceinline__ void select_blocks(const DecodeArgs &a, const Plan &p
         const int row = w.rank + k * C;
         const uint32_t *keys = own_keys + k * a.width;
         Team &t = f.teams[team];
-        const Found r = narrow(keys, n, kk, t, me, size, sync);
+        // 32 blocks are one interval (1024 tokens: 10.7 us, narrowed 11.7)
+        const bool tiny = n <= 32;
+        const Found r = tiny ? Found{n, 0, false, 0u} : narrow(keys, n, kk, t, me, size, sync);
         if (me >= 32) continue;     // the next row's syncs come before the scratch is reused
         // t, the kk-th largest: rank r.above + (keys above it in the interval,
         // or equal and before it)
-        const uint32_t x = lane < r.in ? t.near[lane] : 0u;
+        const uint32_t x = lane < r.in ? (tiny ? keys[lane] : t.near[lane]) : 0u;
         int rank = r.above;
         for (int j = 0; j < r.in; ++j) {
             const uint32_t y = __shfl_sync(kFull, x, j);
@@ -553,9 +555,10 @@ __device__ __forceinline__ void select_blocks(const DecodeArgs &a, const Plan &p
         const uint32_t hit = __ballot_sync(kFull, lane < r.in && rank == kk - 1);
         const uint32_t kth = __shfl_sync(kFull, x, hit != 0 ? __ffs(hit) - 1 : 0);
         // |computed - true| <= e: at most 8 + 4 roundings on a path of the sum
-        // (4 + 5 with a lane's four channels), 2^-24 each of sum |q||mean|, which is at most sum |q| times
-        // the largest |mean|; a shared row's q is itself a sum of `group`
-        // terms.  The last unit leaves room for this bound's own roundings.
+        // (4 + 5 with a lane's four channels), 2^-24 each of sum |q||mean|,
+        // which is at most sum |q| times the largest |mean|; a shared row's q
+        // is itself a sum of `group` terms.  The last unit leaves room for
+        // this bound's own roundings.
         const float e = (f.qabs[row] * __uint_as_float(f.kmax)) *
                             (float(13 + (a.share ? p.group : 0)) * 5.9604645e-8f) + 1e-36f;
         uint32_t lo = 0u, hi = kFull;           // unknown: every block is open
@@ -1153,19 +1156,21 @@ cudaError_t launch_paged_decode(const DecodeArgs &a, cudaStream_t st) {
     // card all at once.  Many: small CTAs, three or four to an SM, so that some
     // load while others select, in clusters as large as leave all CTAs on the
     // card at once (52 drafted tokens, 4 heads: 64 us in pairs; 71 in fours,
-    // which take two turns; 90 alone).  No more warps than there are 16-key
-    // tiles to attend to.
+    // which take two turns; 90 alone).  No more warps than have two 16-key tiles
+    // to attend to or sixteen blocks to score (1024 tokens, top-4: one CTA,
+    // 10.7 us; two, 11.1).
     const bool large = items <= kFewItems;
     const int warps = large ? warps_large(p.rows > 8 ? 2 : 1) : kWarpsSmall;
     const int64_t picked = int64_t(p.score_rows) * a.topk;
     const int64_t tiles = (picked < a.width ? picked : a.width) * (a.c.page / 16);
+    const int64_t pairs = (tiles > a.width / 8 ? tiles : a.width / 8) / 2;
     if (large) {
         p.cluster = kMaxCluster;
         while (kClustersFit[p.cluster] < items) --p.cluster;
-        while (p.cluster > 1 && (p.cluster - 1) * warps >= tiles) --p.cluster;
+        while (p.cluster > 1 && (p.cluster - 1) * warps >= pairs) --p.cluster;
     } else {
         p.cluster = 1;
-        while (p.cluster < 8 && p.cluster * warps < tiles &&
+        while (p.cluster < 8 && p.cluster * warps < pairs &&
                items * p.cluster * 2 <= 152 * ctas_per_sm(a.c.d, p.rows > 8 ? 2 : 1))
             p.cluster *= 2;
     }

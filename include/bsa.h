@@ -514,7 +514,9 @@ bsa_status bsa_cache_copy_pages(bsa_cache cache, const int32_t *pairs, int64_t c
  * cache head h / (q_heads / heads) (score = q . kbar, unscaled), keeps its
  * topk best, and attends to their keys j < lens[t].  The selection is that of
  * the scores' exact values for the given kbar (close calls are settled in
- * fp64), ties to the lower block id; a NaN score ranks as -inf.
+ * fp64, one block after another: means that differ by rounding only, in
+ * thousands of blocks, cost milliseconds), ties to the lower block id; a NaN
+ * score ranks as -inf.
  *   q          [tokens][q_heads][d] bf16 (device); q_stride: elements from a
  *              token to the next (multiple of 8, >= q_heads * d).
  *   table      int32 [seqs][table_width] (device), table_width <= 16384.
