@@ -41,7 +41,7 @@
 // rate); 32 such sequences, 32 heads over 8, d 64, top-16, each head for
 // itself: 57 us, 4.6 TB/s (the CTAs run in step, so memory idles while they
 // select: a fifth of a CTA's time); one sequence of 131072 tokens, 64 heads
-// over 8, top-32: 33 us against 11 us of traffic.
+// over 8, top-32: 32 us against 11 us of traffic.
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -268,7 +268,7 @@ __device__ __forceinline__ void score_blocks(const DecodeArgs &a, const Plan &p,
     };
     if (RP == 1 && a.share) {
         float qa = 0.f;
-#pragma unroll 4
+#pragma unroll 8
         for (int g = 0; g < p.group; ++g)
 #pragma unroll
             for (int l = 0; l < L; ++l) {
@@ -283,24 +283,28 @@ __device__ __forceinline__ void score_blocks(const DecodeArgs &a, const Plan &p,
             }
         if (warp == 0) row_sum(qa, 0);
     } else {
+        uint2 raw[RP][L];               // all rows requested before any is used
 #pragma unroll
         for (int r = 0; r < RP; ++r)
-            if (r < w.rows) {
-                float qa = 0.f;
 #pragma unroll
-                for (int l = 0; l < L; ++l) {
-                    const uint2 x =
-                        *reinterpret_cast<const uint2 *>(qt + (w.row0 + r) * D + l * LPB * 4);
-                    const float v[4] = {bf16_low_half(x.x), bf16_high_half(x.x),
-                                        bf16_low_half(x.y), bf16_high_half(x.y)};
+            for (int l = 0; l < L; ++l)
+                raw[r][l] = *reinterpret_cast<const uint2 *>(
+                    qt + (w.row0 + min(r, w.rows - 1)) * D + l * LPB * 4);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        q[r][l][e] = v[e];
-                        qa += fabsf(v[e]);
-                    }
-                }
-                if (r % W == warp) row_sum(qa, r);
+        for (int r = 0; r < RP; ++r) {
+            float qa = 0.f;
+#pragma unroll
+            for (int l = 0; l < L; ++l) {
+                const uint2 x = r < w.rows ? raw[r][l] : make_uint2(0u, 0u);
+                q[r][l][0] = bf16_low_half(x.x);
+                q[r][l][1] = bf16_high_half(x.x);
+                q[r][l][2] = bf16_low_half(x.y);
+                q[r][l][3] = bf16_high_half(x.y);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) qa += fabsf(q[r][l][e]);
             }
+            if (r % W == warp) row_sum(qa, r);
+        }
     }
     const int srows = a.share ? 1 : w.rows;
     if (p.cluster > 1) cluster_wait();
@@ -1120,7 +1124,9 @@ cudaError_t launch(const DecodeArgs &a, const Plan &p, size_t smem, int64_t item
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a, p);
+    e = cudaLaunchKernelEx(&cfg, kernel, a, p);
+    if (e != cudaSuccess) cudaGetLastError();           // reported here, not by the next launch
+    return e;
 }
 
 template <int D, int RP, int NT>
@@ -1155,7 +1161,7 @@ cudaError_t launch_paged_decode(const DecodeArgs &a, cudaStream_t st) {
     // Few items: large CTAs, one to an SM, in the largest clusters that fit the
     // card all at once.  Many: small CTAs, three or four to an SM, so that some
     // load while others select, in clusters as large as leave all CTAs on the
-    // card at once (52 drafted tokens, 4 heads: 64 us in pairs; 71 in fours,
+    // card at once (52 drafted tokens, 4 heads: 62 us in pairs; 70 in fours,
     // which take two turns; 90 alone).  No more warps than have two 16-key tiles
     // to attend to or sixteen blocks to score (1024 tokens, top-4: one CTA,
     // 10.7 us; two, 11.1).
