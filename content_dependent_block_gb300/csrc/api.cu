@@ -808,7 +808,7 @@ static bsa_status rope_impl(const bsa_heads &h, const void *x, const bsa_strides
     if (rot.rot < 2 || rot.rot % 2 != 0 || rot.rot > h.d)
         return fail(BSA_ERR_INVALID_ARG, "rot must be even and in [2, d] (got %d)", rot.rot);
     if (rot.table == nullptr) return fail(BSA_ERR_INVALID_ARG, "rotation table is NULL");
-    if (!aligned(rot.table, 8)) return fail(BSA_ERR_ALIGNMENT, "rotation table is not 8-byte aligned");
+    if (!aligned(rot.table, 16)) return fail(BSA_ERR_ALIGNMENT, "rotation table is not 16-byte aligned");
     if (!std::isfinite(rot.factor)) return fail(BSA_ERR_INVALID_ARG, "factor must be finite");
     if (positions != nullptr && !aligned(positions, 4))
         return fail(BSA_ERR_ALIGNMENT, "positions is not 4-byte aligned");

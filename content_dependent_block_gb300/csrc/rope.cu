@@ -157,23 +157,14 @@ __global__ void __launch_bounds__(kThreads) rope_vec_kernel(RopeArgs a, int32_t 
         o0 = task * V;
         o1 = o0 + a.rot / 2;
     }
-    float c[V], s[V];
-    if (!copied) {
-        const int64_t pos = position_of(a, b, i);
-        const uint64_t *f = a.table + task * V;
-#pragma unroll
-        for (int p = 0; p < V; ++p)
-            if (!kInterleaved || task * V + p < a.rot / 2)
-                turn(__ldg(f + p), pos, a.factor, a.sign, c[p], s[p]);
-    }
     // copied pairs of the task (interleaved): from this one on
     const int stay = kInterleaved ? a.rot / 2 - task * V : V;
     const int32_t h0 = chunk * hpt, h1 = h0 + hpt < a.heads ? h0 + hpt : a.heads;
     const T *x = static_cast<const T *>(a.x) + b * a.xs_b + i * a.xs_n;
     T *out = static_cast<T *>(a.out) + b * a.os_b + i * a.os_n;
     constexpr int U = 4;        // heads in flight
-    for (int32_t h = h0; h < h1; h += U) {
-        uint4 u0[U], u1[U];
+    uint4 u0[U], u1[U];
+    const auto load = [&](int32_t h) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (h + u < h1) {
@@ -181,6 +172,26 @@ __global__ void __launch_bounds__(kThreads) rope_vec_kernel(RopeArgs a, int32_t 
                 u0[u] = *reinterpret_cast<const uint4 *>(row + o0);
                 u1[u] = *reinterpret_cast<const uint4 *>(row + o1);
             }
+    };
+    load(h0);                   // on their way during the trigonometry
+    float c[V], s[V];
+    if (!copied) {
+        const int64_t pos = position_of(a, b, i);
+        const uint64_t *f = a.table + task * V;         // 16-byte aligned
+#pragma unroll
+        for (int p = 0; p < V; p += 2) {
+            // an odd number of pairs: the last one alone, the table ends there
+            ulonglong2 u = make_ulonglong2(0, 0);
+            if (task * V + p + 1 < a.rot / 2)
+                u = __ldg(reinterpret_cast<const ulonglong2 *>(f + p));
+            else if (task * V + p < a.rot / 2)
+                u.x = __ldg(reinterpret_cast<const unsigned long long *>(f + p));
+            turn(u.x, pos, a.factor, a.sign, c[p], s[p]);
+            turn(u.y, pos, a.factor, a.sign, c[p + 1], s[p + 1]);
+        }
+    }
+    for (int32_t h = h0; h < h1; h += U) {
+        if (h > h0) load(h);
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (h + u < h1) {
@@ -235,6 +246,18 @@ __global__ void __launch_bounds__(kThreads) rope_row_kernel(RopeArgs a, int32_t 
     const int32_t vec = w.task, chunk = w.chunk;
     const int64_t i = w.i, b = w.b;
     const int half = a.rot / 2, c0 = vec * V;
+    const int32_t h0 = chunk * hpt;
+    const T *x = static_cast<const T *>(a.x) + b * a.xs_b + i * a.xs_n + c0;
+    T *out = static_cast<T *>(a.out) + b * a.os_b + i * a.os_n + c0;
+    uint4(&buf)[U][32] = rows[threadIdx.x >> 5];
+    uint4 own[U];
+    const auto load = [&](int32_t k) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (k + u < hpt && h0 + k + u < a.heads)
+                own[u] = *reinterpret_cast<const uint4 *>(x + int64_t(h0 + k + u) * a.xs_h);
+    };
+    load(0);                    // on their way during the trigonometry
     float c[V], s[V];
     const int64_t pos = position_of(a, b, i);
 #pragma unroll
@@ -244,16 +267,8 @@ __global__ void __launch_bounds__(kThreads) rope_row_kernel(RopeArgs a, int32_t 
             turn(__ldg(a.table + (first ? c0 + e : c0 + e - half)), pos, a.factor,
                  first ? -a.sign : a.sign, c[e], s[e]);
         }
-    const int32_t h0 = chunk * hpt;
-    const T *x = static_cast<const T *>(a.x) + b * a.xs_b + i * a.xs_n + c0;
-    T *out = static_cast<T *>(a.out) + b * a.os_b + i * a.os_n + c0;
-    uint4(&buf)[U][32] = rows[threadIdx.x >> 5];
     for (int32_t k = 0; k < hpt; k += U) {
-        uint4 own[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (k + u < hpt && h0 + k + u < a.heads)
-                own[u] = *reinterpret_cast<const uint4 *>(x + int64_t(h0 + k + u) * a.xs_h);
+        if (k > 0) load(k);
 #pragma unroll
         for (int u = 0; u < U; ++u) buf[u][lane] = own[u];
         __syncwarp();
@@ -287,6 +302,7 @@ cudaError_t launch(const RopeArgs &a, bool interleaved, cudaStream_t st) {
                        a.batch * a.n * per_row * ((a.heads + hpt - 1) / hpt) < int64_t(152) * 1024))
         hpt /= 2;
     const int32_t chunks = (a.heads + hpt - 1) / hpt;
+    hpt = (a.heads + chunks - 1) / chunks;              // ten heads: five and five
     const int64_t total = a.batch * a.n * per_row * chunks;
     const int64_t blocks = (total + kThreads - 1) / kThreads;
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
