@@ -231,7 +231,8 @@ __global__ void __launch_bounds__(kThreads) rope_vec_kernel(RopeArgs a, int32_t 
 // Halves with any even rot: a channel's partner lies rot / 2 away, at no vector
 // boundary, so rows pass through shared memory.  Thread = (batch, token, chunk
 // of heads, vector), vector fastest: a row belongs to lanes of one warp, which
-// has read all of it before it writes any (out may be x).
+// has read all of it before it writes any (out may be x).  bf16 runs at 45 to
+// 68 % of the copy rate, bound by the 2-byte reads of the partners.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) rope_row_kernel(RopeArgs a, int32_t hpt, int32_t chunks,
                                                             int64_t total) {
