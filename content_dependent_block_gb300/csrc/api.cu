@@ -798,11 +798,12 @@ bsa_status bsa_fine_backward_lse(bsa_shape shape, const void *q, const void *k, 
 static bsa_status rope_impl(const bsa_heads &h, const void *x, const bsa_strides &xs,
                             const int32_t *positions, int64_t first, const bsa_rotation &rot,
                             float sign, void *out, const bsa_strides &os, void *stream) {
-    if (h.batch < 1 || h.n < 1 || h.heads < 1)
-        return fail(BSA_ERR_INVALID_ARG, "batch, n and heads must be >= 1");
+    if (h.batch < 1 || h.n < 0 || h.heads < 1)
+        return fail(BSA_ERR_INVALID_ARG, "batch and heads must be >= 1, n >= 0");
     if (h.d != 64 && h.d != 128) return fail(BSA_ERR_UNSUPPORTED, "d must be 64 or 128 (got %d)", h.d);
     if (h.dtype != BSA_BF16 && h.dtype != BSA_FP32) return fail(BSA_ERR_INVALID_ARG, "bad dtype %d", h.dtype);
     const int64_t most = int64_t(1) << 40;
+    if (h.n == 0) return ok();              // x and out may be empty then
     if (h.n > most || h.batch > most / h.n || h.heads > most / (h.n * h.batch))
         return fail(BSA_ERR_UNSUPPORTED, "batch * heads * n must be <= 2^40");
     if (rot.rot < 2 || rot.rot % 2 != 0 || rot.rot > h.d)

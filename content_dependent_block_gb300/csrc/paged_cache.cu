@@ -11,10 +11,11 @@ namespace {
 constexpr int kThreads = 128;
 
 // Pages a sequence's `n` new tokens can touch is at most floor(n / B) + 2, so
-// sequence s owns the work items [cu[s] / B + 2 s, cu[s + 1] / B + 2 (s + 1)):
-// no item list has to be made, and spare items return at once.
+// sequence s owns the work items [c / B + 2 s, c' / B + 2 (s + 1)), c and c' the
+// tokens before and after its own: no item list has to be made, and spare items
+// return at once.
 __device__ __forceinline__ int64_t first_item(const int32_t *cu, int64_t s, int32_t page) {
-    return int64_t(cu[s] / page) + 2 * s;
+    return (int64_t(cu[s]) - cu[0]) / page + 2 * s;
 }
 
 // One CTA per (touched page, head).  The new rows are copied into the page

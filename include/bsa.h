@@ -428,7 +428,8 @@ bsa_status bsa_rope_table(const double *inv_freq, int32_t count, uint64_t *table
  *   out        may be x itself, with x's strides; otherwise the two must not
  *              overlap.  Rows of out must not overlap (no stride 0); x may be
  *              broadcast.
- * bf16 or fp32; d in {64, 128}; strides multiples of 16 bytes, not negative.
+ * bf16 or fp32; d in {64, 128}; strides multiples of 16 bytes, not negative;
+ * the table 16-byte aligned; n = 0 does nothing.
  * bsa_rope_backward: dx = the gradient with respect to x given dout (the
  * same map with -t; m applies again, the map being linear).
  */
@@ -482,8 +483,8 @@ typedef struct {
  *               (multiples of 8, >= heads * d).  They must not overlap the
  *               cache.
  *   cu_tokens   int32 [seqs + 1] (device): sequence s has the tokens
- *               [cu[s], cu[s + 1]), possibly none; tokens from cu[seqs] on
- *               are ignored.  NULL: tokens / seqs each (it must divide).
+ *               [cu[s], cu[s + 1]), possibly none; tokens before cu[0] and
+ *               from cu[seqs] on are ignored.  NULL: tokens / seqs each (it must divide).
  *   start       int32 [seqs] (device): tokens each sequence holds already.
  *   table       int32 [seqs][table_width] (device).  A page may be listed by
  *               several sequences, but a page that is written to by one only.

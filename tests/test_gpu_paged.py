@@ -90,6 +90,21 @@ def test_append_many_sequences_and_none():
     assert torch.equal(c.k.cpu(), wk) and bsa.device_status() == 0
 
 
+def test_append_tokens_before_the_first_sequence():
+    """cu_tokens need not start at 0: a step's tokens of other sequences lie
+    before and behind."""
+    g = torch.Generator().manual_seed(6)
+    k, v = _randn(g, 12, 2, 16, 64), _randn(g, 12, 2, 16, 64)
+    kbar = _randn(g, 12, 2, 64, dtype=torch.float32)
+    rows = _randn(g, 150, 2, 64)
+    table, start, cu = torch.arange(12).view(3, 4), [0, 15, 3], [83, 100, 101, 140]
+    c = _cache(k, v, kbar)
+    bsa.cache_append(c, rows.cuda(), rows.cuda(), _i32(table), _i32(start), cu_tokens=_i32(cu))
+    wk, wv, wm, tol = ref.append(k, v, kbar, rows, rows, cu, start, table.tolist())
+    assert torch.equal(c.k.cpu(), wk) and torch.equal(c.v.cpu(), wv) and bsa.device_status() == 0
+    ref.assert_within(c.kbar, wm, tol, "means")
+
+
 def test_append_reads_no_row_past_the_filled_ones():
     """Rows behind a sequence's end hold anything; a shorter sequence's means
     are those of its own rows."""
@@ -418,6 +433,25 @@ def test_two_calls_at_once():
     torch.cuda.synchronize()
     for w, runs in zip(want, got):
         assert all(torch.equal(w, x) for x in runs)
+
+
+def test_decode_selects_alike_in_any_batch():
+    """The blocks a token sees do not hang on what it is decoded with: all
+    tokens at once (single CTAs), some, and one (clusters)."""
+    g = torch.Generator().manual_seed(34)
+    lens = torch.randint(1, 9000, (400,), generator=g).tolist()
+    k, v, kbar, _, table = _problem(g, [9000], 8, 2, 64, 16)
+    q = _randn(g, 400, 8, 64)
+    c, seq = _cache(k, v, kbar), _i32([0] * 400)
+    for share in (False, True):
+        call = lambda a, b: bsa.paged_decode(c, q[a:b].cuda(), table.cuda(), _i32(lens[a:b]), 9,
+                                             token_seq=seq[a:b], share_group=share, local_block=False)
+        out, idx = call(0, 400)
+        for a, b in ((0, 1), (17, 18), (100, 120), (200, 333)):
+            some, ids = call(a, b)
+            assert torch.equal(ids, idx[a:b])
+            # other clusters merge in another order: one bf16 step at most
+            assert float((some.float() - out[a:b].float()).abs().max()) <= 2.0 ** -7 * float(out.abs().max())
 
 
 def test_no_tokens():

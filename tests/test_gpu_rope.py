@@ -89,6 +89,11 @@ def test_layouts_strides_and_in_place(rot, inter):
     assert torch.equal(bsa.rope(wide, plan, 3), bsa.rope(wide.contiguous(), plan, 3))
 
 
+def test_no_tokens():
+    x = _x((2, 3, 0, 64), torch.bfloat16)
+    assert bsa.rope(x, bsa.Rope(64)).shape == (2, 3, 0, 64)
+
+
 def test_refused_tensors():
     x = _x((2, 3, 8, 64), torch.bfloat16)
     plan = bsa.Rope(64)
