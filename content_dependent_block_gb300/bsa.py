@@ -185,9 +185,15 @@ def _check(code: int):
         raise BsaError(code, lib().bsa_last_error().decode())
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream():
@@ -492,53 +498,60 @@ class Rope:
         self.rotation = Rotation(self.table.data_ptr(), rot, int(interleaved), attention_factor)
 
 
+# The calls below cost some microseconds on the host against some on the
+# device, so their checks read each attribute once.
 def _here(*tensors) -> int:
     """The current device's stream, all tensors being on that device: pointers
     of another one would be launched on this one's stream."""
-    torch = _torch()
-    here = torch._C._cuda_getDevice()
+    C = _torch()._C
+    here = C._cuda_getDevice()
     for t in tensors:
         if t is not None and t.get_device() != here:
             raise ValueError("tensors must be on the current CUDA device")
-    return torch._C._cuda_getCurrentRawStream(here)
+    return C._cuda_getCurrentRawStream(here)
 
 
 def _i32(t, name: str, shape):
-    if t.dtype != _torch().int32 or t.shape != shape or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not _torch_module.int32 or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous int32 tensor {list(shape)}")
     return t.data_ptr()
 
 
 def _rope(fn, x, rope: Rope, positions, out):
     torch = _torch()
-    dims = x.dim()
-    if dims not in (3, 4) or x.stride(-1) != 1:
+    shape, dtype, xs = x.shape, x.dtype, x.stride()
+    dims = len(shape)
+    if dims not in (3, 4) or xs[-1] != 1:
         raise ValueError("x must be [batch, heads, n, d] or [heads, n, d] with contiguous channels")
-    if x.dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         dt = BF16
-    elif x.dtype == torch.float32:
+    elif dtype is torch.float32:
         dt = FP32
     else:
-        raise TypeError(f"unsupported dtype {x.dtype}")
+        raise TypeError(f"unsupported dtype {dtype}")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape or out.dtype != x.dtype or out.stride(-1) != 1:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    elif out.shape != shape or out.dtype is not dtype or out.stride(-1) != 1:
         raise ValueError("out must have x's shape and dtype and contiguous channels")
-    batch = x.shape[0] if dims == 4 else 1
-    heads, n, d = x.shape[-3:]
-    if isinstance(positions, torch.Tensor):
-        if positions.dim() == 1 and batch != 1:
-            raise TypeError("positions must be [batch, n]")
-        first, pos = 0, _i32(positions, "positions", (batch, n) if positions.dim() == 2 else (n,))
-        stream = _here(x, out, rope.table, positions)
+    os_ = out.stride()
+    if dims == 4:
+        batch, heads, n, d = shape
+        xs, os_ = Strides(xs[0], xs[1], xs[2]), Strides(os_[0], os_[1], os_[2])
     else:
-        first, pos = int(positions), None
-        stream = _here(x, out, rope.table)
-    xs, os_ = x.stride(), out.stride()
-    if dims == 3:
-        xs, os_ = (0, *xs), (0, *os_)
-    _check(fn(Heads(batch, n, heads, d, dt), x.data_ptr(), Strides(*xs[:3]), pos, first,
-              rope.rotation, out.data_ptr(), Strides(*os_[:3]), stream))
+        batch, (heads, n, d) = 1, shape
+        xs, os_ = Strides(0, xs[0], xs[1]), Strides(0, os_[0], os_[1])
+    if isinstance(positions, torch.Tensor):
+        if positions.dim() == 2:
+            pos = _i32(positions, "positions", (batch, n))
+        elif batch == 1:
+            pos = _i32(positions, "positions", (n,))
+        else:
+            raise TypeError("positions must be [batch, n]")
+        first, stream = 0, _here(x, out, rope.table, positions)
+    else:
+        first, pos, stream = int(positions), None, _here(x, out, rope.table)
+    _check(fn(Heads(batch, n, heads, d, dt), x.data_ptr(), xs, pos, first, rope.rotation,
+              out.data_ptr(), os_, stream))
     return out
 
 
@@ -584,10 +597,11 @@ class PagedCache:
 
 def _token_rows(t, name: str, heads: int, d: int) -> int:
     """The stride from a token's rows to the next's."""
-    if t.dim() != 3 or t.dtype != _torch().bfloat16 or t.shape[1] != heads or t.shape[2] != d \
-            or t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+    shape, strides = t.shape, t.stride()
+    if shape[1:] != (heads, d) or t.dtype is not _torch().bfloat16 or strides[2] != 1 \
+            or (heads > 1 and strides[1] != d):
         raise ValueError(f"{name} must be bfloat16 [tokens, {heads}, {d}] with contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else heads * d
+    return strides[0] if shape[0] > 1 else heads * d
 
 
 def cache_append(cache: PagedCache, k, v, table, start, *, cu_tokens=None):
@@ -621,6 +635,10 @@ def copy_pages(cache: PagedCache, pairs):
                                       _here(cache.k, pairs)))
 
 
+_OPTIONS = {(local, share): ctypes.byref(DecodeOptions(local, share))
+            for local in (False, True) for share in (False, True)}
+
+
 def paged_decode(cache: PagedCache, q, table, lens, topk: int, *, token_seq=None,
                  local_block: bool = True, share_group: bool = False, scale: float = 0.0,
                  out=None):
@@ -630,19 +648,18 @@ def paged_decode(cache: PagedCache, q, table, lens, topk: int, *, token_seq=None
     bsa_paged_decode in bsa.h."""
     torch = _torch()
     seqs, width = table.shape
-    tokens, q_heads = q.shape[0], q.shape[1]
+    tokens, q_heads, d = q.shape
     qs = _token_rows(q, "q", q_heads, cache.d)
     seq = None if token_seq is None else _i32(token_seq, "token_seq", (tokens,))
     if out is None:
-        out = torch.empty((tokens, q_heads, cache.d), dtype=q.dtype, device=q.device)
-    elif out.dtype != q.dtype or out.shape != (tokens, q_heads, cache.d) or not out.is_contiguous():
+        out = q.new_empty((tokens, q_heads, d))
+    elif out.dtype is not q.dtype or out.shape != (tokens, q_heads, d) or not out.is_contiguous():
         raise ValueError("out must be contiguous bfloat16 [tokens, q_heads, d]")
-    idx = torch.empty((tokens, cache.heads if share_group else q_heads, topk), dtype=torch.int32,
-                      device=q.device)
+    idx = table.new_empty((tokens, cache.heads if share_group else q_heads, topk))
     _check(lib().bsa_paged_decode(
         cache.struct, q.data_ptr(), qs, tokens, q_heads, _i32(table, "table", (seqs, width)), width,
         seqs, seq, _i32(lens, "lens", (tokens,)), topk,
-        ctypes.byref(DecodeOptions(int(local_block), int(share_group))), scale, out.data_ptr(),
+        _OPTIONS[bool(local_block), bool(share_group)], scale, out.data_ptr(),
         idx.data_ptr(), _here(cache.k, q, table, lens, token_seq, out)))
     return out, idx
 

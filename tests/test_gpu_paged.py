@@ -454,6 +454,24 @@ def test_decode_selects_alike_in_any_batch():
             assert float((some.float() - out[a:b].float()).abs().max()) <= 2.0 ** -7 * float(out.abs().max())
 
 
+def test_c_call_without_options_or_selection():
+    """idx_out NULL: no selection is written; options NULL: no forced block,
+    every head for itself."""
+    g = torch.Generator().manual_seed(35)
+    lens = [700, 31]
+    k, v, kbar, q, table = _problem(g, lens, 4, 2, 64, 16)
+    c, dev, tab, n = _cache(k, v, kbar), q.cuda(), table.cuda(), _i32(lens)
+    out = torch.full((2, 4, 64), 9.0, dtype=BF16, device="cuda")
+    L = bsa.lib()
+    assert L.bsa_paged_decode(c.struct, dev.data_ptr(), 256, 2, 4, tab.data_ptr(), table.shape[1], 2, None,
+                              n.data_ptr(), 3, None, 0.0, out.data_ptr(), None,
+                              torch.cuda.current_stream().cuda_stream) == 0
+    want, tol, _ = ref.decode(k, v, kbar, q, table, lens, 3, local=False)
+    ref.assert_within(out, want, tol, "decode")
+    same, _ = bsa.paged_decode(c, dev, tab, n, 3, local_block=False)
+    assert torch.equal(out, same)
+
+
 def test_no_tokens():
     c = bsa.PagedCache.empty(4, 2, 16, 64)
     q = torch.zeros(0, 4, 64, dtype=BF16, device="cuda")
