@@ -2,13 +2,13 @@
 // launch sequence of every entry point declared in include/bsa.h.
 #include <algorithm>
 #include <cmath>
-#include <cstdarg>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
 #include <new>
 
 #include "bsa.h"
+#include "bsa_errors.h"
 #include "bsa_internal.h"
 
 namespace {
@@ -18,18 +18,8 @@ constexpr int kMaxDevices = 64;
 
 thread_local char g_last_error[256] = "";
 
-bsa_status fail(bsa_status code, const char *fmt, ...) {
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
-    va_end(ap);
-    return code;
-}
-
-bsa_status ok() {
-    g_last_error[0] = '\0';
-    return BSA_OK;
-}
+using bsa::fail;
+using bsa::ok;
 
 // Device status word: first kernel-detected error since the last read.
 __device__ int32_t g_device_status = 0;

@@ -1,5 +1,5 @@
-// One-line error reasons for entry points outside api.cu; no CUDA headers, so
-// that host-only units can include it.
+// One-line error reasons of the entry points; no CUDA headers, so that
+// host-only units can include it.
 #pragma once
 
 #include <cstdarg>

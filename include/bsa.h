@@ -21,9 +21,11 @@
  *   - Tensors Q, K, V, O are [bh][n][d] row-major (d fastest), contiguous,
  *     element type given by bsa_shape.dtype.  bh = batch * heads.
  *   - Every tensor pointer is a DEVICE pointer unless the parameter says
- *     host.  Device pointers must be 16-byte aligned; workspaces 256-byte.
- *   - The caller owns every buffer.  The library never allocates memory and
- *     keeps no per-call state; calls only enqueue work on `stream` (a
+ *     host.  Device pointers must be 16-byte aligned (int32 arrays 4-byte);
+ *     workspaces 256-byte.
+ *   - The caller owns every buffer.  The library never allocates device
+ *     memory and keeps no per-call state (handles -- graphs, page managers --
+ *     hold host memory until destroyed); calls only enqueue work on `stream` (a
  *     cudaStream_t passed as void*, NULL = legacy default stream) and return
  *     at once.  Results are ready when the stream reaches that point.
  *   - Argument errors are detected on the host and returned synchronously;
@@ -32,8 +34,6 @@
  *     bounded wait that ran out) never trap: the kernel skips the offending
  *     work, records the first such code in a device status word and
  *     returns.  bsa_get_device_status() reads and clears that word.
- *   - The first call of an entry point on a device loads its kernels; make
- *     it before capturing a stream.
  *   - Supported: d in {64, 128}; key_block B in {16, 32, 64, 128};
  *     dtype bf16 everywhere, fp32 for the fine stage and the rotary
  *     positions.
@@ -53,7 +53,8 @@ typedef enum {
     BSA_ERR_INVALID_ARG = 1,   /* null pointer, bad size, bad enum value      */
     BSA_ERR_UNSUPPORTED = 2,   /* valid request outside the supported set     */
     BSA_ERR_BAD_INDEX = 3,     /* (device) a listed block id outside [0, nb)  */
-    BSA_ERR_WORKSPACE = 4,     /* workspace null or smaller than required     */
+    BSA_ERR_WORKSPACE = 4,     /* workspace null or smaller than required;
+                                  page pool, table or pair array too small    */
     BSA_ERR_CUDA = 5,          /* a CUDA runtime call failed                  */
     BSA_ERR_TIMEOUT = 6,       /* (device) a bounded barrier wait ran out     */
     BSA_ERR_ALIGNMENT = 7      /* pointer not 16-byte (workspace: 256) aligned */
