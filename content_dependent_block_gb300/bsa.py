@@ -652,10 +652,11 @@ def paged_decode(cache: PagedCache, q, table, lens, topk: int, *, token_seq=None
     qs = _token_rows(q, "q", q_heads, cache.d)
     seq = None if token_seq is None else _i32(token_seq, "token_seq", (tokens,))
     if out is None:
-        out = q.new_empty((tokens, q_heads, d))
+        out = torch.empty((tokens, q_heads, d), dtype=q.dtype, device=q.device)
     elif out.dtype is not q.dtype or out.shape != (tokens, q_heads, d) or not out.is_contiguous():
         raise ValueError("out must be contiguous bfloat16 [tokens, q_heads, d]")
-    idx = table.new_empty((tokens, cache.heads if share_group else q_heads, topk))
+    idx = torch.empty((tokens, cache.heads if share_group else q_heads, topk), dtype=torch.int32,
+                      device=q.device)
     _check(lib().bsa_paged_decode(
         cache.struct, q.data_ptr(), qs, tokens, q_heads, _i32(table, "table", (seqs, width)), width,
         seqs, seq, _i32(lens, "lens", (tokens,)), topk,
