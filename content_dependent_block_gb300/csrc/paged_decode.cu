@@ -44,6 +44,7 @@
 // over 8, top-32: 32 us against 11 us of traffic.
 #include <cooperative_groups.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstddef>
 
@@ -725,9 +726,10 @@ __device__ __forceinline__ void make_items(const DecodeArgs &a, const Plan &p, c
     __syncthreads();
 }
 
-// A row whose output is not finite, again and alone: the shared tiles multiply
-// a masked key's weight 0 with its value, which must not count where that is
-// infinite or NaN.  Every warp takes keys of the row's own blocks; `sum` has
+// A row whose output is not finite, again and alone: the tiles multiply a
+// masked key's weight 0, or the remainder of a weight, which may be 0 or below,
+// with the key's value, which must not count where that is infinite or NaN.
+// Every warp takes keys of the row's own blocks; `sum` has
 // W + 1 rows of D.
 template <int D, int W>
 __device__ __forceinline__ void attend_alone(const DecodeArgs &a, const Plan &p, const Job &w,
@@ -858,7 +860,7 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
         }
         unit = find(unit + step);
         if (unit < units) load_k();     // in flight during the softmax and P V
-        uint32_t b0[NT], b1[NT];
+        uint32_t b0[NT], b1[NT], r0[NT], r1[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             float corr[2];
@@ -891,10 +893,13 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
                     o[t][i][3] *= corr[1];
                 }
             }
-            // P rounds to bf16 for the product (as in the block-major fine
-            // stage); its sum l stays fp32
-            b0[t] = transpose_8x8(pack_bf16x2(s[t][0], s[t][1]));
-            b1[t] = transpose_8x8(pack_bf16x2(s[t][2], s[t][3]));
+            // P for the product is its bf16 value and what that leaves, again
+            // in bf16: off by 2^-18 of p at most (of one bf16 value, 2^-9)
+            const uint32_t p0 = pack_bf16x2(s[t][0], s[t][1]), p1 = pack_bf16x2(s[t][2], s[t][3]);
+            b0[t] = transpose_8x8(p0);
+            b1[t] = transpose_8x8(p1);
+            r0[t] = transpose_8x8(pack_bf16x2(s[t][0] - bf16_low_half(p0), s[t][1] - bf16_high_half(p0)));
+            r1[t] = transpose_8x8(pack_bf16x2(s[t][2] - bf16_low_half(p1), s[t][3] - bf16_high_half(p1)));
         }
         if (now_valid < 16) {
             // rows past the end hold anything: 0 * NaN must not reach O
@@ -914,7 +919,10 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
                 const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
                 const uint32_t a2 = __byte_perm(w2, w3, 0x5410), a3 = __byte_perm(w2, w3, 0x7632);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) mma_bf16(o[t][g * 4 + j], a0, a1, a2, a3, b0[t], b1[t]);
+                for (int t = 0; t < NT; ++t) {
+                    mma_bf16(o[t][g * 4 + j], a0, a1, a2, a3, b0[t], b1[t]);
+                    mma_bf16(o[t][g * 4 + j], a0, a1, a2, a3, r0[t], r1[t]);
+                }
             }
         if (unit < units) load_v(row0);
     }
@@ -951,7 +959,8 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
         x0 *= inv;
         x1 *= inv;
         *reinterpret_cast<uint32_t *>(out + i) = pack_bf16x2(x0, x1);
-        if (!(fabsf(x0) < -kNegInf && fabsf(x1) < -kNegInf)) {
+        // a sum that is not a number comes from the row's own scores
+        if (ls == ls && !(fabsf(x0) < -kNegInf && fabsf(x1) < -kNegInf)) {
             f.redo_m[r] = mx;
             f.redo_inv[r] = inv;
             atomicOr(&f.redo, 1u << r);
@@ -1006,8 +1015,7 @@ __device__ __forceinline__ void attend(const DecodeArgs &a, const Plan &p, const
         }
     }
     __syncthreads();
-    // one list for all rows has no masked key
-    if (f.redo == 0u || a.share || w.rows == 1) return;
+    if (f.redo == 0u) return;
     for (int r = 0; r < w.rows; ++r) {
         if (!(f.redo >> r & 1u)) continue;
         attend_alone<D, W>(a, p, w, f, r, f.redo_m[r], po);
@@ -1192,8 +1200,10 @@ cudaError_t launch_paged_decode(const DecodeArgs &a, cudaStream_t st) {
     if (p.cluster > 1) off = up(off + size_t(p.cluster) * p.rows * (a.c.d / p.takers) * 4);
     p.main_off = int32_t(off);
     const size_t scores = size_t(kept()) * 4;
+    // the warps' outputs, or the W + 1 rows of a row that is attended to alone
     const size_t merge = size_t(warps) * p.rows * (a.c.d + 1) * 4;
-    const size_t smem = off + up(scores > merge ? scores : merge);
+    const size_t alone = size_t(warps + 1) * a.c.d * 4;
+    const size_t smem = off + up(std::max({scores, merge, alone}));
     return a.c.d == 64 ? dispatch<64>(a, p, large, smem, items, st)
                        : dispatch<128>(a, p, large, smem, items, st);
 }

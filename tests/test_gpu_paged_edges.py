@@ -1,0 +1,93 @@
+"""The paged cache's operators on the GPU where the other tests do not go: the
+precision of the weights, infinite values under one selection, forks."""
+import pytest
+import torch
+
+from content_dependent_block_gb300 import _build, bsa
+from tests import paged_reference as ref
+from tests.test_gpu_paged import _cache, _i32, _problem
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    _build.build()
+
+
+@pytest.fixture(autouse=True)
+def _clean_status():
+    bsa.device_status()
+    yield
+    torch.cuda.synchronize()
+
+
+# ------------------------------------------------------- decode: precision
+def half_step(y):
+    """Half of the distance between the bf16 numbers around |y| (normal range)."""
+    return torch.exp2(torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -120))) - 8)
+
+
+def narrow_bounds(k, v, q, table, lens, share, scale):
+    """(out, tol) in fp64 of tokens that see all their blocks.  The weights'
+    rounding is not among what tol allows but for 2^-17 (a bf16 value and the
+    bf16 remainder of it leave 2^-18): the scores' roundings, exponentials and
+    sums as in the decode reference, and the output's to the nearest bf16."""
+    hkv, page, d = k.shape[1:]
+    g = q.shape[1] // hkv
+    out = torch.zeros(q.shape, dtype=torch.float64)
+    tol = torch.zeros_like(out)
+    for t, n in enumerate(lens):
+        for h in range(hkv):
+            pages = table[t, :-(-n // page)].long()
+            kk, vv = (x[pages, h].reshape(-1, d)[:n].double() for x in (k, v))
+            for r in range(h * g, (h + 1) * g):
+                qd = q[t, r].double()
+                w = torch.softmax(kk @ qd * scale, 0)
+                out[t, r] = w @ vv
+                slip = float((kk.abs() @ qd.abs()).max()) * scale * (d + 2) * 2.0 ** -24
+                rel = 2.0 ** -17 + 2 * slip + 2.0 ** -20 + 2 * n * 2.0 ** -24
+                off = rel * (w @ vv.abs())
+                tol[t, r] = off + half_step(out[t, r].abs() + off)
+    return out, tol
+
+
+@pytest.mark.parametrize("hq,hkv,d,page", [(1, 1, 64, 16), (8, 2, 128, 16), (16, 1, 64, 64), (6, 1, 128, 128),
+                                           (48, 4, 128, 32)])
+@pytest.mark.parametrize("share", [False, True])
+def test_decode_weights_keep_more_than_bf16(hq, hkv, d, page, share):
+    """One rounding, to the output's type, is what the result is off by."""
+    g = torch.Generator().manual_seed(hq + d + page)
+    lens = [2, 3, 7, 15, page + 1, 3 * page - 1] * 4
+    k, v, kbar, q, table = _problem(g, lens, hq, hkv, d, page)
+    want, tol = narrow_bounds(k, v, q, table, lens, share, d ** -0.5)
+    out, _ = bsa.paged_decode(_cache(k, v, kbar), q.cuda(), table.cuda(), _i32(lens), 32, share_group=share)
+    ref.assert_within(out, want, tol, "decode")
+
+
+@pytest.mark.parametrize("hq,share", [(1, False), (1, True), (4, True), (16, True), (3, False)])
+@pytest.mark.parametrize("seqs", [1, 40])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf")])
+def test_decode_infinite_values_of_selected_blocks(hq, share, seqs, value):
+    """An infinite value of the block that every head selects: its channel is
+    that infinity, the other channels and tokens are finite."""
+    g = torch.Generator().manual_seed(hq + seqs)
+    lens = [30 * 16 + 9] * seqs
+    k, v, kbar, q, table = _problem(g, lens, hq, 1, 64, 16)
+    v = torch.where(torch.isfinite(v), v, 0)
+    clean = v.clone()
+    hit = [s for s in range(seqs) if s % 3 == 0]
+    for s in hit:
+        v[table[s, 30], 0, 4, 11] = value                   # the last block, always selected
+    want, tol, widx = ref.decode(k, clean, kbar, q, table, lens, 4, share=share)
+    out, idx = bsa.paged_decode(_cache(k, v, kbar), q.cuda(), table.cuda(), _i32(lens), 4, share_group=share)
+    out = out.cpu()
+    assert torch.equal(idx.cpu(), widx)
+    rest = [c for c in range(64) if c != 11]
+    ref.assert_within(out[..., rest], want[..., rest], tol[..., rest], "the other channels")
+    for s in range(seqs):
+        if s in hit:
+            assert (out[s, :, 11] == value).all()
+        else:
+            ref.assert_within(out[s, :, 11], want[s, :, 11], tol[s, :, 11], "the other tokens")
+    assert bsa.device_status() == 0
