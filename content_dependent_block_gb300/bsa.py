@@ -669,7 +669,10 @@ class PageTable:
     """Which sequence owns which page (host side, bsa_pages_* in bsa.h):
     ``reserve`` room, ``fork`` with copy on write, ``truncate`` or ``free``,
     ``compact``.  ``take_copies`` and ``compact`` return int32 [count, 2]
-    arrays for ``copy_pages``; run the former's before the next append."""
+    arrays for ``copy_pages``; run the former's before the next append.
+    A step reserves, runs the copies, and appends what it reserved; fork
+    before the reserves or after the append (``take_copies`` refuses copies
+    that would miss tokens, see bsa_pages_take_copies in bsa.h)."""
 
     def __init__(self, num_pages: int, page: int, max_seqs: int, width: int):
         self.num_pages, self.max_seqs, self.width = num_pages, max_seqs, width

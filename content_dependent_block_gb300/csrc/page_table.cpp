@@ -6,6 +6,13 @@
 // page a queued copy reads is held by the queue (it cannot become free and be
 // given away), and a copy from a page that is itself still to be written
 // reads that page's source instead.
+//
+// Copies run before the appends of their step.  So one that reads rows which
+// were reserved in the same step would miss them: a sequence is forked after
+// its reserve, and one of the two grows.  The manager does not see the appends;
+// rows count as written once a later call handed out the copies or the tables
+// they are appended by, and until then such a copy is not handed out.
+#include <algorithm>
 #include <cstdint>
 #include <exception>
 #include <vector>
@@ -20,9 +27,16 @@ struct bsa_pages_s {
     };
     struct Copy {
         int32_t from, to;
+        uint64_t step;               // reads rows reserved in it; 0: none
+    };
+    struct Fresh {
+        uint64_t step = 0;
+        int32_t row = 0;
     };
     int32_t page = 0, width = 0;
+    uint64_t step = 1;               // ends when copies or tables are handed out
     std::vector<int32_t> refs;       // holders of each page
+    std::vector<Fresh> fresh;        // of each page: lowest row reserved in a step
     std::vector<int32_t> free_list;  // taken from the back
     std::vector<Seq> seqs;
     std::vector<Copy> copies;
@@ -31,6 +45,9 @@ struct bsa_pages_s {
     void release(int32_t p) {
         if (--refs[p] > 0) return;
         free_list.push_back(p);
+    }
+    int32_t fresh_row(int32_t p) const {            // rows from it on are not written yet
+        return fresh[size_t(p)].step == step ? fresh[size_t(p)].row : page;
     }
     void drop(int32_t p) {           // a sequence lets go of its page
         if (refs[p] == 1)
@@ -75,6 +92,7 @@ bsa_status bsa_pages_create(int64_t num_pages, int32_t page, int32_t max_seqs,
             p->page = page;
             p->width = table_width;
             p->refs.assign(size_t(num_pages), 0);
+            p->fresh.resize(size_t(num_pages));
             p->free_list.reserve(size_t(num_pages));
             for (int64_t i = num_pages; i-- > 0;) p->free_list.push_back(int32_t(i));
             p->seqs.resize(size_t(max_seqs));
@@ -123,18 +141,23 @@ bsa_status bsa_pages_reserve(bsa_pages pages, int32_t seq, int64_t tokens) {
         const int32_t p = pages->free_list.back();
         pages->free_list.pop_back();
         pages->refs[size_t(p)] = 1;
+        pages->fresh[size_t(p)] = {pages->step, 0};
         return p;
     };
+    const int32_t rows = int32_t(s.length % page);      // of the last page, if partly filled
+    int32_t unwritten = rows;
+    if (rows != 0) unwritten = std::min(rows, pages->fresh_row(s.pages.back()));
     if (split) {
         const int32_t old = s.pages.back(), p = take();
         int32_t from = old;
         for (const auto &c : pages->copies)
             if (c.to == old) from = c.from;     // still to be written itself
-        pages->copies.push_back({from, p});
+        pages->copies.push_back({from, p, unwritten < rows ? pages->step : 0});
         ++pages->refs[size_t(from)];            // held until the copy is taken
         s.pages.back() = p;
         pages->drop(old);
     }
+    if (rows != 0) pages->fresh[size_t(s.pages.back())] = {pages->step, unwritten};
     while (s.pages.size() < want) s.pages.push_back(take());
     s.length += tokens;
     return ok();
@@ -179,6 +202,13 @@ bsa_status bsa_pages_take_copies(bsa_pages pages, int32_t *pairs, int64_t capaci
     if (pairs == nullptr) return ok();
     if (capacity < *count)
         return fail(BSA_ERR_WORKSPACE, "%lld copies are queued", (long long)*count);
+    for (const auto &c : pages->copies)
+        if (c.step == pages->step)
+            return fail(BSA_ERR_INVALID_ARG,
+                        "the copy of page %d to %d would miss tokens reserved since the last "
+                        "take_copies or tables: append them first and call tables, or free the fork",
+                        c.from, c.to);
+    ++pages->step;
     for (const auto &c : pages->copies) {
         *pairs++ = c.from;
         *pairs++ = c.to;
@@ -215,6 +245,7 @@ bsa_status bsa_pages_compact(bsa_pages pages, int32_t *pairs, int64_t capacity, 
         *pairs++ = int32_t(hole);
         refs[size_t(hole)] = refs[size_t(p)];
         refs[size_t(p)] = 0;
+        pages->fresh[size_t(hole)] = pages->fresh[size_t(p)];
         at[size_t(p - used)] = int32_t(hole);
     }
     for (auto &s : pages->seqs)
@@ -227,6 +258,7 @@ bsa_status bsa_pages_compact(bsa_pages pages, int32_t *pairs, int64_t capacity, 
 
 bsa_status bsa_pages_tables(bsa_pages pages, int32_t *table, int32_t *lengths) {
     if (pages == nullptr) return fail(BSA_ERR_INVALID_ARG, "pages is NULL");
+    if (table != nullptr || lengths != nullptr) ++pages->step;
     for (size_t s = 0; s < pages->seqs.size(); ++s) {
         const auto &q = pages->seqs[s];
         if (table != nullptr) {

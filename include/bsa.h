@@ -567,7 +567,9 @@ bsa_status bsa_paged_decode(bsa_cache cache, const void *q, int64_t q_stride, in
  *               All or nothing: BSA_ERR_WORKSPACE when the pool or the table
  *               is too small.
  *   fork        the empty sequence `to` gets all of `from`'s tokens, sharing
- *               the pages.
+ *               the pages.  Tokens that are reserved but not appended yet come
+ *               with the shared pages once they are appended to `from`; if
+ *               one of the two grows before that, see take_copies.
  *   truncate    keeps the first `length` tokens; pages nobody holds any more
  *               become free (length 0: all of them).
  *   take_copies hands out the queued copies, pairs HOST int32 [capacity][2],
@@ -576,6 +578,13 @@ bsa_status bsa_paged_decode(bsa_cache cache, const void *q, int64_t q_stride, in
  *               *count is written.  A page that a queued copy reads is not
  *               given away until then.  BSA_ERR_WORKSPACE when capacity is
  *               too small (nothing is taken).
+ *               A copy brings the tokens that are in the page when it runs.
+ *               BSA_ERR_INVALID_ARG, and nothing is taken, when a sequence
+ *               was forked and grew after tokens were reserved that no
+ *               take_copies or tables has followed: its copy would miss them.
+ *               Free the fork, and make it again after the append.  A call of
+ *               tables says that they are appended by now, or will be to
+ *               every sequence that has them, and lifts the refusal.
  *   compact     moves the pages in use to the lowest ids; pairs as above, at
  *               most num_pages / 2 of them.  Not while copies are queued
  *               (BSA_ERR_INVALID_ARG).
