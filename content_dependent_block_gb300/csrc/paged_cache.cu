@@ -41,6 +41,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, int64_t 
         lo = seq * n_each;
         hi = lo + n_each;
     } else {
+        // Where cu falls, the search below may pass over sequences (and over the
+        // pages of others), so each is looked at here; the grid has more
+        // threads than there are sequences.
+        const int64_t mine = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+        if (head == 0 && mine < a.seqs) {
+            const int32_t c0 = a.cu[mine], c1 = a.cu[mine + 1];
+            if (c0 < 0 || c1 < c0 || c1 > a.tokens) report_status(a.status, kStatusInvalidArg);
+        }
         // the last sequence whose items start at or before this one: 32-way
         // search, every lane probing one sequence
         int64_t s0 = 0, s1 = a.seqs;        // in [s0, s1)
@@ -58,10 +66,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, int64_t 
         item = int64_t(blockIdx.x) - first_item(a.cu, seq, page);
         lo = a.cu[seq];
         hi = a.cu[seq + 1];
-        if (lo < 0 || hi < lo || hi > a.tokens || item < 0) {
-            if (threadIdx.x == 0) report_status(a.status, kStatusInvalidArg);
-            return;
-        }
+        if (lo < 0 || hi < lo || hi > a.tokens || item < 0) return;
     }
     if (hi == lo) return;
     const int64_t start = a.start[seq];

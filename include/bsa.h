@@ -492,7 +492,9 @@ typedef struct {
  * A sequence whose new tokens do not fit its table (or whose cu_tokens or
  * start make no sense) is skipped and reported as BSA_ERR_INVALID_ARG
  * through bsa_get_device_status(), a page outside [0, num_pages) is skipped
- * and reported as BSA_ERR_BAD_INDEX.
+ * and reported as BSA_ERR_BAD_INDEX.  Where cu_tokens fall or leave [0,
+ * tokens], which is always reported, the other sequences may get only some of
+ * their pages' tokens.
  */
 bsa_status bsa_cache_append(bsa_cache cache, const void *k, int64_t k_stride, const void *v,
                             int64_t v_stride, int64_t tokens, int64_t seqs,

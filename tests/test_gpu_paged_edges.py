@@ -5,7 +5,7 @@ import torch
 
 from content_dependent_block_gb300 import _build, bsa
 from tests import paged_reference as ref
-from tests.test_gpu_paged import _cache, _i32, _problem
+from tests.test_gpu_paged import _cache, _i32, _problem, _randn
 
 pytestmark = pytest.mark.gpu
 
@@ -91,3 +91,51 @@ def test_decode_infinite_values_of_selected_blocks(hq, share, seqs, value):
         else:
             ref.assert_within(out[s, :, 11], want[s, :, 11], tol[s, :, 11], "the other tokens")
     assert bsa.device_status() == 0
+
+
+# --------------------------------------------------------- append: cu_tokens
+@pytest.mark.parametrize("cu,start", [
+    ([0, 64, 0, 64], [5, 0, 0]), ([0, 1000, 10, 20], [0, 64, 4]), ([0, 2, 1, 6], [0, 14, 3]),
+    ([0, 500, 499, 1000], [3, 0, 16]), ([-1, 2, 4, 6], [0, 0, 0]), ([0, 2, 4, 1001], [0, 0, 0]),
+    ([0, 2000, 2005, 1000], [0, 0, 0]), ([0, 1 << 30, -(1 << 30), 1000], [0, 0, 0]),
+    ([1000, 0, 1000, 0], [0, 0, 0]), ([0, 3, 3, -1], [1, 2, 3]),
+])
+def test_append_reports_cu_tokens_that_make_no_sense(cu, start):
+    """Reported wherever they are; a row that is written is its sequence's own,
+    and a sequence with impossible bounds writes none."""
+    g = torch.Generator().manual_seed(50)
+    seqs, width, page, tokens = 3, 70, 16, 1000
+    k, v = (_randn(g, seqs * width, 1, page, 64) for _ in range(2))
+    rows = _randn(g, tokens, 2, 64)
+    table = torch.arange(seqs * width).view(seqs, width)
+    c, on = _cache(k, v, torch.zeros(seqs * width, 1, 64)), rows.cuda()
+    bsa.cache_append(c, on[:, :1], on[:, 1:], table.int().cuda(), _i32(start), cu_tokens=_i32(cu))
+    assert bsa.device_status() == 1
+    for s in range(seqs):
+        lo, hi = cu[s], cu[s + 1]
+        for got, was, new in ((c.k, k, rows[:, 0]), (c.v, v, rows[:, 1])):
+            a = got.cpu()[s * width:(s + 1) * width, 0].reshape(-1, 64)
+            b = was[s * width:(s + 1) * width, 0].reshape(-1, 64).clone()
+            moved = (a != b).any(1)
+            if 0 <= lo <= hi <= tokens:
+                at = slice(start[s], start[s] + hi - lo)
+                b[at] = torch.where(moved[at, None], new[lo:hi], b[at])
+            assert torch.equal(a, b)
+
+
+def test_append_many_sequences_report_one_bad_bound():
+    """One fall among thousands of sequences that get a token each or none."""
+    g = torch.Generator().manual_seed(51)
+    seqs = 5000
+    for at in (0, 1, 127, 128, 2500, seqs - 1):
+        cu = (torch.arange(seqs + 1) // 3).int()
+        cu[at + 1:] -= 1
+        if at == seqs - 1:
+            cu[seqs] = cu[seqs - 1] - 1
+        cu = torch.where(torch.arange(seqs + 1) == 0, 0, cu).int()
+        falls = bool((cu.diff() < 0).any()) or bool((cu < 0).any())
+        rows = _randn(g, int(seqs // 3) + 1, 1, 64).cuda()
+        c = bsa.PagedCache.empty(seqs, 1, 16, 64)
+        bsa.cache_append(c, rows, rows, torch.arange(seqs, dtype=torch.int32, device="cuda")[:, None],
+                         _i32([0] * seqs), cu_tokens=cu.cuda())
+        assert (bsa.device_status() == 1) == falls, at
