@@ -13,8 +13,10 @@
 // bits are split into the nearest quarter turn and a rest of at most an eighth
 // of a turn either way; sine and cosine of the rest are their Taylor series
 // (to x^11 and x^10: the terms left out are below 2^-29 and 2^-28 of the
-// result).  The angle is off by 2^-25 of the rest and 2^-32 of a turn, at any
-// position.
+// result).  The angle is off by 2^-25 of the rest, by 2^-32 of a turn, and by the
+// position times the rounding of the table, which comes from fp64 frequencies:
+// at most 2^-52 of all the p f / 2 pi turns (f = 1: 2^-31 of a turn at position
+// 2^23, 2^-23 at 2^31).
 //
 // HBM-bound: x is read once and out written once (2 x 32 heads x 32768 x 128
 // bf16: 161 us, 6.7 TB/s, 98 % of a plain copy's rate).  A thread owns V pairs

@@ -382,8 +382,10 @@ bsa_status bsa_forward_noalloc(bsa_shape shape, const void *q, const void *k,
  * t = p * f_i:
  *   x_a' = m (x_a cos t - x_b sin t),  x_b' = m (x_b cos t + x_a sin t),
  * with (a, b) = (i, i + rot/2), or (2i, 2i + 1) when interleaved; channels
- * from rot on are copied.  Angles are exact in the position (below), the
- * rotation is computed in fp32 and rounded once.
+ * from rot on are copied.  Products of a position and the
+ * table (below) are exact modulo one turn, so an angle is off by fp32 rounding
+ * and by 2^-52 of p f, the fp64 frequency's; the rotation is computed in fp32
+ * and rounded once.
  *
  * The frequencies f_i are made on the host, in two steps so that a caller
  * can put its own in between:
@@ -423,7 +425,8 @@ bsa_status bsa_rope_table(const double *inv_freq, int32_t count, uint64_t *table
  * the d channels of a row contiguous), so that q and k can be rotated where a
  * projection left them and come out in the layout bsa_forward takes.
  *   positions  int32 [batch][n] (device), or NULL: token i is at first + i.
- *              Any int32 value, negative ones too.
+ *              Any int32 value, negative ones too.  (first may lie beyond, at
+ *              2^-52 of p f an angle means nothing from about 2^50 on.)
  *   rotation   table (DEVICE uint64 [rot/2], from bsa_rope_table), rot even
  *              and in [2, d], layout, and the factor m on cos and sin.
  *   out        may be x itself, with x's strides; otherwise the two must not
