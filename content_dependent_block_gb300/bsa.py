@@ -511,6 +511,12 @@ def _here(*tensors) -> int:
     return C._cuda_getCurrentRawStream(here)
 
 
+def _written(*tensors):
+    """A tensor of the caller's is written through its pointer: autograd, which
+    does not see that, is to refuse what it saved of it."""
+    _torch_module.autograd.graph.increment_version(tensors)
+
+
 def _i32(t, name: str, shape):
     if t.shape != shape or t.dtype is not _torch_module.int32 or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous int32 tensor {list(shape)}")
@@ -533,6 +539,9 @@ def _rope(fn, x, rope: Rope, positions, out):
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
     elif out.shape != shape or out.dtype is not dtype or out.stride(-1) != 1:
         raise ValueError("out must have x's shape and dtype and contiguous channels")
+    if torch.is_grad_enabled() and (x.requires_grad or out.requires_grad):
+        raise ValueError("rope and rope_backward record no history: call them under no_grad or in "
+                         "the forward and backward of an autograd function")
     os_ = out.stride()
     if dims == 4:
         batch, heads, n, d = shape
@@ -552,6 +561,7 @@ def _rope(fn, x, rope: Rope, positions, out):
         first, pos, stream = int(positions), None, _here(x, out, rope.table)
     _check(fn(Heads(batch, n, heads, d, dt), x.data_ptr(), xs, pos, first, rope.rotation,
               out.data_ptr(), os_, stream))
+    _written(out)
     return out
 
 
@@ -559,7 +569,8 @@ def rope(x, rope: Rope, positions=0, *, out=None):
     """Rotated x: [batch, heads, n, d] (or [heads, n, d]), any strides with
     contiguous channels.  ``positions``: the first token's position, or an
     int32 device tensor [batch, n].  ``out`` may be x itself; by default a
-    contiguous tensor, the layout ``forward`` takes."""
+    contiguous tensor, the layout ``forward`` takes.  Autograd does not record
+    it: ``rope_backward`` is its gradient."""
     return _rope(lib().bsa_rope, x, rope, positions, out)
 
 
@@ -619,6 +630,7 @@ def cache_append(cache: PagedCache, k, v, table, start, *, cu_tokens=None):
         cache.struct, k.data_ptr(), ks, v.data_ptr(), vs, k.shape[0], seqs, cu,
         _i32(start, "start", (seqs,)), _i32(table, "table", (seqs, width)), width,
         _here(cache.k, k, v, table, start, cu_tokens)))
+    _written(cache.k, cache.v, cache.kbar)
 
 
 def copy_pages(cache: PagedCache, pairs):
@@ -633,6 +645,7 @@ def copy_pages(cache: PagedCache, pairs):
     count = pairs.shape[0]
     _check(lib().bsa_cache_copy_pages(cache.struct, _i32(pairs, "pairs", (count, 2)), count,
                                       _here(cache.k, pairs)))
+    _written(cache.k, cache.v, cache.kbar)
 
 
 _OPTIONS = {(local, share): ctypes.byref(DecodeOptions(local, share))
@@ -662,6 +675,7 @@ def paged_decode(cache: PagedCache, q, table, lens, topk: int, *, token_seq=None
         seqs, seq, _i32(lens, "lens", (tokens,)), topk,
         _OPTIONS[bool(local_block), bool(share_group)], scale, out.data_ptr(),
         idx.data_ptr(), _here(cache.k, q, table, lens, token_seq, out)))
+    _written(out)
     return out, idx
 
 

@@ -59,3 +59,60 @@ def test_several_heads_of_a_thread(heads, n, d, rot, dtype, inter, way):
     got = call(x, plan, pos, out=out)
     off = (got.double() - want).abs()
     assert bool((off <= tol).all()), float((off - tol).max())
+
+
+# ------------------------------------------------------------------ autograd
+class Turn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, plan, positions):
+        ctx.rest = plan, positions
+        return bsa.rope(x, plan, positions)
+
+    @staticmethod
+    def backward(ctx, dy):
+        return bsa.rope_backward(dy.contiguous(), *ctx.rest), None, None
+
+
+def test_a_gradient_is_not_dropped_silently():
+    plan = bsa.Rope(64)
+    x = torch.randn(1, 2, 9, 64, device="cuda", requires_grad=True)
+    for call in (bsa.rope, bsa.rope_backward):
+        with pytest.raises(ValueError):
+            call(x, plan, 3)
+        with pytest.raises(ValueError):
+            call(x * 2, plan, 3)
+        with pytest.raises(ValueError):
+            call(x.detach(), plan, 3, out=torch.empty_like(x).requires_grad_())
+        with torch.no_grad():
+            y = call(x, plan, 3)
+        assert torch.equal(y, call(x.detach(), plan, 3)) and not y.requires_grad
+    w = torch.randn(1, 2, 9, 64, device="cuda")
+    (Turn.apply(x, plan, 3) * w).sum().backward()
+    assert torch.equal(x.grad, bsa.rope_backward(w, plan, 3))
+
+
+def test_tensors_that_autograd_saved_are_not_overwritten_unseen():
+    plan = bsa.Rope(64)
+    scale = torch.ones(64, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    cache = bsa.PagedCache.empty(4, 2, 16, 64)
+    table, ones = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([[0], [1]], [1, 1]))
+    new = torch.randn(2, 2, 64, device="cuda").bfloat16()
+    out, qk = new.clone(), new.transpose(0, 1)
+    writes = [
+        (qk, lambda: bsa.rope(qk, plan, 1, out=qk)),
+        (new, lambda: bsa.rope(qk, plan, 1, out=qk)),                  # the base of a view
+        (cache.v, lambda: bsa.cache_append(cache, new, new, table, ones - 1)),
+        (cache.k, lambda: bsa.copy_pages(cache, torch.tensor([[0, 2]], dtype=torch.int32, device="cuda"))),
+        (out, lambda: bsa.paged_decode(cache, new, table, ones, 1, out=out)),
+    ]
+    for saved, write in writes:
+        y = (saved * scale).sum()
+        write()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+        y = (saved * scale).sum()
+        y.backward()
+    with torch.inference_mode():
+        x = torch.randn(2, 9, 64, device="cuda")
+        want = bsa.rope(x, plan, 5)
+        assert torch.equal(bsa.rope(x, plan, 5, out=x), want)
