@@ -471,6 +471,14 @@ def selftest_wait_timeout(kind: int, limit_ns: int) -> None:
     _check(lib().bsa_selftest_wait_timeout(int(kind), int(limit_ns), _stream()))
 
 
+def _whole(x, bits: int, name: str) -> int:
+    """x as an integer of `bits` bits; ctypes would keep the low ones of any."""
+    i = int(x)
+    if i != x or not -(1 << (bits - 1)) <= i < 1 << (bits - 1):
+        raise ValueError(f"{name} must be a whole number of {bits} bits (got {x})")
+    return i
+
+
 # ------------------------------------------------------------ rotary positions
 class Rope:
     """A rotation's plan: frequencies, fixed-point table on the device, layout
@@ -482,6 +490,7 @@ class Rope:
                  low: float = 1.0, high: float = 32.0, attention_factor: float = 1.0,
                  inv_freq=None, device="cuda"):
         torch = _torch()
+        rot = _whole(rot, 32, "rot")
         if inv_freq is None:
             p = RopeParams(rot, ROPE_SCALING[scaling], theta, factor, original, low, high)
             self.inv_freq = np.empty(max(rot, 2) // 2, dtype=np.float64)
@@ -558,7 +567,7 @@ def _rope(fn, x, rope: Rope, positions, out):
             raise TypeError("positions must be [batch, n]")
         first, stream = 0, _here(x, out, rope.table, positions)
     else:
-        first, pos, stream = int(positions), None, _here(x, out, rope.table)
+        first, pos, stream = _whole(positions, 64, "positions"), None, _here(x, out, rope.table)
     _check(fn(Heads(batch, n, heads, d, dt), x.data_ptr(), xs, pos, first, rope.rotation,
               out.data_ptr(), os_, stream))
     _written(out)
@@ -641,6 +650,8 @@ def copy_pages(cache: PagedCache, pairs):
         pairs = np.asarray(pairs).reshape(-1, 2)
         if len(np.unique(pairs[:, 1])) < len(pairs) or np.isin(pairs[:, 1], pairs[:, 0]).any():
             raise ValueError("a page is the target of two pairs, or of one and the source of another")
+        if pairs.size and not (np.abs(pairs) < 1 << 31).all() or (pairs != np.floor(pairs)).any():
+            raise ValueError("pairs must be whole numbers of 32 bits")
         pairs = torch.from_numpy(np.ascontiguousarray(pairs, dtype=np.int32)).to(cache.k.device)
     count = pairs.shape[0]
     _check(lib().bsa_cache_copy_pages(cache.struct, _i32(pairs, "pairs", (count, 2)), count,
@@ -689,18 +700,20 @@ class PageTable:
     that would miss tokens, see bsa_pages_take_copies in bsa.h)."""
 
     def __init__(self, num_pages: int, page: int, max_seqs: int, width: int):
-        self.num_pages, self.max_seqs, self.width = num_pages, max_seqs, width
         self._h = ctypes.c_void_p()
+        num_pages, page = _whole(num_pages, 64, "num_pages"), _whole(page, 32, "page")
+        max_seqs, width = _whole(max_seqs, 32, "max_seqs"), _whole(width, 32, "width")
+        self.num_pages, self.max_seqs, self.width = num_pages, max_seqs, width
         _check(lib().bsa_pages_create(num_pages, page, max_seqs, width, ctypes.byref(self._h)))
 
     def reserve(self, seq: int, tokens: int):
-        _check(lib().bsa_pages_reserve(self._h, seq, tokens))
+        _check(lib().bsa_pages_reserve(self._h, _whole(seq, 32, "seq"), _whole(tokens, 64, "tokens")))
 
     def fork(self, source: int, to: int):
-        _check(lib().bsa_pages_fork(self._h, source, to))
+        _check(lib().bsa_pages_fork(self._h, _whole(source, 32, "source"), _whole(to, 32, "to")))
 
     def truncate(self, seq: int, length: int):
-        _check(lib().bsa_pages_truncate(self._h, seq, length))
+        _check(lib().bsa_pages_truncate(self._h, _whole(seq, 32, "seq"), _whole(length, 64, "length")))
 
     def free(self, seq: int):
         self.truncate(seq, 0)

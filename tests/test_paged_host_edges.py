@@ -4,6 +4,7 @@ import random
 
 import numpy as np
 import pytest
+import torch
 
 from content_dependent_block_gb300 import _build, bsa
 
@@ -173,3 +174,27 @@ def test_page_table_against_a_model_in_any_order(L, seed):
             copy(t.compact())
             check()
     assert refusals > 0
+
+
+# ------------------------------------------------ numbers that do not fit in C
+def test_numbers_that_do_not_fit_are_refused(L):
+    """ctypes keeps the low bits of any number: 2^32 would be sequence 0."""
+    t = bsa.PageTable(4, 16, 2, 3)
+    t.reserve(np.int64(0), np.int32(5))
+    for call in (lambda: t.reserve(1 << 32, 1), lambda: t.reserve(0, (1 << 64) + 1), lambda: t.reserve(0, 1.5),
+                 lambda: t.fork(1 << 32, 1), lambda: t.fork(0, (1 << 32) + 1), lambda: t.truncate(-(1 << 32), 0),
+                 lambda: t.truncate(0, 1 << 64), lambda: t.free(1 << 32),
+                 lambda: bsa.PageTable((1 << 64) + 4, 16, 2, 3), lambda: bsa.PageTable(4, (1 << 32) + 16, 2, 3),
+                 lambda: bsa.PageTable(4, 16, (1 << 32) + 2, 3), lambda: bsa.PageTable(4, 16, 2, (1 << 32) + 3),
+                 lambda: bsa.Rope((1 << 32) + 64, device="cpu")):
+        with pytest.raises(ValueError):
+            call()
+    assert t.tables()[1].tolist() == [5, 0]
+    x, plan = torch.zeros(2, 3, 64), bsa.Rope(64, device="cpu")
+    for first in (1 << 63, -(1 << 63) - 1, 1 << 64, 2.5):
+        with pytest.raises(ValueError):
+            bsa.rope(x, plan, first)
+    c = type("C", (), {"k": torch.zeros(1)})()
+    for pair in ([1 << 32, 1], [0, (1 << 32) + 1], [0.5, 1.0], [0, float("nan")], [0, 1 << 31]):
+        with pytest.raises(ValueError):
+            bsa.copy_pages(c, np.array([pair]))
