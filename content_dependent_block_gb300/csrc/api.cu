@@ -957,6 +957,7 @@ bsa_status bsa_cache_copy_pages(bsa_cache cache, const int32_t *pairs, int64_t c
     bsa::CacheView c;
     BSA_TRY(cache_view(cache, &c));
     if (count < 0) return fail(BSA_ERR_INVALID_ARG, "count must be >= 0");
+    if (count > 0x7fffffff) return fail(BSA_ERR_UNSUPPORTED, "count must fit in int32");
     if (count == 0) return ok();
     BSA_TRY(check_i32(pairs, "pairs"));
     int32_t *status = device_status_ptr();

@@ -198,3 +198,11 @@ def test_numbers_that_do_not_fit_are_refused(L):
     for pair in ([1 << 32, 1], [0, (1 << 32) + 1], [0.5, 1.0], [0, float("nan")], [0, 1 << 31]):
         with pytest.raises(ValueError):
             bsa.copy_pages(c, np.array([pair]))
+
+
+@pytest.mark.parametrize("count", [1 << 31, 1 << 62, (1 << 62) + 1, (1 << 63) - 1])
+def test_more_pairs_than_a_launch_takes_are_refused(L, count):
+    """The launch's CTAs, a multiple of the count, wrapped modulo 2^64."""
+    c = bsa.Cache(0x100000, 0x4000000, 0x8000000, 8, 2, 64, 64)
+    assert L.bsa_cache_copy_pages(c, ctypes.c_void_p(0x100000), count, None) == 2
+    assert b"count" in L.bsa_last_error()
