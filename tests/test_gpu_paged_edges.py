@@ -139,3 +139,50 @@ def test_append_many_sequences_report_one_bad_bound():
         bsa.cache_append(c, rows, rows, torch.arange(seqs, dtype=torch.int32, device="cuda")[:, None],
                          _i32([0] * seqs), cu_tokens=cu.cuda())
         assert (bsa.device_status() == 1) == falls, at
+
+
+# ----------------------------------------------------- decode: cluster sizes
+def _tokens_of_one_sequence(g, width, rows, tokens, least, d=64):
+    """One sequence over a table of `width` pages of 16, read by several tokens."""
+    k, v, kbar, _, table = _problem(g, [width * 16], rows, 1, d, 16)
+    lens = torch.randint(least, width * 16 + 1, (tokens,), generator=g).tolist()
+    return k, v, kbar, _randn(g, tokens, rows, d), table, lens, [0] * tokens
+
+
+def _check_tokens(k, v, kbar, q, table, lens, seq, topk, share):
+    out, idx = bsa.paged_decode(_cache(k, v, kbar), q.cuda(), table.cuda(), _i32(lens), topk,
+                                token_seq=_i32(seq), share_group=share)
+    want, tol, widx = ref.decode(k, v, kbar, q, table, lens, topk, seq, share=share)
+    assert torch.equal(idx.cpu(), widx)
+    ref.assert_within(out, want, tol, "decode")
+    assert bsa.device_status() == 0
+
+
+@pytest.mark.parametrize("cluster", range(1, 17))
+@pytest.mark.parametrize("rows,share", [(3, False), (3, True), (12, False), (12, True)])
+def test_decode_in_clusters_of_every_size(cluster, rows, share):
+    """One token takes a CTA for every 192 blocks (128 where a group has more
+    than eight heads, and three at least for the blocks these select), up to
+    sixteen."""
+    g = torch.Generator().manual_seed(cluster + rows)
+    width = (192 if rows <= 8 else 128) * cluster - 40
+    _check_tokens(*_tokens_of_one_sequence(g, width, rows, 1, width * 15), 3, share)
+
+
+@pytest.mark.parametrize("tokens", [7, 8, 13, 15, 23, 28, 29, 76, 100, 152, 200, 400])
+@pytest.mark.parametrize("rows,share", [(2, False), (2, True), (9, False)])
+def test_decode_in_the_clusters_of_every_batch(tokens, rows, share):
+    """As the tokens grow, two heads take clusters of 13, 12, 10, 9, 6 and 5,
+    then of 8, 8, 4, 4, 2 and 1 small CTAs; nine heads start at 16."""
+    g = torch.Generator().manual_seed(tokens + rows)
+    _check_tokens(*_tokens_of_one_sequence(g, 2500 if tokens <= 28 else 620, rows, tokens, 1), 4, share)
+
+
+@pytest.mark.parametrize("tokens", [17, 28, 160])
+def test_decode_in_clusters_that_grow_to_hold_the_scores(tokens):
+    """Sixteen rows of 16384 scores are more than the cluster of that batch
+    holds: it is doubled until they fit."""
+    g = torch.Generator().manual_seed(tokens)
+    k, v, kbar, _, table = _problem(g, [500], 16, 1, 64, 16, width=16384)
+    lens = torch.randint(1, 501, (tokens,), generator=g).tolist()
+    _check_tokens(k, v, kbar, _randn(g, tokens, 16, 64), table, lens, [0] * tokens, 3, False)
