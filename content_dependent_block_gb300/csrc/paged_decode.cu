@@ -35,13 +35,14 @@
 // latency of the chain table -> means -> k-th best -> keys.  m16n8k16 mma.sync
 // carries it: 8 or 16 rows against 16 keys is far below a tcgen05 tile (128
 // rows), and the keys arrive at about 23 bytes a clock and SM, for which the
-// tensor pipe is busy 5 to 7 % of the time.
+// tensor pipe is busy 7 to 8 % of the time, each weight entering twice (5 to
+// 7 % and the same times with the weights rounded to bf16 once).
 // Measured, device time: 96 sequences up to 32768 tokens, 64 heads over 8
-// sharing selections, d 128, top-32: 157 us, 5.9 TB/s (87 % of a plain copy's
+// sharing selections, d 128, top-32: 158 us, 5.8 TB/s (86 % of a plain copy's
 // rate); 32 such sequences, 32 heads over 8, d 64, top-16, each head for
-// itself: 57 us, 4.6 TB/s (the CTAs run in step, so memory idles while they
+// itself: 57 us, 4.7 TB/s (the CTAs run in step, so memory idles while they
 // select: a fifth of a CTA's time); one sequence of 131072 tokens, 64 heads
-// over 8, top-32: 32 us against 11 us of traffic.
+// over 8, top-32: 31 us against 11 us of traffic.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -1033,7 +1034,8 @@ constexpr int warps_large(int nt) { return nt == 1 ? 12 : 8; }
 constexpr int ctas_per_sm(int d, int nt) { return nt == 2 ? 2 : d == 64 ? 4 : 3; }
 
 // Clusters of 5 to 16 CTAs the card holds with one CTA to an SM (its SMs come
-// in groups of unequal size, and a cluster lies within one).
+// in groups of unequal size, and a cluster lies within one).  Asked of one
+// GB300; where another holds fewer, the last clusters take a second turn.
 constexpr int kFewItems = 28;
 constexpr int8_t kClustersFit[kMaxCluster + 1] = {0, 0, 0, 0, 0, 28, 23, 15, 15, 15, 13, 8, 8, 7, 7, 7, 7};
 
@@ -1170,9 +1172,11 @@ cudaError_t launch_paged_decode(const DecodeArgs &a, cudaStream_t st) {
     // card all at once.  Many: small CTAs, three or four to an SM, so that some
     // load while others select, in clusters as large as leave all CTAs on the
     // card at once (52 drafted tokens, 4 heads: 62 us in pairs; 70 in fours,
-    // which take two turns; 90 alone).  No more warps than have two 16-key tiles
-    // to attend to or sixteen blocks to score (1024 tokens, top-4: one CTA,
-    // 10.7 us; two, 11.1).
+    // which take two turns; 90 alone).  That counts registers; tables of many
+    // blocks take shared memory besides, up to one CTA to an SM (32 sequences
+    // of 131072 tokens in pages of 32: 606 us against 184 us of traffic).  No
+    // more warps than have two 16-key tiles to attend to or sixteen blocks to
+    // score (1024 tokens, top-4: one CTA, 10.7 us; two, 11.1).
     const bool large = items <= kFewItems;
     const int warps = large ? warps_large(p.rows > 8 ? 2 : 1) : kWarpsSmall;
     const int64_t picked = int64_t(p.score_rows) * a.topk;

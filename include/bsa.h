@@ -382,10 +382,9 @@ bsa_status bsa_forward_noalloc(bsa_shape shape, const void *q, const void *k,
  * t = p * f_i:
  *   x_a' = m (x_a cos t - x_b sin t),  x_b' = m (x_b cos t + x_a sin t),
  * with (a, b) = (i, i + rot/2), or (2i, 2i + 1) when interleaved; channels
- * from rot on are copied.  Products of a position and the
- * table (below) are exact modulo one turn, so an angle is off by fp32 rounding
- * and by 2^-52 of p f, the fp64 frequency's; the rotation is computed in fp32
- * and rounded once.
+ * from rot on are copied.  Products of a position and the table (below) are
+ * exact modulo one turn, so an angle is off by fp32 rounding and by 2^-52 of
+ * p f, the fp64 frequency's; the rotation is computed in fp32 and rounded once.
  *
  * The frequencies f_i are made on the host, in two steps so that a caller
  * can put its own in between:
@@ -521,9 +520,12 @@ bsa_status bsa_cache_copy_pages(bsa_cache cache, const int32_t *pairs, int64_t c
  * cache head h / (q_heads / heads) (score = q . kbar, unscaled), keeps its
  * topk best, and attends to their keys j < lens[t].  The selection is that of
  * the scores' exact values for the given kbar (close calls are settled in
- * fp64, one block after another: means that differ by rounding only, in
- * thousands of blocks, cost milliseconds), ties to the lower block id; a NaN
- * score ranks as -inf.
+ * fp64, one block after another: means that differ by rounding only, or one
+ * that is not finite, in thousands of blocks, cost milliseconds), ties to the
+ * lower block id; a NaN score ranks as -inf.  A kbar is that of the rows its
+ * page held at the last append: without local_block, a token with rows behind
+ * it in its own block (drafts; a sequence that was cut short) scores that
+ * block by a mean they are part of, although it does not attend to them.
  *   q          [tokens][q_heads][d] bf16 (device); q_stride: elements from a
  *              token to the next (multiple of 8, >= q_heads * d).
  *   table      int32 [seqs][table_width] (device), table_width <= 16384.
