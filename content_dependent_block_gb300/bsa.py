@@ -38,6 +38,8 @@ EXPORTS = (
     "bsa_last_error", "bsa_version",
     "bsa_rope_frequencies", "bsa_rope_table", "bsa_rope", "bsa_rope_backward",
     "bsa_cache_append", "bsa_cache_copy_pages", "bsa_paged_decode",
+    "bsa_cache8_append", "bsa_cache8_copy_pages", "bsa_paged_decode8",
+    "bsa_cache_read", "bsa_cache8_read", "bsa_paged_attention", "bsa_paged_attention8",
     "bsa_pages_create", "bsa_pages_destroy", "bsa_pages_reserve", "bsa_pages_fork",
     "bsa_pages_truncate", "bsa_pages_take_copies", "bsa_pages_compact", "bsa_pages_tables",
     "bsa_pages_free_pages",
@@ -98,8 +100,19 @@ class Cache(ctypes.Structure):
                 ("page", ctypes.c_int32), ("d", ctypes.c_int32)]
 
 
+class Cache8(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("kbar", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("d", ctypes.c_int32)]
+
+
 class DecodeOptions(ctypes.Structure):
     _fields_ = [("local_block", ctypes.c_int32), ("share_group", ctypes.c_int32)]
+
+
+class Window(ctypes.Structure):
+    _fields_ = [("window", ctypes.c_int32), ("sinks", ctypes.c_int32)]
 
 
 _lib = None
@@ -162,6 +175,16 @@ def lib():
         "bsa_cache_copy_pages": ([Cache, vp, i64, vp], i32),
         "bsa_paged_decode": ([Cache, vp, i64, i64, i32, vp, i32, i64, vp, vp, i32,
                               ctypes.POINTER(DecodeOptions), f32, vp, vp, vp], i32),
+        "bsa_cache8_append": ([Cache8, vp, i64, vp, i64, i64, i64, vp, vp, vp, i32, vp], i32),
+        "bsa_cache8_copy_pages": ([Cache8, vp, i64, vp], i32),
+        "bsa_paged_decode8": ([Cache8, vp, i64, i64, i32, vp, i32, i64, vp, vp, i32,
+                               ctypes.POINTER(DecodeOptions), f32, vp, vp, vp], i32),
+        "bsa_cache_read": ([Cache, i64, i64, vp, vp, vp, i32, vp, vp, Strides, vp], i32),
+        "bsa_cache8_read": ([Cache8, i64, i64, vp, vp, vp, i32, vp, vp, Strides, vp], i32),
+        "bsa_paged_attention": ([Cache, vp, i64, i64, i32, vp, i32, i64, vp, vp, vp,
+                                 ctypes.POINTER(Window), f32, vp, vp], i32),
+        "bsa_paged_attention8": ([Cache8, vp, i64, i64, i32, vp, i32, i64, vp, vp, vp,
+                                  ctypes.POINTER(Window), f32, vp, vp], i32),
         "bsa_pages_create": ([i64, i32, i32, i32, ctypes.POINTER(vp)], i32),
         "bsa_pages_destroy": ([vp], i32),
         "bsa_pages_reserve": ([vp, i32, i64], i32),
@@ -592,20 +615,28 @@ def rope_backward(dout, rope: Rope, positions=0, *, out=None):
 class PagedCache:
     """A paged cache's device tensors: k, v [pages, heads, page, d] bf16 and
     the block means kbar [pages, heads, d] fp32 (bsa_cache in bsa.h)."""
+    _calls = ("bsa_cache_append", "bsa_cache_copy_pages", "bsa_paged_decode", "bsa_cache_read",
+              "bsa_paged_attention")
 
     def __init__(self, k, v, kbar):
         torch = _torch()
         if k.dim() != 4 or k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 \
                 or k.shape != v.shape or not k.is_contiguous() or not v.is_contiguous():
             raise ValueError("k and v must be contiguous bfloat16 [pages, heads, page, d]")
-        if kbar.dtype != torch.float32 or not kbar.is_contiguous() \
-                or tuple(kbar.shape) != (k.shape[0], k.shape[1], k.shape[3]):
-            raise ValueError("kbar must be contiguous float32 [pages, heads, d]")
+        _check_means(kbar, k.shape)
         _here(k, v, kbar)
         self.k, self.v, self.kbar = k, v, kbar
         self.num_pages, self.heads, self.page, self.d = k.shape
         self.struct = Cache(k.data_ptr(), v.data_ptr(), kbar.data_ptr(), self.num_pages,
                             self.heads, self.page, self.d)
+        self._bind(k, v, kbar)
+
+    def _bind(self, *written):
+        """The tensors that appends and copies write, and the entry points for
+        this kind of cache."""
+        self.written = written
+        self._append, self._copy, self._decode, self._read, self._attention = \
+            (getattr(lib(), name) for name in self._calls)
 
     @classmethod
     def empty(cls, num_pages: int, heads: int, page: int, d: int, device="cuda"):
@@ -613,6 +644,47 @@ class PagedCache:
         k, v = (torch.zeros((num_pages, heads, page, d), dtype=torch.bfloat16, device=device)
                 for _ in range(2))
         return cls(k, v, torch.zeros((num_pages, heads, d), dtype=torch.float32, device=device))
+
+
+def _check_means(kbar, shape):
+    if kbar.dtype != _torch().float32 or not kbar.is_contiguous() \
+            or tuple(kbar.shape) != (shape[0], shape[1], shape[3]):
+        raise ValueError("kbar must be contiguous float32 [pages, heads, d]")
+
+
+class PagedCache8(PagedCache):
+    """A paged cache in 8 bits: k, v [pages, heads, page, d] int8, k_scale,
+    v_scale [pages, heads, page] fp32 and the block means kbar [pages, heads,
+    d] fp32 (bsa_cache8 in bsa.h).  A row stands for its codes times its
+    scale; ``cache_append`` quantises bf16 rows.  Every function that takes a
+    PagedCache takes either kind."""
+    _calls = ("bsa_cache8_append", "bsa_cache8_copy_pages", "bsa_paged_decode8", "bsa_cache8_read",
+              "bsa_paged_attention8")
+
+    def __init__(self, k, v, k_scale, v_scale, kbar):
+        torch = _torch()
+        if k.dim() != 4 or k.dtype != torch.int8 or v.dtype != torch.int8 \
+                or k.shape != v.shape or not k.is_contiguous() or not v.is_contiguous():
+            raise ValueError("k and v must be contiguous int8 [pages, heads, page, d]")
+        for scale in (k_scale, v_scale):
+            if scale.dtype != torch.float32 or not scale.is_contiguous() or scale.shape != k.shape[:3]:
+                raise ValueError("k_scale and v_scale must be contiguous float32 [pages, heads, page]")
+        _check_means(kbar, k.shape)
+        _here(k, v, k_scale, v_scale, kbar)
+        self.k, self.v, self.k_scale, self.v_scale, self.kbar = k, v, k_scale, v_scale, kbar
+        self.num_pages, self.heads, self.page, self.d = k.shape
+        self.struct = Cache8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                             kbar.data_ptr(), self.num_pages, self.heads, self.page, self.d)
+        self._bind(k, v, k_scale, v_scale, kbar)
+
+    @classmethod
+    def empty(cls, num_pages: int, heads: int, page: int, d: int, device="cuda"):
+        torch = _torch()
+        k, v = (torch.zeros((num_pages, heads, page, d), dtype=torch.int8, device=device)
+                for _ in range(2))
+        ks, vs = (torch.zeros((num_pages, heads, page), dtype=torch.float32, device=device)
+                  for _ in range(2))
+        return cls(k, v, ks, vs, torch.zeros((num_pages, heads, d), dtype=torch.float32, device=device))
 
 
 def _token_rows(t, name: str, heads: int, d: int) -> int:
@@ -635,11 +707,11 @@ def cache_append(cache: PagedCache, k, v, table, start, *, cu_tokens=None):
     if k.shape != v.shape:
         raise ValueError("k and v must have one shape")
     cu = None if cu_tokens is None else _i32(cu_tokens, "cu_tokens", (seqs + 1,))
-    _check(lib().bsa_cache_append(
+    _check(cache._append(
         cache.struct, k.data_ptr(), ks, v.data_ptr(), vs, k.shape[0], seqs, cu,
         _i32(start, "start", (seqs,)), _i32(table, "table", (seqs, width)), width,
         _here(cache.k, k, v, table, start, cu_tokens)))
-    _written(cache.k, cache.v, cache.kbar)
+    _written(*cache.written)
 
 
 def copy_pages(cache: PagedCache, pairs):
@@ -654,9 +726,9 @@ def copy_pages(cache: PagedCache, pairs):
             raise ValueError("pairs must be whole numbers of 32 bits")
         pairs = torch.from_numpy(np.ascontiguousarray(pairs, dtype=np.int32)).to(cache.k.device)
     count = pairs.shape[0]
-    _check(lib().bsa_cache_copy_pages(cache.struct, _i32(pairs, "pairs", (count, 2)), count,
-                                      _here(cache.k, pairs)))
-    _written(cache.k, cache.v, cache.kbar)
+    _check(cache._copy(cache.struct, _i32(pairs, "pairs", (count, 2)), count,
+                       _here(cache.k, pairs)))
+    _written(*cache.written)
 
 
 _OPTIONS = {(local, share): ctypes.byref(DecodeOptions(local, share))
@@ -681,13 +753,80 @@ def paged_decode(cache: PagedCache, q, table, lens, topk: int, *, token_seq=None
         raise ValueError("out must be contiguous bfloat16 [tokens, q_heads, d]")
     idx = torch.empty((tokens, cache.heads if share_group else q_heads, topk), dtype=torch.int32,
                       device=q.device)
-    _check(lib().bsa_paged_decode(
+    _check(cache._decode(
         cache.struct, q.data_ptr(), qs, tokens, q_heads, _i32(table, "table", (seqs, width)), width,
         seqs, seq, _i32(lens, "lens", (tokens,)), topk,
         _OPTIONS[bool(local_block), bool(share_group)], scale, out.data_ptr(),
         idx.data_ptr(), _here(cache.k, q, table, lens, token_seq, out)))
     _written(out)
     return out, idx
+
+
+def cache_read(cache: PagedCache, table, start, tokens: int, *, cu_tokens=None,
+               heads_first: bool = False, out=None):
+    """(k, v) bf16 of cached tokens: sequence s's positions from ``start`` on,
+    ``tokens`` in all, cut by ``cu_tokens`` (None: as many for each), as
+    [tokens, heads, d], or [heads, tokens, d] with ``heads_first`` (the layout
+    ``forward`` takes).  ``out``: a pair of tensors of that shape, of one
+    layout, with contiguous channels.  See bsa_cache_read in bsa.h."""
+    torch = _torch()
+    seqs, width = table.shape
+    tokens = _whole(tokens, 64, "tokens")
+    shape = (cache.heads, tokens, cache.d) if heads_first else (tokens, cache.heads, cache.d)
+    if out is None:
+        k, v = (torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) for _ in range(2))
+    else:
+        k, v = out
+        for t in out:
+            if t.shape != shape or t.dtype is not torch.bfloat16 or t.stride(2) != 1:
+                raise ValueError(f"out must be two bfloat16 {list(shape)} with contiguous channels")
+        if k.stride() != v.stride():
+            raise ValueError("out's tensors must have one layout")
+        if torch.is_grad_enabled() and (k.requires_grad or v.requires_grad):
+            raise ValueError("cache_read records no history: out must not require a gradient")
+    st = k.stride()
+    cu = None if cu_tokens is None else _i32(cu_tokens, "cu_tokens", (seqs + 1,))
+    _check(cache._read(
+        cache.struct, tokens, seqs, cu, _i32(start, "start", (seqs,)),
+        _i32(table, "table", (seqs, width)), width, k.data_ptr(), v.data_ptr(),
+        Strides(0, st[0], st[1]) if heads_first else Strides(0, st[1], st[0]),
+        _here(cache.k, table, start, cu_tokens, k, v)))
+    _written(k, v)
+    return k, v
+
+
+def paged_attention(cache: PagedCache, q, table, start, *, cu_tokens=None, tree=None,
+                    window: int = 0, sinks: int = 0, scale: float = 0.0, out=None):
+    """Attention of new tokens q [tokens, q_heads, d], whose K and V the cache
+    holds from position ``start`` of each sequence on, to all keys up to
+    themselves.  ``cu_tokens`` int32 [seqs + 1], None: as many tokens for each.
+    ``tree`` int64 [tokens]: which of its sequence's (at most 64) new tokens a
+    token sees, besides the prefix.  ``window`` W and ``sinks``: only the last W
+    positions and the first few; 0: all.  See bsa_paged_attention in bsa.h."""
+    torch = _torch()
+    seqs, width = table.shape
+    tokens, q_heads, d = q.shape
+    qs = _token_rows(q, "q", q_heads, cache.d)
+    cu = None if cu_tokens is None else _i32(cu_tokens, "cu_tokens", (seqs + 1,))
+    if tree is not None and (tree.shape != (tokens,) or tree.dtype is not torch.int64
+                             or not tree.is_contiguous()):
+        raise TypeError(f"tree must be a contiguous int64 tensor {[tokens]}")
+    window, sinks = _whole(window, 32, "window"), _whole(sinks, 32, "sinks")
+    if window == 0 and sinks != 0:
+        raise ValueError("sinks without a window")
+    if out is None:
+        out = torch.empty((tokens, q_heads, d), dtype=q.dtype, device=q.device)
+    elif out.dtype is not q.dtype or out.shape != (tokens, q_heads, d) or not out.is_contiguous():
+        raise ValueError("out must be contiguous bfloat16 [tokens, q_heads, d]")
+    if torch.is_grad_enabled() and (q.requires_grad or out.requires_grad):
+        raise ValueError("paged_attention records no history: call it under no_grad")
+    _check(cache._attention(
+        cache.struct, q.data_ptr(), qs, tokens, q_heads, _i32(table, "table", (seqs, width)), width,
+        seqs, cu, _i32(start, "start", (seqs,)), None if tree is None else tree.data_ptr(),
+        None if window == 0 else ctypes.byref(Window(window, sinks)), scale, out.data_ptr(),
+        _here(cache.k, q, table, start, cu_tokens, tree, out)))
+    _written(out)
+    return out
 
 
 class PageTable:

@@ -873,7 +873,10 @@ bsa_status bsa_rope_backward(bsa_heads shape, const void *dout, bsa_strides dout
                      stream);
 }
 
+}  // extern "C"
+
 // -------------------------------------------------------------- paged cache
+// (C linkage by the header's declarations; the helpers overload and are templates)
 static bsa_status cache_view(const bsa_cache &c, bsa::CacheView *v) {
     if (c.d != 64 && c.d != 128) return fail(BSA_ERR_UNSUPPORTED, "d must be 64 or 128 (got %d)", c.d);
     if (c.page != 16 && c.page != 32 && c.page != 64 && c.page != 128)
@@ -914,91 +917,251 @@ static bsa_status check_token_stride(int64_t stride, int64_t row, const char *na
     return BSA_OK;
 }
 
-bsa_status bsa_cache_append(bsa_cache cache, const void *k, int64_t k_stride, const void *v,
-                            int64_t v_stride, int64_t tokens, int64_t seqs,
-                            const int32_t *cu_tokens, const int32_t *start, const int32_t *table,
-                            int32_t table_width, void *stream) {
-    bsa::AppendArgs a = {};
-    BSA_TRY(cache_view(cache, &a.c));
+static bsa_status cache8_view(const bsa_cache8 &c, bsa::Cache8View *v) {
+    bsa::CacheView plain;
+    BSA_TRY(cache_view({c.k, c.v, c.kbar, c.num_pages, c.heads, c.page, c.d}, &plain));
+    BSA_TRY(check_ptr(c.k_scale, "cache.k_scale"));
+    BSA_TRY(check_ptr(c.v_scale, "cache.v_scale"));
+    *v = {c.k, c.v, c.k_scale, c.v_scale, c.kbar, c.num_pages, c.heads, c.page, c.d};
+    return BSA_OK;
+}
+
+static bool in_cache(const bsa_cache8 &c, const void *p, int64_t bytes) {
+    const int64_t rows = c.num_pages * c.heads * c.page;
+    return overlap(c.k, rows * c.d, p, bytes) || overlap(c.v, rows * c.d, p, bytes) ||
+           overlap(c.k_scale, rows * 4, p, bytes) || overlap(c.v_scale, rows * 4, p, bytes) ||
+           overlap(c.kbar, c.num_pages * c.heads * c.d * 4, p, bytes);
+}
+
+// What the two kinds of cache have in common below: checks of the arguments
+// that do not depend on how the pages hold their rows.
+static bsa_status check_step(int64_t tokens, int64_t seqs, const int32_t *cu_tokens, int32_t table_width) {
     if (tokens < 0 || seqs < 1 || table_width < 1)
         return fail(BSA_ERR_INVALID_ARG, "tokens must be >= 0, seqs and table_width >= 1");
     if (tokens > 0x7fffffff || seqs > 0x7fffff)
         return fail(BSA_ERR_UNSUPPORTED, "tokens must fit in int32, seqs in 23 bits");
     if (cu_tokens == nullptr && tokens % seqs != 0)
         return fail(BSA_ERR_INVALID_ARG, "tokens must be a multiple of seqs without cu_tokens");
-    if (tokens == 0) return ok();           // k and v may be empty then
-    BSA_TRY(check_ptr(k, "k"));
-    BSA_TRY(check_ptr(v, "v"));
-    BSA_TRY(check_token_stride(k_stride, int64_t(cache.heads) * cache.d, "k_stride"));
-    BSA_TRY(check_token_stride(v_stride, int64_t(cache.heads) * cache.d, "v_stride"));
+    return BSA_OK;
+}
+
+static bsa_status check_lists(const int32_t *cu_tokens, const int32_t *start, const int32_t *table) {
     if (cu_tokens != nullptr) BSA_TRY(check_i32(cu_tokens, "cu_tokens"));
     BSA_TRY(check_i32(start, "start"));
-    BSA_TRY(check_i32(table, "table"));
+    return check_i32(table, "table");
+}
+
+template <typename Cache>
+static bsa_status check_new_rows(const Cache &cache, const void *k, int64_t k_stride, const void *v,
+                                 int64_t v_stride, int64_t tokens, const int32_t *cu_tokens,
+                                 const int32_t *start, const int32_t *table) {
     const int64_t row = int64_t(cache.heads) * cache.d;
+    BSA_TRY(check_ptr(k, "k"));
+    BSA_TRY(check_ptr(v, "v"));
+    BSA_TRY(check_token_stride(k_stride, row, "k_stride"));
+    BSA_TRY(check_token_stride(v_stride, row, "v_stride"));
+    BSA_TRY(check_lists(cu_tokens, start, table));
     if (in_cache(cache, k, ((tokens - 1) * k_stride + row) * 2) ||
         in_cache(cache, v, ((tokens - 1) * v_stride + row) * 2))
         return fail(BSA_ERR_INVALID_ARG, "k or v overlaps the cache");
-    a.k = static_cast<const uint16_t *>(k);
-    a.v = static_cast<const uint16_t *>(v);
-    a.k_stride = k_stride;
-    a.v_stride = v_stride;
-    a.tokens = tokens;
-    a.seqs = seqs;
-    a.cu = cu_tokens;
-    a.start = start;
-    a.table = table;
-    a.width = table_width;
-    a.status = device_status_ptr();
-    if (a.status == nullptr) return fail(BSA_ERR_CUDA, "status word unavailable");
+    return BSA_OK;
+}
+
+// Fills what AppendArgs and Append8Args share.
+template <typename Args>
+static bsa_status append_args(Args *a, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                              int64_t tokens, int64_t seqs, const int32_t *cu_tokens,
+                              const int32_t *start, const int32_t *table, int32_t table_width) {
+    a->k = static_cast<const uint16_t *>(k);
+    a->v = static_cast<const uint16_t *>(v);
+    a->k_stride = k_stride;
+    a->v_stride = v_stride;
+    a->tokens = tokens;
+    a->seqs = seqs;
+    a->cu = cu_tokens;
+    a->start = start;
+    a->table = table;
+    a->width = table_width;
+    a->status = device_status_ptr();
+    if (a->status == nullptr) return fail(BSA_ERR_CUDA, "status word unavailable");
+    return BSA_OK;
+}
+
+bsa_status bsa_cache_append(bsa_cache cache, const void *k, int64_t k_stride, const void *v,
+                            int64_t v_stride, int64_t tokens, int64_t seqs,
+                            const int32_t *cu_tokens, const int32_t *start, const int32_t *table,
+                            int32_t table_width, void *stream) {
+    bsa::AppendArgs a = {};
+    BSA_TRY(cache_view(cache, &a.c));
+    BSA_TRY(check_step(tokens, seqs, cu_tokens, table_width));
+    if (tokens == 0) return ok();           // k and v may be empty then
+    BSA_TRY(check_new_rows(cache, k, k_stride, v, v_stride, tokens, cu_tokens, start, table));
+    BSA_TRY(append_args(&a, k, k_stride, v, v_stride, tokens, seqs, cu_tokens, start, table, table_width));
     return launched(bsa::launch_cache_append(a, static_cast<cudaStream_t>(stream)), "append launch");
+}
+
+bsa_status bsa_cache8_append(bsa_cache8 cache, const void *k, int64_t k_stride, const void *v,
+                             int64_t v_stride, int64_t tokens, int64_t seqs,
+                             const int32_t *cu_tokens, const int32_t *start, const int32_t *table,
+                             int32_t table_width, void *stream) {
+    bsa::Append8Args a = {};
+    BSA_TRY(cache8_view(cache, &a.c));
+    BSA_TRY(check_step(tokens, seqs, cu_tokens, table_width));
+    if (tokens == 0) return ok();           // k and v may be empty then
+    BSA_TRY(check_new_rows(cache, k, k_stride, v, v_stride, tokens, cu_tokens, start, table));
+    BSA_TRY(append_args(&a, k, k_stride, v, v_stride, tokens, seqs, cu_tokens, start, table, table_width));
+    return launched(bsa::launch_cache_append8(a, static_cast<cudaStream_t>(stream)), "append launch");
+}
+
+static bsa_status check_pairs(const int32_t *pairs, int64_t count) {
+    if (count < 0) return fail(BSA_ERR_INVALID_ARG, "count must be >= 0");
+    if (count > 0x7fffffff) return fail(BSA_ERR_UNSUPPORTED, "count must fit in int32");
+    return count == 0 ? BSA_OK : check_i32(pairs, "pairs");
 }
 
 bsa_status bsa_cache_copy_pages(bsa_cache cache, const int32_t *pairs, int64_t count, void *stream) {
     bsa::CacheView c;
     BSA_TRY(cache_view(cache, &c));
-    if (count < 0) return fail(BSA_ERR_INVALID_ARG, "count must be >= 0");
-    if (count > 0x7fffffff) return fail(BSA_ERR_UNSUPPORTED, "count must fit in int32");
+    BSA_TRY(check_pairs(pairs, count));
     if (count == 0) return ok();
-    BSA_TRY(check_i32(pairs, "pairs"));
     int32_t *status = device_status_ptr();
     if (status == nullptr) return fail(BSA_ERR_CUDA, "status word unavailable");
     return launched(bsa::launch_copy_pages(c, pairs, count, status, static_cast<cudaStream_t>(stream)),
                     "page copy launch");
 }
 
-bsa_status bsa_paged_decode(bsa_cache cache, const void *q, int64_t q_stride, int64_t tokens,
-                            int32_t q_heads, const int32_t *table, int32_t table_width,
-                            int64_t seqs, const int32_t *token_seq, const int32_t *lens,
-                            int32_t topk, const bsa_decode_options *options, float scale,
-                            void *out, int32_t *idx_out, void *stream) {
-    bsa::DecodeArgs a = {};
-    BSA_TRY(cache_view(cache, &a.c));
+bsa_status bsa_cache8_copy_pages(bsa_cache8 cache, const int32_t *pairs, int64_t count, void *stream) {
+    bsa::Cache8View c;
+    BSA_TRY(cache8_view(cache, &c));
+    BSA_TRY(check_pairs(pairs, count));
+    if (count == 0) return ok();
+    int32_t *status = device_status_ptr();
+    if (status == nullptr) return fail(BSA_ERR_CUDA, "status word unavailable");
+    return launched(bsa::launch_copy_pages8(c, pairs, count, status, static_cast<cudaStream_t>(stream)),
+                    "page copy launch");
+}
+
+template <typename Cache>
+static bsa_status read_impl(const Cache &cache, bsa::ReadArgs a, int64_t tokens, int64_t seqs,
+                            const int32_t *cu_tokens, const int32_t *start, const int32_t *table,
+                            int32_t table_width, void *k, void *v, const bsa_strides &out, void *stream) {
+    BSA_TRY(check_step(tokens, seqs, cu_tokens, table_width));
+    if (tokens == 0) return ok();           // k and v may be empty then
+    BSA_TRY(check_ptr(k, "k"));
+    BSA_TRY(check_ptr(v, "v"));
+    BSA_TRY(check_lists(cu_tokens, start, table));
+    const int64_t most = int64_t(1) << 40;
+    const int64_t size[2] = {cache.heads, tokens}, st[2] = {out.head, out.token};
+    int64_t end = cache.d;                  // one past the last element
+    for (int i = 0; i < 2; ++i) {
+        if (size[i] == 1) continue;
+        if (st[i] < 0 || st[i] >= most) return fail(BSA_ERR_UNSUPPORTED, "strides must be in [0, 2^40)");
+        if (st[i] % 8 != 0) return fail(BSA_ERR_ALIGNMENT, "strides must be multiples of 16 bytes");
+        if (st[i] * double(size[i]) > 4e18 / 64)
+            return fail(BSA_ERR_UNSUPPORTED, "tensor extent is too large");
+        end += st[i] * (size[i] - 1);
+    }
+    // rows must be apart: the larger stride spans what lies below it
+    const int in = size[1] == 1 || (size[0] > 1 && st[0] < st[1]) ? 0 : 1;
+    const int64_t inner = size[in] == 1 ? cache.d : cache.d + st[in] * (size[in] - 1);
+    if ((size[in] > 1 && st[in] < cache.d) || (size[1 - in] > 1 && st[1 - in] < inner))
+        return fail(BSA_ERR_INVALID_ARG, "rows of the output overlap");
+    if (overlap(k, end * 2, v, end * 2) || in_cache(cache, k, end * 2) || in_cache(cache, v, end * 2))
+        return fail(BSA_ERR_INVALID_ARG, "k and v overlap, or the cache");
+    a.num_pages = cache.num_pages;
+    a.heads = cache.heads;
+    a.page = cache.page;
+    a.d = cache.d;
+    a.tokens = tokens;
+    a.seqs = seqs;
+    a.cu = cu_tokens;
+    a.start = start;
+    a.table = table;
+    a.width = table_width;
+    a.k_out = static_cast<uint16_t *>(k);
+    a.v_out = static_cast<uint16_t *>(v);
+    a.token_stride = out.token;
+    a.head_stride = out.head;
+    a.status = device_status_ptr();
+    if (a.status == nullptr) return fail(BSA_ERR_CUDA, "status word unavailable");
+    return launched(bsa::launch_cache_read(a, static_cast<cudaStream_t>(stream)), "read launch");
+}
+
+bsa_status bsa_cache_read(bsa_cache cache, int64_t tokens, int64_t seqs, const int32_t *cu_tokens,
+                          const int32_t *start, const int32_t *table, int32_t table_width, void *k,
+                          void *v, bsa_strides out, void *stream) {
+    bsa::CacheView c;
+    BSA_TRY(cache_view(cache, &c));
+    bsa::ReadArgs a = {};
+    a.k = c.k;
+    a.v = c.v;
+    return read_impl(cache, a, tokens, seqs, cu_tokens, start, table, table_width, k, v, out, stream);
+}
+
+bsa_status bsa_cache8_read(bsa_cache8 cache, int64_t tokens, int64_t seqs, const int32_t *cu_tokens,
+                           const int32_t *start, const int32_t *table, int32_t table_width, void *k,
+                           void *v, bsa_strides out, void *stream) {
+    bsa::Cache8View c;
+    BSA_TRY(cache8_view(cache, &c));
+    bsa::ReadArgs a = {};
+    a.k = c.k;
+    a.v = c.v;
+    a.ks = c.ks;
+    a.vs = c.vs;
+    return read_impl(cache, a, tokens, seqs, cu_tokens, start, table, table_width, k, v, out, stream);
+}
+
+// The queries of a step, their output and the scale; in between the int32 arrays.
+template <typename Cache, typename Lists>
+static bsa_status check_queries(const Cache &cache, const void *q, int64_t q_stride, int64_t tokens,
+                                int32_t q_heads, float scale, const void *out, const Lists &lists) {
+    const int64_t row = int64_t(q_heads) * cache.d, out_bytes = tokens * row * 2;
+    BSA_TRY(check_ptr(q, "q"));
+    BSA_TRY(check_ptr(out, "out"));
+    BSA_TRY(check_token_stride(q_stride, row, "q_stride"));
+    BSA_TRY(lists());
+    if (std::isnan(scale)) return fail(BSA_ERR_INVALID_ARG, "scale is NaN");
+    if (overlap(q, ((tokens - 1) * q_stride + row) * 2, out, out_bytes) ||
+        in_cache(cache, out, out_bytes))
+        return fail(BSA_ERR_INVALID_ARG, "out overlaps q or the cache");
+    return BSA_OK;
+}
+
+static bsa_status check_group(int32_t q_heads, int32_t heads) {
+    if (q_heads < 1 || q_heads % heads != 0)
+        return fail(BSA_ERR_INVALID_ARG, "q_heads must be a multiple of the cache's heads");
+    if (q_heads / heads > bsa::kDecodeMaxGroup)
+        return fail(BSA_ERR_UNSUPPORTED, "at most %d query heads per cache head", bsa::kDecodeMaxGroup);
+    return BSA_OK;
+}
+
+static float paged_scale_log2(float scale, int32_t d) {
+    return (scale > 0.f ? scale : 1.f / std::sqrt(float(d))) * 1.4426950408889634f;
+}
+
+template <typename Cache>
+static bsa_status decode_impl(const Cache &cache, bsa::DecodeArgs a, const void *q, int64_t q_stride,
+                              int64_t tokens, int32_t q_heads, const int32_t *table,
+                              int32_t table_width, int64_t seqs, const int32_t *token_seq,
+                              const int32_t *lens, int32_t topk, const bsa_decode_options *options,
+                              float scale, void *out, int32_t *idx_out, void *stream) {
     if (tokens < 0 || seqs < 1 || table_width < 1)
         return fail(BSA_ERR_INVALID_ARG, "tokens must be >= 0, seqs and table_width >= 1");
     if (tokens > 0x7fffffff || seqs > 0x7fffffff)
         return fail(BSA_ERR_UNSUPPORTED, "tokens and seqs must fit in int32");
-    if (q_heads < 1 || q_heads % cache.heads != 0)
-        return fail(BSA_ERR_INVALID_ARG, "q_heads must be a multiple of the cache's heads");
-    if (q_heads / cache.heads > bsa::kDecodeMaxGroup)
-        return fail(BSA_ERR_UNSUPPORTED, "at most %d query heads per cache head", bsa::kDecodeMaxGroup);
+    BSA_TRY(check_group(q_heads, cache.heads));
     if (topk < 1 || topk > 32) return fail(BSA_ERR_UNSUPPORTED, "topk must be in [1, 32] (got %d)", topk);
     if (table_width > bsa::kDecodeMaxWidth)
         return fail(BSA_ERR_UNSUPPORTED, "table_width must be <= %d", bsa::kDecodeMaxWidth);
     if (token_seq == nullptr && seqs < tokens)
         return fail(BSA_ERR_INVALID_ARG, "without token_seq there must be a sequence per token");
     if (tokens == 0) return ok();           // q and out may be empty then
-    BSA_TRY(check_ptr(q, "q"));
-    BSA_TRY(check_ptr(out, "out"));
-    BSA_TRY(check_token_stride(q_stride, int64_t(q_heads) * cache.d, "q_stride"));
-    BSA_TRY(check_i32(table, "table"));
-    BSA_TRY(check_i32(lens, "lens"));
-    if (token_seq != nullptr) BSA_TRY(check_i32(token_seq, "token_seq"));
-    if (idx_out != nullptr) BSA_TRY(check_i32(idx_out, "idx_out"));
-    if (std::isnan(scale)) return fail(BSA_ERR_INVALID_ARG, "scale is NaN");
-    const int64_t row = int64_t(q_heads) * cache.d, out_bytes = tokens * row * 2;
-    if (overlap(q, ((tokens - 1) * q_stride + row) * 2, out, out_bytes) ||
-        in_cache(cache, out, out_bytes))
-        return fail(BSA_ERR_INVALID_ARG, "out overlaps q or the cache");
+    BSA_TRY(check_queries(cache, q, q_stride, tokens, q_heads, scale, out, [&]() -> bsa_status {
+        BSA_TRY(check_i32(table, "table"));
+        BSA_TRY(check_i32(lens, "lens"));
+        if (token_seq != nullptr) BSA_TRY(check_i32(token_seq, "token_seq"));
+        return idx_out != nullptr ? check_i32(idx_out, "idx_out") : BSA_OK;
+    }));
     a.q = static_cast<const uint16_t *>(q);
     a.q_stride = q_stride;
     a.tokens = tokens;
@@ -1011,13 +1174,108 @@ bsa_status bsa_paged_decode(bsa_cache cache, const void *q, int64_t q_stride, in
     a.topk = topk;
     a.local = options != nullptr && options->local_block ? 1 : 0;
     a.share = options != nullptr && options->share_group ? 1 : 0;
-    a.scale_log2 = (scale > 0.f ? scale : 1.f / std::sqrt(float(cache.d))) * 1.4426950408889634f;
+    a.scale_log2 = paged_scale_log2(scale, cache.d);
     a.out = static_cast<uint16_t *>(out);
     a.idx = idx_out;
     a.status = device_status_ptr();
     if (a.status == nullptr) return fail(BSA_ERR_CUDA, "status word unavailable");
-    return launched(bsa::launch_paged_decode(a, static_cast<cudaStream_t>(stream)), "decode launch");
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return launched(a.ks != nullptr ? bsa::launch_paged_decode8(a, st) : bsa::launch_paged_decode(a, st),
+                    "decode launch");
 }
+
+// An 8-bit cache as the kernels over both kinds take it.
+static bsa::CacheView codes_view(const bsa::Cache8View &c) {
+    return {reinterpret_cast<uint16_t *>(c.k), reinterpret_cast<uint16_t *>(c.v), c.kbar, c.num_pages,
+            c.heads, c.page, c.d};
+}
+
+bsa_status bsa_paged_decode(bsa_cache cache, const void *q, int64_t q_stride, int64_t tokens,
+                            int32_t q_heads, const int32_t *table, int32_t table_width,
+                            int64_t seqs, const int32_t *token_seq, const int32_t *lens,
+                            int32_t topk, const bsa_decode_options *options, float scale,
+                            void *out, int32_t *idx_out, void *stream) {
+    bsa::DecodeArgs a = {};
+    BSA_TRY(cache_view(cache, &a.c));
+    return decode_impl(cache, a, q, q_stride, tokens, q_heads, table, table_width, seqs, token_seq, lens,
+                       topk, options, scale, out, idx_out, stream);
+}
+
+bsa_status bsa_paged_decode8(bsa_cache8 cache, const void *q, int64_t q_stride, int64_t tokens,
+                             int32_t q_heads, const int32_t *table, int32_t table_width,
+                             int64_t seqs, const int32_t *token_seq, const int32_t *lens,
+                             int32_t topk, const bsa_decode_options *options, float scale,
+                             void *out, int32_t *idx_out, void *stream) {
+    bsa::Cache8View c;
+    BSA_TRY(cache8_view(cache, &c));
+    bsa::DecodeArgs a = {};
+    a.c = codes_view(c);
+    a.ks = c.ks;
+    a.vs = c.vs;
+    return decode_impl(cache, a, q, q_stride, tokens, q_heads, table, table_width, seqs, token_seq, lens,
+                       topk, options, scale, out, idx_out, stream);
+}
+
+template <typename Cache>
+static bsa_status attention_impl(const Cache &cache, bsa::AttentionArgs a, const void *q,
+                                 int64_t q_stride, int64_t tokens, int32_t q_heads,
+                                 const int32_t *table, int32_t table_width, int64_t seqs,
+                                 const int32_t *cu_tokens, const int32_t *start, const uint64_t *tree,
+                                 const bsa_window *window, float scale, void *out, void *stream) {
+    BSA_TRY(check_step(tokens, seqs, cu_tokens, table_width));
+    BSA_TRY(check_group(q_heads, cache.heads));
+    if (window != nullptr && (window->window < 1 || window->sinks < 0))
+        return fail(BSA_ERR_INVALID_ARG, "window must be >= 1 and sinks >= 0");
+    if (tree != nullptr && !aligned(tree, 8)) return fail(BSA_ERR_ALIGNMENT, "tree is not 8-byte aligned");
+    if (tokens == 0) return ok();           // q and out may be empty then
+    BSA_TRY(check_queries(cache, q, q_stride, tokens, q_heads, scale, out,
+                          [&] { return check_lists(cu_tokens, start, table); }));
+    a.q = static_cast<const uint16_t *>(q);
+    a.q_stride = q_stride;
+    a.tokens = tokens;
+    a.seqs = seqs;
+    a.q_heads = q_heads;
+    a.cu = cu_tokens;
+    a.start = start;
+    a.table = table;
+    a.width = table_width;
+    a.tree = tree;
+    a.window = window != nullptr ? window->window : 0;
+    a.sinks = window != nullptr ? window->sinks : 0;
+    a.scale_log2 = paged_scale_log2(scale, cache.d);
+    a.out = static_cast<uint16_t *>(out);
+    a.status = device_status_ptr();
+    if (a.status == nullptr) return fail(BSA_ERR_CUDA, "status word unavailable");
+    return launched(bsa::launch_paged_attention(a, static_cast<cudaStream_t>(stream)), "attention launch");
+}
+
+bsa_status bsa_paged_attention(bsa_cache cache, const void *q, int64_t q_stride, int64_t tokens,
+                               int32_t q_heads, const int32_t *table, int32_t table_width,
+                               int64_t seqs, const int32_t *cu_tokens, const int32_t *start,
+                               const uint64_t *tree, const bsa_window *window, float scale,
+                               void *out, void *stream) {
+    bsa::AttentionArgs a = {};
+    BSA_TRY(cache_view(cache, &a.c));
+    return attention_impl(cache, a, q, q_stride, tokens, q_heads, table, table_width, seqs, cu_tokens,
+                          start, tree, window, scale, out, stream);
+}
+
+bsa_status bsa_paged_attention8(bsa_cache8 cache, const void *q, int64_t q_stride, int64_t tokens,
+                                int32_t q_heads, const int32_t *table, int32_t table_width,
+                                int64_t seqs, const int32_t *cu_tokens, const int32_t *start,
+                                const uint64_t *tree, const bsa_window *window, float scale,
+                                void *out, void *stream) {
+    bsa::Cache8View c;
+    BSA_TRY(cache8_view(cache, &c));
+    bsa::AttentionArgs a = {};
+    a.c = codes_view(c);
+    a.ks = c.ks;
+    a.vs = c.vs;
+    return attention_impl(cache, a, q, q_stride, tokens, q_heads, table, table_width, seqs, cu_tokens,
+                          start, tree, window, scale, out, stream);
+}
+
+extern "C" {
 
 // ------------------------------------------------------- failure path
 bsa_status bsa_selftest_wait_timeout(int32_t kind, uint64_t limit_ns, void *stream) {

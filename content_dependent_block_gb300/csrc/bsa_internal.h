@@ -223,8 +223,41 @@ cudaError_t launch_cache_append(const AppendArgs &a, cudaStream_t st);
 cudaError_t launch_copy_pages(const CacheView &c, const int32_t *pairs, int64_t count,
                               int32_t *status, cudaStream_t st);
 
+// The same in 8 bits: codes, and a scale for each row.
+struct Cache8View {
+    int8_t *k, *v;
+    float *ks, *vs;               // [num_pages][heads][page]
+    float *kbar;
+    int64_t num_pages;
+    int32_t heads, page, d;
+};
+struct Append8Args {
+    Cache8View c;
+    const uint16_t *k, *v;
+    int64_t k_stride, v_stride, tokens, seqs;
+    const int32_t *cu, *start, *table;
+    int32_t width;
+    int32_t *status;
+};
+cudaError_t launch_cache_append8(const Append8Args &a, cudaStream_t st);
+cudaError_t launch_copy_pages8(const Cache8View &c, const int32_t *pairs, int64_t count,
+                               int32_t *status, cudaStream_t st);
+struct ReadArgs {
+    const void *k, *v;            // bf16, or codes where the scales are not null
+    const float *ks, *vs;
+    int64_t num_pages;
+    int32_t heads, page, d;
+    int64_t tokens, seqs;
+    const int32_t *cu, *start, *table;
+    int32_t width;
+    uint16_t *k_out, *v_out;
+    int64_t token_stride, head_stride;
+    int32_t *status;
+};
+cudaError_t launch_cache_read(const ReadArgs &a, cudaStream_t st);
+
 struct DecodeArgs {
-    CacheView c;
+    CacheView c;                  // k and v are the codes where the scales are not null
     const uint16_t *q;            // [tokens][q_heads][d], token stride below
     int64_t q_stride, tokens, seqs;
     int32_t q_heads;
@@ -237,9 +270,37 @@ struct DecodeArgs {
     uint16_t *out;                // [tokens][q_heads][d]
     int32_t *idx;                 // optional [tokens][share ? heads : q_heads][topk]
     int32_t *status;
+    const float *ks, *vs;         // 8-bit pages: [num_pages][heads][page]
 };
 constexpr int32_t kDecodeMaxWidth = 16384;   // blocks of a sequence
 constexpr int32_t kDecodeMaxGroup = 128;     // query heads of a cache head
 cudaError_t launch_paged_decode(const DecodeArgs &a, cudaStream_t st);
+cudaError_t launch_paged_decode8(const DecodeArgs &a, cudaStream_t st);
+
+// Attention of new tokens over the paged cache, themselves in it.
+struct AttentionArgs {
+    CacheView c;                  // k and v are the codes where the scales are not null
+    const float *ks, *vs;
+    const uint16_t *q;            // [tokens][q_heads][d], token stride below
+    int64_t q_stride, tokens, seqs;
+    int32_t q_heads;
+    const int32_t *cu;            // [seqs + 1], or null: tokens / seqs each
+    const int32_t *start;         // [seqs] keys before the new tokens'
+    const int32_t *table;         // [seqs][width]
+    int32_t width;
+    const uint64_t *tree;         // [tokens] new tokens that each sees, or null: those up to itself
+    int32_t window, sinks;        // window 0: every key
+    float scale_log2;
+    uint16_t *out;                // [tokens][q_heads][d]
+    int32_t *status;
+};
+constexpr int32_t kTreeTokens = 64;
+constexpr int64_t kMostKeys = (int64_t(1) << 31) - 256;      // of a sequence that is attended to
+cudaError_t launch_paged_attention(const AttentionArgs &a, cudaStream_t st);
+// its form for at most sixteen query rows at a time, and the one for tiles of 128
+cudaError_t launch_attention_rows(const AttentionArgs &a, cudaStream_t st);
+cudaError_t launch_attention_rows8(const AttentionArgs &a, cudaStream_t st);
+cudaError_t launch_attention_tiles(const AttentionArgs &a, cudaStream_t st);
+cudaError_t launch_attention_tiles8(const AttentionArgs &a, cudaStream_t st);
 
 }  // namespace bsa

@@ -1,7 +1,8 @@
 /*
  * bsa.h -- C ABI of libbsa.so: content-dependent block-sparse attention on
  * one NVIDIA GB300 (sm_103a): the forward, its backward, rotary positions,
- * and decoding of single tokens over a paged cache.
+ * a paged cache in 16 or 8 bits, decoding of single tokens over it, and
+ * attention of new tokens to all of it, a window, or a tree.
  *
  * The method (page "sparse-attention-triton-bench", section "Two-stage
  * block indexer"):
@@ -561,6 +562,119 @@ bsa_status bsa_paged_decode(bsa_cache cache, const void *q, int64_t q_stride, in
                             int64_t seqs, const int32_t *token_seq, const int32_t *lens,
                             int32_t topk, const bsa_decode_options *options, float scale,
                             void *out, int32_t *idx_out, void *stream);
+
+/*
+ * The paged cache in 8 bits.  A row (one token's d channels of one head) is
+ * held as codes c_i = 127 x_i / a, rounded to the nearest whole number (ties
+ * to the even one), a = max |x_i|, and the scale a / 127: it stands for
+ * c_i * scale, off by a / 254 at most.  Codes are those of the exact quotients;
+ * a row of zeros has scale 0; a row with a value that is not finite has scale
+ * NaN (and codes 0), so all of it reads as NaN.
+ *   k, v              [num_pages][heads][page][d] int8 (device)
+ *   k_scale, v_scale  [num_pages][heads][page] fp32 (device)
+ *   kbar              [num_pages][heads][d] fp32 (device): the mean of what
+ *                     the page's filled rows stand for
+ * Sizes as bsa_cache.
+ */
+typedef struct {
+    int8_t *k;
+    int8_t *v;
+    float *k_scale;
+    float *v_scale;
+    float *kbar;
+    int64_t num_pages;
+    int32_t heads, page, d;
+} bsa_cache8;
+
+/*
+ * bsa_cache_append, bsa_cache_copy_pages and bsa_paged_decode over the 8-bit
+ * cache: arguments, results and errors are theirs.  Appending quantises the
+ * bf16 rows; copies take the codes, the scales and the means; decoding attends
+ * to what the rows stand for, exactly (no second rounding of K and V).
+ */
+bsa_status bsa_cache8_append(bsa_cache8 cache, const void *k, int64_t k_stride, const void *v,
+                             int64_t v_stride, int64_t tokens, int64_t seqs,
+                             const int32_t *cu_tokens, const int32_t *start,
+                             const int32_t *table, int32_t table_width, void *stream);
+bsa_status bsa_cache8_copy_pages(bsa_cache8 cache, const int32_t *pairs, int64_t count,
+                                 void *stream);
+bsa_status bsa_paged_decode8(bsa_cache8 cache, const void *q, int64_t q_stride, int64_t tokens,
+                             int32_t q_heads, const int32_t *table, int32_t table_width,
+                             int64_t seqs, const int32_t *token_seq, const int32_t *lens,
+                             int32_t topk, const bsa_decode_options *options, float scale,
+                             void *out, int32_t *idx_out, void *stream);
+
+/*
+ * Reads cached tokens back: positions [start[s], start[s] + n_s) of every
+ * sequence s, as bf16 rows (of an 8-bit cache code * scale in fp32, rounded
+ * once), for instance a prefix for bsa_forward.
+ *   tokens, cu_tokens, seqs, start, table, table_width  as bsa_cache_append;
+ *              token cu[s] + i of the output is position start[s] + i.
+ *   k, v       outputs (device) with the strides `out` in elements (batch is
+ *              ignored): [tokens][heads][d] has token = heads * d, head = d;
+ *              [heads][tokens][d] has token = d, head = tokens * d.  Strides
+ *              are multiples of 8, rows must not overlap, nor k, v and the
+ *              cache.
+ * A sequence whose tokens lie beyond its table is skipped and reported as
+ * BSA_ERR_INVALID_ARG, a page outside [0, num_pages) is skipped and reported
+ * as BSA_ERR_BAD_INDEX; rows that are skipped and tokens that no sequence has
+ * are left as they were.
+ */
+bsa_status bsa_cache_read(bsa_cache cache, int64_t tokens, int64_t seqs, const int32_t *cu_tokens,
+                          const int32_t *start, const int32_t *table, int32_t table_width,
+                          void *k, void *v, bsa_strides out, void *stream);
+bsa_status bsa_cache8_read(bsa_cache8 cache, int64_t tokens, int64_t seqs,
+                           const int32_t *cu_tokens, const int32_t *start, const int32_t *table,
+                           int32_t table_width, void *k, void *v, bsa_strides out, void *stream);
+
+/*
+ * Attention of new tokens to the cache that holds them (append first, with
+ * the same cu_tokens, start and table): the last token of each sequence, a
+ * prompt's chunk, or a tree of drafted tokens.  Nothing is selected; with a
+ * window it is what a sliding-window model does around the block selection
+ * (page "Block-Sparse & Linear Attention Kernels", section 2, sliding window).
+ * New token i of sequence s has its K and V at slot start[s] + i.
+ *   Without tree   its position is its slot, and it sees the keys of the
+ *                  slots up to its own.
+ *   tree           uint64 [tokens] (device), 8-byte aligned: bit j of token
+ *                  i's word says that it sees new token j of its sequence (its
+ *                  ancestors, and itself); it sees all keys of slots before
+ *                  start[s].  At most 64 new tokens each.  Its position is
+ *                  start[s] + the number of other new tokens it sees.
+ *   window         NULL: all of these.  Otherwise only those at positions
+ *                  above its own less `window`, and those below `sinks`
+ *                  (window >= 1, sinks >= 0).
+ *   q              [tokens][q_heads][d] bf16 (device); q_stride: elements from
+ *                  a token to the next (multiple of 8, >= q_heads * d).
+ *   scale          softmax scale; <= 0 selects 1/sqrt(d).
+ *   out            [tokens][q_heads][d] bf16 (device); not q, nor in the
+ *                  cache.  A token that sees no key gets zeros.
+ * q_heads a multiple of heads, at most 128 per cache head.  A masked key does
+ * not count whatever its K and V hold; a key of the cache that is not finite
+ * costs time where it is masked (its rows are computed again, one by one).
+ * A sequence with start below 0, more keys than its table has room for or
+ * than 2^31 - 256, or more than 64 new tokens and a tree, is skipped and
+ * reported as BSA_ERR_INVALID_ARG, like one whose cu_tokens make no sense; its
+ * rows, and those of tokens that no sequence has, are left as they were.
+ * The keys of a page outside [0, num_pages) are skipped and reported as
+ * BSA_ERR_BAD_INDEX; only pages that hold a key some row sees are looked up
+ * for certain.
+ */
+typedef struct {
+    int32_t window;
+    int32_t sinks;
+} bsa_window;
+
+bsa_status bsa_paged_attention(bsa_cache cache, const void *q, int64_t q_stride, int64_t tokens,
+                               int32_t q_heads, const int32_t *table, int32_t table_width,
+                               int64_t seqs, const int32_t *cu_tokens, const int32_t *start,
+                               const uint64_t *tree, const bsa_window *window, float scale,
+                               void *out, void *stream);
+bsa_status bsa_paged_attention8(bsa_cache8 cache, const void *q, int64_t q_stride, int64_t tokens,
+                                int32_t q_heads, const int32_t *table, int32_t table_width,
+                                int64_t seqs, const int32_t *cu_tokens, const int32_t *start,
+                                const uint64_t *tree, const bsa_window *window, float scale,
+                                void *out, void *stream);
 
 /*
  * Which sequence owns which page, on the host: page counts of references,
