@@ -1,0 +1,877 @@
+// New tokens over the paged cache, many query rows at a time, on the tensor
+// cores: prompts in chunks, trees of drafted tokens, many heads to a cache head
+// (the mathematics is in paged_attention.cuh).
+//
+// A tile is 128 query rows: the G heads that share a cache head, times 128 / G
+// tokens of one sequence.  K and V arrive in tiles of 128 keys, page by page
+// (TMA straight from the 16-bit pages; from 8-bit pages four warps turn the
+// codes into fp16 on the way, which is exact).  A CTA runs two streams of
+//   S = Q K^T (M 128, N 128, into tensor memory), softmax by one thread per
+//   row, P over the scores it came from, O += P V (N = d),
+// so that one stream's softmax runs under the other's products:
+//   pair  two tiles of rows over the same keys (K and V loaded once for 256
+//         rows), where that still gives every SM a CTA;
+//   dual  one tile of rows, the streams taking key tiles in turn and merged at
+//         the end; the keys may also be dealt to a cluster of CTAs, whose
+//         states are merged through shared memory.
+// The running maximum of a row follows only when it has grown by 2^8 (any
+// shift gives the same softmax; weights stay below 2^8), so O in tensor memory
+// is seldom rescaled.  Masks are bit sets of 32 keys, built only where a tile
+// is not seen whole.  Where the keys are split (dual) memory is the bound and P
+// is the sum of two bf16 numbers (off by 2^-18); in pairs it is one (2^-9, as in
+// the prompt's sparse forward), since a second product would cost a third of
+// the tensor time.  8-bit pages: P in fp16 as in paged_tiles.cuh.
+//
+//   warps 0-3, 4-7  softmax of streams 0 and 1
+//   warp 8          MMA: one thread issues whatever product is ready
+//   warp 9          producer (16-bit pages), or warps 9-12 (8-bit pages)
+#pragma once
+
+#include <algorithm>
+#include <atomic>
+
+#include <cooperative_groups.h>
+#include <cudaTypedefs.h>
+
+#include "bsa_device.cuh"
+#include "bsa_internal.h"
+#include "paged_common.cuh"
+#include "tc.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace bsa {
+namespace {
+
+constexpr int kRows = 128;               // rows of a stream
+constexpr int kKeys = 128;               // keys of a tile
+constexpr int kNotes = 16;               // tiles whose notes are kept: more than the ring holds
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr float kMinusInf = -__builtin_huge_valf();
+constexpr float kLazy = 8.f;             // growth of a row's maximum that is let pass, log2
+constexpr int kWeightShift = 6;          // 8-bit pages: weights times 2^(6 - E)
+
+template <int D, bool kPair, bool Q8>
+struct TCfg {
+    static constexpr int kSub = D / 64;
+    static constexpr int kPanel = kKeys * 128;              // 128 rows x 64 channels
+    static constexpr int kStage = kSub * kPanel;            // K or V of a tile, or a stream's Q
+    static constexpr int kStages = D == 64 ? 8 : kPair ? (Q8 ? 4 : 5) : (Q8 ? 5 : 6);
+    static constexpr int kQTiles = kPair ? 2 : 1;
+    static constexpr int kWarps = Q8 ? 13 : 10;
+    static constexpr int oQ = 0;
+    static constexpr int oRing = oQ + kQTiles * kStage;
+    static constexpr int oNotes = oRing + kStages * kStage; // uint32 [kNotes]: 16-key groups that are there
+    static constexpr int oTops = oNotes + kNotes * 4;       // uint32 [kNotes][4]: largest vs (bits)
+    static constexpr int oScales = oTops + (Q8 ? kNotes * 16 : 0);   // float [8][2][128]
+    static constexpr int oBar = oScales + (Q8 ? 8 * 2 * kKeys * 4 : 0);
+    static constexpr int oStat = oQ;                        // float2 [2][128], for the merge
+    enum { bQ = 0, bTail, bFull, bEmpty = bFull + kStages, bS = bEmpty + kStages, bP = bS + 2, bPv = bP + 2,
+           bCount = bPv + 2 };
+    static constexpr int oMisc = oBar + bCount * 8;
+    static constexpr int kTotal = oMisc + 16 + 1024;
+    static constexpr uint32_t cS = 0, cO = 2 * kKeys;       // columns of tensor memory
+    static constexpr int kOStride = D + 4;                  // floats of a row of the merge
+};
+static_assert(TCfg<128, true, false>::kTotal <= 227 * 1024 && TCfg<128, false, false>::kTotal <= 227 * 1024 &&
+                  TCfg<128, true, true>::kTotal <= 227 * 1024 && TCfg<128, false, true>::kTotal <= 227 * 1024,
+              "shared memory");
+static_assert(2 * kRows * TCfg<128, false, true>::kOStride * 4 <= TCfg<128, false, true>::kStages *
+                  TCfg<128, false, true>::kStage, "the merge uses the ring");
+static_assert(2 * kRows * TCfg<64, false, true>::kOStride * 4 <= TCfg<64, false, true>::kStages *
+                  TCfg<64, false, true>::kStage, "the merge uses the ring");
+static_assert(TCfg<128, true, false>::cO + 256 <= 512, "tensor memory");
+
+struct TilesPlan {
+    int64_t items_each;
+    int32_t cluster;
+    int32_t tokens;           // of a stream's tile: 128 / G, or as many as a sequence has
+    int32_t size;             // of a CTA's
+};
+
+__device__ __forceinline__ float exp2_ftz(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
+
+// Bits [lo, hi) of a word, the bounds clamped to [0, 32].
+__device__ __forceinline__ uint32_t bits_from_to(int lo, int hi) {
+    const int l = min(max(lo, 0), 32), h = min(max(hi, 0), 32);
+    if (l >= h) return 0u;
+    return (kAll >> (32 - h)) & (kAll << l);
+}
+
+// Which of the 32 keys from j on a row sees.
+__device__ __forceinline__ uint32_t seen_bits(const Sight &s, int32_t start, int32_t sinks, int32_t j) {
+    uint32_t m = bits_from_to(s.lo - j, s.hi - j) | bits_from_to(-j, min(sinks, s.hi) - j);
+    const int64_t off = int64_t(j) - start;
+    if (s.tree != 0 && off > -32 && off < 64)
+        m |= uint32_t(off >= 0 ? s.tree >> off : s.tree << -off);
+    return m;
+}
+
+// The tiles of keys that a CTA takes, of those that some of its rows see.
+struct KeyTiles {
+    int sinks, gap, first, count;
+    __device__ __forceinline__ KeyTiles(const Reach &r, int rank, int cluster) {
+        sinks = min((r.sinks_end + kKeys - 1) / kKeys, r.first / kKeys);
+        gap = r.first / kKeys - sinks;
+        const int all = (r.end + kKeys - 1) / kKeys - gap;
+        const int each = (all + cluster - 1) / cluster;
+        first = min(all, rank * each);
+        count = min(all, first + each) - first;
+    }
+    __device__ __forceinline__ int32_t key0(int i) const {
+        const int u = first + i;
+        return (u < sinks ? u : u + gap) * kKeys;
+    }
+};
+
+// Page of a tile's `i`-th page of `page` keys: -1 where no row sees any of it
+// (not looked up), -2 where it is not in the cache.
+__device__ __forceinline__ int32_t page_of(const AttentionArgs &a, const Reach &r, int32_t key0, int i) {
+    const int32_t k0 = key0 + i * a.c.page;
+    if (i * a.c.page >= kKeys || k0 >= r.end || (k0 >= r.sinks_end && k0 + a.c.page <= r.first)) return -1;
+    const int32_t pid = __ldg(a.table + r.seq * a.width + k0 / a.c.page);
+    if (pid >= 0 && pid < a.c.num_pages) return pid;
+    report_status(a.status, kStatusBadIndex);
+    return -2;
+}
+
+// A row by itself, by one warp: every key it sees, online in fp32; out[e] =
+// channel lane * D / 32 + e.  For rows whose tile's products met a masked value
+// that is not finite.
+template <int D>
+__device__ __noinline__ void row_alone(const AttentionArgs &a, const Reach &r, const Sight &s, int head,
+                                       const uint16_t *q_row, float (&out)[D / 32]) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    float q[E], m = kMinusInf, l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        q[e] = __uint_as_float(uint32_t(q_row[lane * E + e]) << 16);
+        out[e] = 0.f;
+    }
+    for (int32_t j = 0; j < r.end; j += 32) {
+        if (j >= r.sinks_end && j + 32 <= r.first) {
+            j = r.first / 32 * 32 - 32;
+            continue;
+        }
+        for (uint32_t left = seen_bits(s, int32_t(r.start), a.window > 0 ? a.sinks : 0, j); left != 0;
+             left &= left - 1) {
+            const int32_t key = j + __ffs(left) - 1;
+            const int32_t pid = a.table[r.seq * a.width + key / a.c.page];
+            if (pid < 0 || pid >= a.c.num_pages) continue;
+            const int64_t at = ((int64_t(pid) * a.c.heads + head) * a.c.page + key % a.c.page) * D + lane * E;
+            float x = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) x = fmaf(q[e], __uint_as_float(uint32_t(a.c.k[at + e]) << 16), x);
+            x = warp_sum(x) * a.scale_log2;
+            const float mn = fmaxf(m, x), base = mn == kMinusInf ? 0.f : mn;
+            const float corr = exp2_ftz(m - base), p = exp2_ftz(x - base);
+            m = mn;
+            l = fmaf(l, corr, p);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                out[e] = fmaf(p, __uint_as_float(uint32_t(a.c.v[at + e]) << 16), out[e] * corr);
+        }
+    }
+    const float inv = l > 0.f || l != l ? __fdiv_rn(1.f, l) : 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) out[e] *= inv;
+}
+
+// Sixteen codes of a key, as fp16, to their two chunks of a swizzled row.
+__device__ __forceinline__ void store_codes(uint8_t *row, int chunk, int r, const uint4 &x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t h[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t b = w[i] ^ 0x80808080u;              // a byte plus 128: the low byte of 1024 + it
+        const uint32_t lo = __byte_perm(b, 0x64646464u, 0x4140), hi = __byte_perm(b, 0x64646464u, 0x4342);
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h[2 * i]) : "r"(lo), "r"(0x64806480u));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h[2 * i + 1]) : "r"(hi), "r"(0x64806480u));
+    }
+    *reinterpret_cast<uint4 *>(row + ((chunk ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4 *>(row + (((chunk + 1) ^ (r & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+}
+
+template <int D, bool kPair, bool Q8>
+__global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
+    attention_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                           const AttentionArgs a, const TilesPlan p) {
+    using C = TCfg<D, kPair, Q8>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = tc::align_smem_1024(smem_raw);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + C::oBar);
+    uint32_t *notes = reinterpret_cast<uint32_t *>(sm + C::oNotes);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::oMisc);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = int(blockIdx.x % unsigned(p.cluster));
+    const unsigned cluster = blockIdx.x / unsigned(p.cluster);
+    const int64_t number = cluster / unsigned(a.c.heads);
+    const int head = int(cluster - unsigned(number) * unsigned(a.c.heads));
+    const int group = a.q_heads / a.c.heads;
+    int32_t *status = a.status;
+    check_bounds(a.cu, a.seqs, a.tokens, int64_t(blockIdx.x) * (C::kWarps * 32) + tid, status);
+    Reach r;
+    // the whole cluster leaves together
+    if (!find_reach(a, p.size, p.items_each, number, rank == 0 && tid == 0, &r)) return;
+    const int32_t sinks = a.window > 0 ? a.sinks : 0;
+    const KeyTiles tiles(r, rank, p.cluster);
+    const int n = tiles.count;
+    // rows and key tiles of a stream; key tile of its t-th step
+    const auto rows_of = [&](int s) {
+        return kPair ? max(0, min(p.tokens, r.nt - s * p.tokens)) * group : r.nt * group;
+    };
+    const auto steps_of = [&](int s) { return kPair ? (rows_of(s) > 0 ? n : 0) : (n + 1 - s) / 2; };
+    const auto tile_of = [&](int s, int t) { return kPair ? t : 2 * t + s; };
+
+    if (tid == 0) {
+        tc::mbar_init(bars + C::bQ, 256);
+        tc::mbar_init(bars + C::bTail, 1);
+        const uint32_t users = kPair && rows_of(1) > 0 ? 2 : 1;
+        for (int i = 0; i < C::kStages; ++i) {
+            tc::mbar_init(bars + C::bFull + i, Q8 ? 128 : 1);
+            tc::mbar_init(bars + C::bEmpty + i, users);
+        }
+        for (int s = 0; s < 2; ++s) {
+            tc::mbar_init(bars + C::bS + s, 1);
+            tc::mbar_init(bars + C::bP + s, kRows);
+            tc::mbar_init(bars + C::bPv + s, 1);
+        }
+        tc::fence_barrier_init();
+        if (!Q8) {
+            tc::prefetch_tensormap(&tm_k);
+            tc::prefetch_tensormap(&tm_v);
+        }
+    }
+    if (warp == 8) {
+        tc::tmem_alloc(tmem_slot, 512);
+        tc::tmem_relinquish();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const auto token_row = [&](int s, int row, int64_t stride) {
+        const int t = row / group;
+        return (r.lo + r.t0 + (kPair ? s * p.tokens : 0) + t) * stride + int64_t(head * group + row - t * group) * D;
+    };
+    const auto sight_at = [&](int s, int row) {
+        return sight_of(a, r.start, r.lo, r.n, min(r.n - 1, r.t0 + (kPair ? s * p.tokens : 0) + row / group));
+    };
+
+    if (warp < 8) {
+        // ---------------------------------------------------- softmax of stream s
+        const int s = warp >> 2, row = tid & 127;
+        const int rows = rows_of(s), steps = steps_of(s);
+        const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + C::cS + uint32_t(s * kKeys) + lane_off, tO = tmem + C::cO + uint32_t(s * D) + lane_off;
+        float back = a.scale_log2;                          // times a row's raw scores
+        {
+            // Q into shared memory, swizzled; the streams of one tile share the work
+            const bool there = row < rows;
+            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + token_row(s, there ? row : 0, a.q_stride));
+            uint8_t *dst = sm + C::oQ + (kPair ? s * C::kStage : 0) + row * 128;
+            float to = 1.f;
+            if (Q8) {
+                uint32_t top = 0u;
+#pragma unroll 4
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 x = there ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                                 __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+                }
+                // the power of two that brings the largest |q| to [2^14, 2^15), as in paged_tiles.cuh
+                const int e = min(max(int(max(top & 0xffffu, top >> 16) >> 7), 15), 254) - 127;
+                back *= exp2_int(e - 14);
+                to = exp2_int(14 - e);
+            }
+            constexpr int kChunks = D / 8, kMine = kPair ? kChunks : kChunks / 2;
+            const int c0 = kPair ? 0 : s * kMine;
+#pragma unroll 4
+            for (int c = c0; c < c0 + kMine; ++c) {
+                uint4 x = there ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+                if (Q8) {
+                    x.x = pack_f16x2(bf16_low_half(x.x) * to, bf16_high_half(x.x) * to);
+                    x.y = pack_f16x2(bf16_low_half(x.y) * to, bf16_high_half(x.y) * to);
+                    x.z = pack_f16x2(bf16_low_half(x.z) * to, bf16_high_half(x.z) * to);
+                    x.w = pack_f16x2(bf16_low_half(x.w) * to, bf16_high_half(x.w) * to);
+                }
+                *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::kPanel + (((c & 7) ^ (row & 7)) << 4)) = x;
+            }
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(bars + C::bQ);
+        }
+        const Sight sight = sight_at(s, max(0, min(row, rows - 1)));
+        const bool active = (warp & 3) * 32 < rows;         // any row in this warp
+        const int32_t lo_max = __reduce_max_sync(kAll, sight.lo), hi_min = __reduce_min_sync(kAll, sight.hi);
+        float m = kMinusInf, l = 0.f;
+        int big = -110;                                     // E of the weights (8-bit pages)
+        bool ok = true;
+        for (int t = 0; t < steps; ++t) {
+            const int i = tile_of(s, t);
+            const int32_t key0 = tiles.key0(i);
+            if (!tc::mbar_wait(bars + C::bS + s, t & 1, status)) {
+                ok = false;
+                break;
+            }
+            tc::tc_fence_after();
+            if (active) {
+                const uint32_t there = notes[i % kNotes];
+                const bool full = key0 >= lo_max && key0 + kKeys <= hi_min && there == 0xffu;
+                const float4 *ks = reinterpret_cast<const float4 *>(sm + C::oScales) + (i % 8) * 64, *vs = ks + 32;
+                const auto admitted = [&](int c) {
+                    const uint32_t g = there >> (2 * c);
+                    return seen_bits(sight, int32_t(r.start), sinks, key0 + c * 32) &
+                           ((g & 1u ? 0xffffu : 0u) | (g & 2u ? 0xffff0000u : 0u));
+                };
+                // the row's maximum
+                float top = kMinusInf;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t sv[32];
+                    tc::tmem_ld32(tS + uint32_t(c * 32), sv);
+                    tc::tmem_ld_wait();
+                    const uint32_t adm = full ? kAll : admitted(c);
+                    float mx[4] = {kMinusInf, kMinusInf, kMinusInf, kMinusInf};
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        float x[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(sv[j + e]);
+                        if (Q8) {
+                            const float4 k4 = ks[c * 8 + j / 4];
+                            x[0] *= k4.x * back;
+                            x[1] *= k4.y * back;
+                            x[2] *= k4.z * back;
+                            x[3] *= k4.w * back;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            mx[e] = fmaxf(mx[e], full || ((adm >> (j + e)) & 1u) ? x[e] : kMinusInf);
+                    }
+                    top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                }
+                if (!Q8) top *= back;
+                float corr = 1.f;
+                if (top > m + kLazy || m == kMinusInf) {
+                    const float mn = fmaxf(m, top);
+                    corr = mn == kMinusInf ? 1.f : exp2_ftz(m - mn);
+                    m = mn;
+                }
+                l *= corr;
+                float vf = 1.f;
+                if (Q8) {
+                    const uint4 tops = *reinterpret_cast<const uint4 *>(sm + C::oTops + (i % kNotes) * 16);
+                    const int e = min(int(max(max(tops.x, tops.y), max(tops.z, tops.w)) >> 23), 254) - 127;
+                    if (e > big) {
+                        corr *= exp2_int(max(big - e, -126));
+                        big = e;
+                    }
+                    vf = exp2_int(kWeightShift - big);
+                }
+                if (t > 0 && __any_sync(kAll, corr != 1.f)) {
+                    // the product of the last step is done: this one's scores came after it
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tc::tmem_ld32(tO + uint32_t(c), o);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
+                        uint32_t h[16];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) h[j] = o[16 * k + j];
+                            tc::tmem_st16(tO + uint32_t(c + 16 * k), h);
+                        }
+                    }
+                }
+                const float base = m == kMinusInf ? 0.f : m;
+                float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t sv[32], pk[16], lo[16];
+                    tc::tmem_ld32(tS + uint32_t(c * 32), sv);
+                    tc::tmem_ld_wait();
+                    const uint32_t adm = full ? kAll : admitted(c);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        float x[4];
+                        float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (Q8) k4 = ks[c * 8 + j / 4];
+                        const float kk[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            x[e] = exp2_ftz(fmaf(__uint_as_float(sv[j + e]), Q8 ? kk[e] * back : back, -base));
+                            if (!full && !((adm >> (j + e)) & 1u)) x[e] = 0.f;
+                            ls[e] += x[e];
+                        }
+                        if (Q8) {
+                            const float4 v4 = vs[c * 8 + j / 4];
+                            const float vv[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                x[e] *= vv[e] * vf;
+                                if (!full && !((adm >> (j + e)) & 1u)) x[e] = 0.f;
+                            }
+                            pk[j / 2] = pack_f16x2(x[0], x[1]);
+                            pk[j / 2 + 1] = pack_f16x2(x[2], x[3]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; e += 2) {
+                                const uint32_t w = pack_bf16x2(x[e], x[e + 1]);
+                                pk[(j + e) / 2] = w;
+                                if (!kPair) lo[(j + e) / 2] = pack_bf16x2(x[e] - bf16_low_half(w), x[e + 1] - bf16_high_half(w));
+                            }
+                        }
+                    }
+                    // P over the scores just read, what its rounding left behind it
+                    tc::tmem_st16(tS + uint32_t(c * 32), pk);
+                    if (!kPair && !Q8) tc::tmem_st16(tS + uint32_t(c * 32 + 16), lo);
+                }
+                l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                tc::tmem_st_wait();
+            }
+            tc::tc_fence_before();
+            tc::mbar_arrive(bars + C::bP + s);
+        }
+        if (ok && steps > 0 && !tc::mbar_wait(bars + C::bPv + s, (steps - 1) & 1, status)) ok = false;
+        tc::tc_fence_after();
+        const float un = Q8 ? exp2_int(big - kWeightShift) : 1.f;
+        if (kPair) {
+            const float inv = (l > 0.f || l != l ? __fdiv_rn(1.f, l) : 0.f) * un;
+            bool finite = true;
+            if (ok && active) {
+                uint16_t *dst = a.out + token_row(s, min(row, rows - 1), int64_t(a.q_heads) * D);
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    if (steps > 0) {
+                        tc::tmem_ld32(tO + uint32_t(c), o);
+                        tc::tmem_ld_wait();
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float x = steps > 0 && l != 0.f ? __uint_as_float(o[j]) * inv : 0.f;
+                        finite = finite && fabsf(x) < -kMinusInf;
+                        o[j] = __float_as_uint(x);
+                    }
+                    if (row < rows)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                w[j] = pack_bf16x2(__uint_as_float(o[8 * v + 2 * j]), __uint_as_float(o[8 * v + 2 * j + 1]));
+                            *reinterpret_cast<uint4 *>(dst + c + 8 * v) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                }
+                if (!Q8) {
+                    // a sum that is not a number comes from the row's own scores
+                    for (uint32_t again = __ballot_sync(kAll, row < rows && !finite && l == l); again != 0;
+                         again &= again - 1) {
+                        const int which = (warp & 3) * 32 + __ffs(again) - 1;
+                        float x[D / 32];
+                        row_alone<D>(a, r, sight_at(s, which), head, a.q + token_row(s, which, a.q_stride), x);
+                        uint16_t *to = a.out + token_row(s, which, int64_t(a.q_heads) * D) + lane * (D / 32);
+#pragma unroll
+                        for (int e = 0; e < D / 32; ++e) to[e] = f32_to_bf16_bits(x[e]);
+                    }
+                }
+            }
+        } else {
+            // the stream's state, for the merge: the ring is no longer read once
+            // both streams' products are done
+            tc::named_bar_sync(1, 256);
+            float2 *stat = reinterpret_cast<float2 *>(sm + C::oStat) + s * kRows;
+            const bool any = ok && steps > 0 && l != 0.f;
+            stat[row] = any ? make_float2(m, l) : make_float2(kMinusInf, 0.f);
+            float *dst = reinterpret_cast<float *>(sm + C::oRing) + (s * kRows + row) * C::kOStride;
+            if (ok && steps > 0 && active)
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tc::tmem_ld32(tO + uint32_t(c), o);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4)
+                        *reinterpret_cast<float4 *>(dst + c + j) =
+                            make_float4(__uint_as_float(o[j]) * un, __uint_as_float(o[j + 1]) * un,
+                                        __uint_as_float(o[j + 2]) * un, __uint_as_float(o[j + 3]) * un);
+                }
+        }
+        tc::tc_fence_before();
+    } else if (warp == 8) {
+        // ------------------------------------------------------------ MMA
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = Q8 ? tc::idesc_f16_f32(kRows, kKeys) : tc::idesc_bf16_f32(kRows, kKeys);
+            constexpr uint32_t idesc_o = Q8 ? tc::idesc_f16_f32(kRows, D, true) : tc::idesc_bf16_f32(kRows, D, true);
+            const uint32_t ring = tc::smem_u32(sm + C::oRing);
+            const int steps[2] = {steps_of(0), steps_of(1)};
+            int s_next[2] = {0, 0}, p_next[2] = {0, 0};
+            bool ok = tc::mbar_wait(bars + C::bQ, 0, status);
+            tc::tc_fence_after();
+            uint64_t t0 = 0;
+            uint32_t idle = 0;
+            while (ok && (p_next[0] < steps[0] || p_next[1] < steps[1])) {
+                bool moved = false;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const uint32_t tS = tmem + C::cS + uint32_t(s * kKeys), tO = tmem + C::cO + uint32_t(s * D);
+                    // O += P V, once P is written and V is there
+                    if (p_next[s] < s_next[s]) {
+                        const int t = p_next[s], i = tile_of(s, t), q = 2 * i + 1, st = q % C::kStages;
+                        if (tc::mbar_test_wait(bars + C::bP + s, t & 1) &&
+                            tc::mbar_test_wait(bars + C::bFull + st, (q / C::kStages) & 1) &&
+                            (Q8 || i < n - 1 || tc::mbar_test_wait(bars + C::bTail, 0))) {
+                            tc::tc_fence_after();
+                            const uint32_t av = ring + uint32_t(st * C::kStage);
+#pragma unroll
+                            for (int k = 0; k < kKeys / 16; ++k) {
+                                const uint64_t dv = tc::smem_desc_sw128_mn(av + k * 2048, C::kPanel, 1024);
+                                const uint32_t ap = tS + uint32_t((k >> 1) * 32 + (k & 1) * 8);
+                                tc::mma_bf16_ts(tO, ap, dv, idesc_o, (t > 0 || k > 0) ? 1u : 0u);
+                                if (!kPair && !Q8) tc::mma_bf16_ts(tO, ap + 16, dv, idesc_o, 1u);
+                            }
+                            tc::mma_commit(bars + C::bPv + s);
+                            tc::mma_commit(bars + C::bEmpty + st);
+                            ++p_next[s];
+                            moved = true;
+                        }
+                    }
+                    // S = Q K^T, once the product with the P that lies there is done
+                    if (s_next[s] < steps[s] && s_next[s] == p_next[s]) {
+                        const int t = s_next[s], i = tile_of(s, t), q = 2 * i, st = q % C::kStages;
+                        if ((t == 0 || tc::mbar_test_wait(bars + C::bPv + s, (t - 1) & 1)) &&
+                            tc::mbar_test_wait(bars + C::bFull + st, (q / C::kStages) & 1)) {
+                            tc::tc_fence_after();
+                            const uint32_t ak = ring + uint32_t(st * C::kStage);
+                            const uint32_t aq = tc::smem_u32(sm + C::oQ + (kPair ? s * C::kStage : 0));
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint32_t off = uint32_t((k >> 2) * C::kPanel + (k & 3) * 32);
+                                tc::mma_bf16(tS, tc::smem_desc_sw128(aq + off, 1024),
+                                             tc::smem_desc_sw128(ak + off, 1024), idesc_s, k > 0);
+                            }
+                            tc::mma_commit(bars + C::bS + s);
+                            tc::mma_commit(bars + C::bEmpty + st);
+                            ++s_next[s];
+                            moved = true;
+                        }
+                    }
+                }
+                if (moved) {
+                    idle = 0;
+                    t0 = 0;
+                } else if ((++idle & 1023u) == 0) {
+                    // bounded, as every wait
+                    if (*reinterpret_cast<volatile int32_t *>(status) == kStatusTimeout) break;
+                    const uint64_t now = tc::global_ns();
+                    if (t0 == 0) {
+                        t0 = now;
+                    } else if (now - t0 > tc::kWaitLimitNs) {
+                        report_status(status, kStatusTimeout);
+                        break;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (!Q8) {
+        // --------------------------------------- producer, 16-bit pages
+        const int pages = max(1, kKeys / a.c.page), per16 = a.c.page / 16;
+        int32_t next = n > 0 && lane < pages ? page_of(a, r, tiles.key0(0), lane) : -1;
+        bool ok = true;
+        for (int i = 0; i < n && ok; ++i) {
+            const int32_t mine = next;
+            if (i + 1 < n) next = lane < pages ? page_of(a, r, tiles.key0(i + 1), lane) : -1;
+            const uint32_t gone = __ballot_sync(kAll, mine == -2);
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const int q = 2 * i + v, st = q % C::kStages;
+                if (q >= C::kStages)
+                    ok = __all_sync(kAll, tc::mbar_wait(bars + C::bEmpty + st, (q / C::kStages - 1) & 1, status));
+                if (!ok) break;
+                if (lane == 0) {
+                    if (v == 0) {
+                        uint32_t there = 0xffu;
+                        for (uint32_t g = gone; g != 0; g &= g - 1)
+                            there &= ~(((1u << per16) - 1) << ((__ffs(g) - 1) * per16));
+                        notes[i % kNotes] = there;
+                    }
+                    tc::mbar_arrive_expect_tx(bars + C::bFull + st, C::kStage);
+                }
+                for (int g = 0; g < pages; ++g) {
+                    const int32_t pid = __shfl_sync(kAll, mine, g);
+                    if (lane == 0)
+#pragma unroll
+                        for (int sub = 0; sub < C::kSub; ++sub)     // what is not there arrives as zeros
+                            tc::tma_load_4d(sm + C::oRing + st * C::kStage + sub * C::kPanel + g * a.c.page * 128,
+                                            v == 0 ? &tm_k : &tm_v, bars + C::bFull + st, sub * 64, 0, head,
+                                            pid < 0 ? -1 : pid);
+                }
+            }
+        }
+        if (ok && n > 0) {
+            // rows past the last key hold anything, and 0 times NaN must not reach O
+            const int q = 2 * n - 1, st = q % C::kStages, tail = r.end - tiles.key0(n - 1);
+            if (tail < kKeys && tc::mbar_wait(bars + C::bFull + st, (q / C::kStages) & 1, status))
+                for (int i = lane; i < (kKeys - tail) * 8 * C::kSub; i += 32) {
+                    const int row = tail + i / (8 * C::kSub), c = i % (8 * C::kSub);
+                    *reinterpret_cast<uint4 *>(sm + C::oRing + st * C::kStage + (c >> 3) * C::kPanel + row * 128 +
+                                               (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(bars + C::bTail);
+        }
+    } else {
+        // --------------- producers, 8-bit pages: codes to fp16 on their way
+        constexpr int kPer = D / 16;                        // 16-byte loads of a row
+        constexpr int kLoads = kKeys * kPer / 128;
+        const int w = tid - 9 * 32, page = a.c.page;
+        const int shift = 31 - __clz(page);
+        float *scales = reinterpret_cast<float *>(sm + C::oScales);
+        // pages of tile i, one for each of eight lanes
+        const auto pages_of = [&](int i) {
+            return i < n && lane < 8 ? page_of(a, r, tiles.key0(i), lane) : -1;
+        };
+        // row x of tile i in the cache, or -1 if nothing sees it
+        const auto row_in = [&](int i, int32_t ids, int x) -> int64_t {
+            const int64_t pid = __shfl_sync(kAll, ids, x >> shift);
+            const int32_t key = tiles.key0(i) + x;
+            if (pid < 0 || key >= r.end || (key >= r.sinks_end && key < r.first)) return -1;
+            return (pid * a.c.heads + head) * page + (x & (page - 1));
+        };
+        const auto load = [&](int i, int32_t ids, bool v, uint4 (&x)[kLoads]) {
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int c = j * 128 + w;
+                const int64_t at = row_in(i, ids, c / kPer);
+                const int8_t *base = reinterpret_cast<const int8_t *>(v ? a.c.v : a.c.k);
+                x[j] = at >= 0 ? __ldg(reinterpret_cast<const uint4 *>(base + at * D) + c % kPer)
+                               : make_uint4(0u, 0u, 0u, 0u);
+            }
+        };
+        uint4 x[kLoads], y[kLoads];
+        float sk = 0.f, sv = 0.f;
+        const auto load_scales = [&](int i, int32_t ids) {
+            const int64_t at = row_in(i, ids, w);
+            sk = at >= 0 ? __ldg(a.ks + at) : 0.f;
+            sv = at >= 0 ? __ldg(a.vs + at) : 0.f;
+        };
+        const auto store = [&](int st, const uint4 (&z)[kLoads]) {
+            uint8_t *stage = sm + C::oRing + st * C::kStage;
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int c = j * 128 + w, row = c / kPer, ch = c % kPer;
+                store_codes(stage + (ch >> 2) * C::kPanel + row * 128, (ch & 3) * 2, row, z[j]);
+            }
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(bars + C::bFull + st);
+        };
+        int32_t ids = pages_of(0);
+        bool ok = true;
+        if (n > 0) {
+            load(0, ids, false, x);
+            load_scales(0, ids);
+        }
+        for (int i = 0; i < n && ok; ++i) {
+            load(i, ids, true, y);
+            int q = 2 * i, st = q % C::kStages;
+            if (q >= C::kStages) ok = tc::mbar_wait(bars + C::bEmpty + st, (q / C::kStages - 1) & 1, status);
+            ok = __all_sync(kAll, ok);
+            if (!ok) break;
+            const uint32_t gone = __ballot_sync(kAll, ids == -2);
+            scales[(i % 8) * 2 * kKeys + w] = sk;
+            scales[((i % 8) * 2 + 1) * kKeys + w] = sv;
+            const uint32_t bits = __float_as_uint(sv) & 0x7fffffffu;
+            const uint32_t top = __reduce_max_sync(kAll, sv == sv ? bits : 0u);
+            if (lane == 0) reinterpret_cast<uint32_t *>(sm + C::oTops)[(i % kNotes) * 4 + (w >> 5)] = top;
+            if (w == 0) {
+                uint32_t there = 0xffu;
+                for (uint32_t g = gone; g != 0; g &= g - 1)
+                    there &= ~(((1u << (page / 16)) - 1) << ((__ffs(g) - 1) * (page / 16)));
+                notes[i % kNotes] = there;
+            }
+            store(st, x);
+            ids = pages_of(i + 1);
+            if (i + 1 < n) {
+                load(i + 1, ids, false, x);
+                load_scales(i + 1, ids);
+            }
+            ++q;
+            st = q % C::kStages;
+            if (q >= C::kStages) ok = tc::mbar_wait(bars + C::bEmpty + st, (q / C::kStages - 1) & 1, status);
+            ok = __all_sync(kAll, ok);
+            if (!ok) break;
+            store(st, y);
+        }
+    }
+
+    if (!kPair) {
+        // rows are dealt to the cluster's CTAs and their warps; each merges the
+        // states of both streams of every CTA
+        cg::cluster_group peers = cg::this_cluster();
+        if (p.cluster > 1)
+            peers.sync();
+        else
+            __syncthreads();
+        const int rows = rows_of(0);
+        constexpr int E = D / 32;
+        for (int row = rank + p.cluster * warp; row < rows; row += p.cluster * C::kWarps) {
+            float2 st = make_float2(kMinusInf, 0.f);
+            if (lane < 2 * p.cluster)
+                st = *peers.map_shared_rank(reinterpret_cast<float2 *>(sm + C::oStat) + (lane & 1) * kRows + row, lane >> 1);
+            const float top = warp_max(st.x);
+            const float w = st.x == kMinusInf && st.y == 0.f ? 0.f : exp2_ftz(st.x - (top == kMinusInf ? 0.f : top));
+            const float l = warp_sum(w * st.y);
+            float x[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = 0.f;
+            for (int i = 0; i < 2 * p.cluster; ++i) {
+                const float wi = __shfl_sync(kAll, w, i);
+                if (__shfl_sync(kAll, st.y, i) == 0.f) continue;          // nothing there
+                const float *o = peers.map_shared_rank(
+                    reinterpret_cast<float *>(sm + C::oRing) + ((i & 1) * kRows + row) * C::kOStride, i >> 1);
+                if (E == 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(o + lane * 4);
+                    x[0] = fmaf(wi, v.x, x[0]);
+                    x[1] = fmaf(wi, v.y, x[1]);
+                    x[E - 2] = fmaf(wi, v.z, x[E - 2]);
+                    x[E - 1] = fmaf(wi, v.w, x[E - 1]);
+                } else {
+                    const float2 v = *reinterpret_cast<const float2 *>(o + lane * 2);
+                    x[0] = fmaf(wi, v.x, x[0]);
+                    x[E - 1] = fmaf(wi, v.y, x[E - 1]);
+                }
+            }
+            const float inv = l > 0.f || l != l ? __fdiv_rn(1.f, l) : 0.f;
+            bool finite = true;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                x[e] *= inv;
+                finite = finite && fabsf(x[e]) < -kMinusInf;
+            }
+            // a sum that is not a number comes from the row's own scores
+            if (!Q8 && l == l && !__all_sync(kAll, finite))
+                row_alone<D>(a, r, sight_at(0, row), head, a.q + token_row(0, row, a.q_stride), x);
+            uint16_t *to = a.out + token_row(0, row, int64_t(a.q_heads) * D) + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t *>(to + e) = pack_bf16x2(x[e], x[e + 1]);
+        }
+        if (p.cluster > 1) peers.sync();                    // peers read this CTA's shared memory
+    }
+    __syncthreads();
+    if (warp == 8) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 paged_encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult qr;
+        const bool found = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                                            &qr) == cudaSuccess && qr == cudaDriverEntryPointSuccess;
+        return found ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
+    }();
+    return fn;
+}
+
+// Pages as a 4-D tensor, box 64 channels x page rows, 128-byte swizzle.
+bool make_page_map(CUtensorMap *m, const void *base, const CacheView &c) {
+    auto fn = paged_encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t row = cuuint64_t(c.d) * 2;
+    cuuint64_t dims[4] = {cuuint64_t(c.d), cuuint64_t(c.page), cuuint64_t(c.heads), cuuint64_t(c.num_pages)};
+    cuuint64_t strides[3] = {row, row * c.page, row * c.page * c.heads};
+    cuuint32_t box[4] = {64, cuuint32_t(c.page), 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool kPair, bool Q8>
+cudaError_t launch_tiles(const AttentionArgs &a, const TilesPlan &p, int64_t items, cudaStream_t st) {
+    using C = TCfg<D, kPair, Q8>;
+    auto kernel = attention_tiles_kernel<D, kPair, Q8>;
+    // once per device: calls on other threads set the same values
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || ((ready.load() >> dev) & 1u) == 0u) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kTotal);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(uint64_t(1) << dev);
+    }
+    CUtensorMap mk = {}, mv = {};
+    if (!Q8 && (!make_page_map(&mk, a.c.k, a.c) || !make_page_map(&mv, a.c.v, a.c))) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(items * p.cluster));
+    cfg.blockDim = dim3(C::kWarps * 32);
+    cfg.dynamicSmemBytes = C::kTotal;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(p.cluster);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, mk, mv, a, p);
+    if (e != cudaSuccess) cudaGetLastError();           // reported here, not by the next launch
+    return e;
+}
+
+template <bool Q8>
+cudaError_t launch_tiles_form(const AttentionArgs &a, cudaStream_t st) {
+    const int group = a.q_heads / a.c.heads;
+    const int64_t mean = (a.tokens + a.seqs - 1) / a.seqs;
+    TilesPlan p;
+    const auto items_of = [&](int size) {
+        p.size = size;
+        p.items_each = (a.tokens / a.seqs + size - 1) / size;
+        return (a.cu != nullptr ? a.tokens / size + 2 * a.seqs : a.seqs * p.items_each) * a.c.heads;
+    };
+    p.tokens = std::max(1, kRows / group);
+    // pairs where they leave no SM without a CTA
+    int64_t items = items_of(2 * p.tokens);
+    const int64_t used = (a.tokens + 2 * p.tokens - 1) / (2 * p.tokens) * a.c.heads;
+    const bool pair = mean > p.tokens && used >= 96;
+    p.cluster = 1;
+    if (!pair) {
+        p.tokens = int32_t(std::min<int64_t>(p.tokens, mean));
+        items = items_of(p.tokens);
+        // the keys dealt to as many CTAs as leave all of them on the card at
+        // once, two tiles of keys for each at least
+        int64_t keys = int64_t(a.width) * a.c.page;
+        if (a.window > 0) keys = std::min<int64_t>(keys, int64_t(a.window) + a.sinks + p.tokens);
+        const int64_t busy = a.cu != nullptr ? (a.tokens / p.tokens + a.seqs) * a.c.heads : items;
+        const int limit[4] = {152, 76, 36, 15};
+        int log = 0;
+        while (log < 3 && busy <= limit[log + 1] && keys >= (int64_t(kKeys) << (log + 2))) ++log;
+        p.cluster = 1 << log;
+    }
+    if (items * p.cluster > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    if (a.c.d == 64) return pair ? launch_tiles<64, true, Q8>(a, p, items, st) : launch_tiles<64, false, Q8>(a, p, items, st);
+    return pair ? launch_tiles<128, true, Q8>(a, p, items, st) : launch_tiles<128, false, Q8>(a, p, items, st);
+}
+
+}  // namespace
+}  // namespace bsa

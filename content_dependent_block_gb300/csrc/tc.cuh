@@ -192,6 +192,16 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, u
         : "memory");
 }
 
+// 4-D tiled load.
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar,
+                                            int32_t x, int32_t y, int32_t z, int32_t w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
 // Four rows (y0..y3) of a 2-D tensor, columns [x, x + box width), written to
 // dst as four consecutive box rows (same swizzle as a 4-row tile load).  The
 // tensor map's box must be one row high.
@@ -369,6 +379,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int m, int n, bool b_mn_ma
            | (uint32_t(b_mn_major) << 16)     // B major-ness
            | (uint32_t(n >> 3) << 17)         // N / 8
            | (uint32_t(m >> 4) << 24);        // M / 16
+}
+
+// Same with fp16 operands.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n, bool b_mn_major = false) {
+    return idesc_bf16_f32(m, n, b_mn_major) & ~((1u << 7) | (1u << 10));
 }
 
 }  // namespace tc

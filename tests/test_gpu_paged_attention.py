@@ -162,6 +162,47 @@ def test_one_long_sequence(bits, group, new):
 
 
 @pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("d,page,heads,group", [(128, 64, 8, 2), (64, 16, 8, 3), (128, 128, 4, 5), (64, 32, 3, 16)])
+def test_many_rows(d, page, heads, group, bits):
+    """Enough rows that two tiles of them share their keys; the second may be
+    short or missing."""
+    start, new = [0, 100, 37, 513], [700, 128 // group * 3, 2 * (128 // group) * 3, 400]
+    step = Step(17, d, page, heads, group, bits, start, new)
+    step.check()
+    for window, sinks in ((150, 0), (90, 4), (300, 140)):
+        step.check(window=window, sinks=sinks, what=f"window {window}, sinks {sinks}")
+    assert bsa.device_status() == 0
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("d,group,seqs", [(128, 4, 24), (64, 7, 20)])
+def test_many_trees(d, group, seqs, bits):
+    g = torch.Generator().manual_seed(18)
+    start = torch.randint(0, 500, (seqs,), generator=g).tolist()
+    new = [64] * (seqs - 3) + [1, 40, 64]
+    step = Step(18, d, 32, 6, group, bits, start, new)
+    step.check(_trees(step.g, new))
+    step.check(_trees(step.g, new), window=70, sinks=5)
+    assert bsa.device_status() == 0
+
+
+def test_masked_values_that_are_not_finite_among_many_rows():
+    step = Step(19, 64, 16, 8, 4, 16, [70], [900])
+    for j, bad in ((3, float("inf")), (70, float("nan")), (500, float("-inf"))):
+        step.v[step.table[0][j // 16], :, j % 16, 5] = bad
+    got = bsa.paged_attention(step.cache(), step.q.cuda(), _i32(step.table), _i32([70]), window=101, sinks=3).cpu()
+    seen = att.sight(70, 900, None, 101, 3)
+    clean = step.v.clone()
+    clean[~torch.isfinite(clean)] = 0.0
+    want, tol = att.attention(step.k, clean, step.q, step.table, [0, 900], [70], None, 101, 3)
+    hit = seen[:, 3] | seen[:, 70] | seen[:, 500]
+    assert 100 < int(hit.sum()) < 800
+    assert bool(torch.isfinite(got[~hit]).all()) and not bool(torch.isfinite(got[hit][..., 5]).any())
+    ref.assert_within(got[~hit], want[~hit], tol[~hit], "rows that see none")
+    ref.assert_within(got[hit][..., 6:], want[hit][..., 6:], tol[hit][..., 6:], "other channels")
+
+
+@pytest.mark.parametrize("bits", [16, 8])
 def test_mixed_batch(bits):
     """Single tokens, drafts and a prompt in one call, tokens before the first
     sequence and behind the last, which stay as they were."""
