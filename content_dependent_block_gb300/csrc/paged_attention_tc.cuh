@@ -22,9 +22,13 @@
 // the prompt's sparse forward), since a second product would cost a third of
 // the tensor time.  8-bit pages: P in fp16 as in paged_tiles.cuh.
 //
-//   warps 0-3, 4-7  softmax of streams 0 and 1
-//   warp 8          MMA: one thread issues whatever product is ready
-//   warp 9          producer (16-bit pages), or warps 9-12 (8-bit pages)
+//   warps 0-7, 8-15  softmax of streams 0 and 1, two threads to a row, each with
+//                    half of a tile's keys: one thread's chain of loads, maxima
+//                    and exponentials is longer than both products
+//   warp 16          MMA, issued by one thread
+//   warp 18          producer: pages into the ring (16-bit), or codes and scales
+//                    into a ring of their own (8-bit)
+//   warps 20-23      8-bit pages: codes to fp16, into the ring
 #pragma once
 
 #include <algorithm>
@@ -45,6 +49,7 @@ namespace {
 
 constexpr int kRows = 128;               // rows of a stream
 constexpr int kKeys = 128;               // keys of a tile
+constexpr int kHalf = kKeys / 2;         // keys of a softmax thread
 constexpr int kNotes = 16;               // tiles whose notes are kept: more than the ring holds
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kMinusInf = -__builtin_huge_valf();
@@ -56,18 +61,22 @@ struct TCfg {
     static constexpr int kSub = D / 64;
     static constexpr int kPanel = kKeys * 128;              // 128 rows x 64 channels
     static constexpr int kStage = kSub * kPanel;            // K or V of a tile, or a stream's Q
-    static constexpr int kStages = D == 64 ? 8 : kPair ? (Q8 ? 4 : 5) : (Q8 ? 5 : 6);
+    static constexpr int kStages = D == 64 ? (Q8 ? 6 : 8) : kPair ? (Q8 ? 3 : 4) : (Q8 ? 4 : 5);
+    static constexpr int kRaw = !Q8 ? 0 : D == 64 ? 6 : 3;  // 8-bit pages: tiles of codes on their way
+    static constexpr int kRawStage = kKeys * D + 2 * kKeys * 4;     // codes, and with K the scales of both
     static constexpr int kQTiles = kPair ? 2 : 1;
-    static constexpr int kWarps = Q8 ? 13 : 10;
+    static constexpr int kWarps = Q8 ? 24 : 20;
     static constexpr int oQ = 0;
     static constexpr int oRing = oQ + kQTiles * kStage;
-    static constexpr int oNotes = oRing + kStages * kStage; // uint32 [kNotes]: 16-key groups that are there
-    static constexpr int oTops = oNotes + kNotes * 4;       // uint32 [kNotes][4]: largest vs (bits)
+    static constexpr int oRaw = oRing + kStages * kStage;
+    static constexpr int oNotes = oRaw + kRaw * kRawStage;  // uint32 [kNotes]: which 16-key groups are there
+    static constexpr int oTops = oNotes + kNotes * 4;       // uint32 [kNotes][4]: largest vs (bits) of a warp's rows
     static constexpr int oScales = oTops + (Q8 ? kNotes * 16 : 0);   // float [8][2][128]
-    static constexpr int oBar = oScales + (Q8 ? 8 * 2 * kKeys * 4 : 0);
+    static constexpr int oSwap = oScales + (Q8 ? 8 * 2 * kKeys * 4 : 0);     // float [2][2][128]
+    static constexpr int oBar = oSwap + 4 * kRows * 4;
     static constexpr int oStat = oQ;                        // float2 [2][128], for the merge
-    enum { bQ = 0, bTail, bFull, bEmpty = bFull + kStages, bS = bEmpty + kStages, bP = bS + 2, bPv = bP + 2,
-           bCount = bPv + 2 };
+    enum { bQ = 0, bTail, bFull, bEmpty = bFull + kStages, bRawFull = bEmpty + kStages, bRawEmpty = bRawFull + kRaw,
+           bS = bRawEmpty + kRaw, bP = bS + 2, bPv = bP + 2, bCount = bPv + 2 };
     static constexpr int oMisc = oBar + bCount * 8;
     static constexpr int kTotal = oMisc + 16 + 1024;
     static constexpr uint32_t cS = 0, cO = 2 * kKeys;       // columns of tensor memory
@@ -76,10 +85,13 @@ struct TCfg {
 static_assert(TCfg<128, true, false>::kTotal <= 227 * 1024 && TCfg<128, false, false>::kTotal <= 227 * 1024 &&
                   TCfg<128, true, true>::kTotal <= 227 * 1024 && TCfg<128, false, true>::kTotal <= 227 * 1024,
               "shared memory");
-static_assert(2 * kRows * TCfg<128, false, true>::kOStride * 4 <= TCfg<128, false, true>::kStages *
-                  TCfg<128, false, true>::kStage, "the merge uses the ring");
-static_assert(2 * kRows * TCfg<64, false, true>::kOStride * 4 <= TCfg<64, false, true>::kStages *
-                  TCfg<64, false, true>::kStage, "the merge uses the ring");
+template <int D, bool Q8>
+constexpr bool merge_fits() {
+    using C = TCfg<D, false, Q8>;
+    return 2 * kRows * C::kOStride * 4 <= C::oNotes - C::oRing;
+}
+static_assert(merge_fits<64, false>() && merge_fits<64, true>() && merge_fits<128, false>() && merge_fits<128, true>(),
+              "the merge uses the rings");
 static_assert(TCfg<128, true, false>::cO + 256 <= 512, "tensor memory");
 
 struct TilesPlan {
@@ -98,6 +110,38 @@ __device__ __forceinline__ float exp2_ftz(float x) {
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Two numbers at a time.
+__device__ __forceinline__ uint64_t as_pair(float2 x) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x.x), "f"(x.y));
+    return r;
+}
+__device__ __forceinline__ float2 of_pair(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(as_pair(x)), "l"(as_pair(y)), "l"(as_pair(z)));
+    return of_pair(r);
+}
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_pair(x)), "l"(as_pair(y)));
+    return of_pair(r);
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_pair(x)), "l"(as_pair(y)));
+    return of_pair(r);
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
     return r;
 }
 
@@ -237,16 +281,20 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
     const auto tile_of = [&](int s, int t) { return kPair ? t : 2 * t + s; };
 
     if (tid == 0) {
-        tc::mbar_init(bars + C::bQ, 256);
+        tc::mbar_init(bars + C::bQ, 512);
         tc::mbar_init(bars + C::bTail, 1);
         const uint32_t users = kPair && rows_of(1) > 0 ? 2 : 1;
         for (int i = 0; i < C::kStages; ++i) {
             tc::mbar_init(bars + C::bFull + i, Q8 ? 128 : 1);
             tc::mbar_init(bars + C::bEmpty + i, users);
         }
+        for (int i = 0; i < C::kRaw; ++i) {
+            tc::mbar_init(bars + C::bRawFull + i, 1);
+            tc::mbar_init(bars + C::bRawEmpty + i, 128);
+        }
         for (int s = 0; s < 2; ++s) {
             tc::mbar_init(bars + C::bS + s, 1);
-            tc::mbar_init(bars + C::bP + s, kRows);
+            tc::mbar_init(bars + C::bP + s, 2 * kRows);
             tc::mbar_init(bars + C::bPv + s, 1);
         }
         tc::fence_barrier_init();
@@ -255,7 +303,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
             tc::prefetch_tensormap(&tm_v);
         }
     }
-    if (warp == 8) {
+    if (warp == 16) {
         tc::tmem_alloc(tmem_slot, 512);
         tc::tmem_relinquish();
     }
@@ -271,15 +319,17 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
         return sight_of(a, r.start, r.lo, r.n, min(r.n - 1, r.t0 + (kPair ? s * p.tokens : 0) + row / group));
     };
 
-    if (warp < 8) {
-        // ---------------------------------------------------- softmax of stream s
-        const int s = warp >> 2, row = tid & 127;
+    if (warp < 16) {
+        // ------------- softmax of stream s; half h of a tile's keys, and of O's channels
+        const int s = warp >> 3, h = (warp >> 2) & 1, row = tid & 127;
         const int rows = rows_of(s), steps = steps_of(s);
         const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + C::cS + uint32_t(s * kKeys) + lane_off, tO = tmem + C::cO + uint32_t(s * D) + lane_off;
+        const uint32_t both = uint32_t(1 + s * 4 + (warp & 3));     // barrier of the two warps of 32 rows
+        float *swap = reinterpret_cast<float *>(sm + C::oSwap) + s * 2 * kRows + row;
         float back = a.scale_log2;                          // times a row's raw scores
         {
-            // Q into shared memory, swizzled; the streams of one tile share the work
+            // Q into shared memory, swizzled, by the threads of its rows (in dual of both streams)
             const bool there = row < rows;
             const uint4 *src = reinterpret_cast<const uint4 *>(a.q + token_row(s, there ? row : 0, a.q_stride));
             uint8_t *dst = sm + C::oQ + (kPair ? s * C::kStage : 0) + row * 128;
@@ -297,8 +347,8 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 back *= exp2_int(e - 14);
                 to = exp2_int(14 - e);
             }
-            constexpr int kChunks = D / 8, kMine = kPair ? kChunks : kChunks / 2;
-            const int c0 = kPair ? 0 : s * kMine;
+            constexpr int kMine = D / 8 / (kPair ? 2 : 4);
+            const int c0 = (kPair ? h : 2 * s + h) * kMine;
 #pragma unroll 4
             for (int c = c0; c < c0 + kMine; ++c) {
                 uint4 x = there ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
@@ -314,61 +364,81 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
             tc::mbar_arrive(bars + C::bQ);
         }
         const Sight sight = sight_at(s, max(0, min(row, rows - 1)));
-        const bool active = (warp & 3) * 32 < rows;         // any row in this warp
+        const bool active = (warp & 3) * 32 < rows;         // any row in this warp (and its other half)
         const int32_t lo_max = __reduce_max_sync(kAll, sight.lo), hi_min = __reduce_min_sync(kAll, sight.hi);
-        float m = kMinusInf, l = 0.f;
+        float m = kMinusInf, l = 0.f;                       // l over this thread's keys
         int big = -110;                                     // E of the weights (8-bit pages)
         bool ok = true;
         for (int t = 0; t < steps; ++t) {
             const int i = tile_of(s, t);
             const int32_t key0 = tiles.key0(i);
-            if (!tc::mbar_wait(bars + C::bS + s, t & 1, status)) {
-                ok = false;
-                break;
-            }
+            // a wait that ran out is on record, and the ones behind it end at
+            // once: the steps go on, so that the barriers below stay paired
+            ok &= tc::mbar_wait(bars + C::bS + s, t & 1, status);
             tc::tc_fence_after();
             if (active) {
-                const uint32_t there = notes[i % kNotes];
+                const uint32_t there = notes[i % kNotes] & 0xffu;
                 const bool full = key0 >= lo_max && key0 + kKeys <= hi_min && there == 0xffu;
-                const float4 *ks = reinterpret_cast<const float4 *>(sm + C::oScales) + (i % 8) * 64, *vs = ks + 32;
+                const float4 *ks = reinterpret_cast<const float4 *>(sm + C::oScales) + (i % 8) * 64 + h * 16;
+                const float2 *vs = reinterpret_cast<const float2 *>(ks + 32);
+                // scores of 32 keys, 8-bit pages in log2 units; masked ones -inf
+                const auto scores = [&](int c, float *x) {
+                    uint32_t raw[32];
+                    tc::tmem_ld32(tS + uint32_t(h * kHalf + c * 32), raw);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(raw[j]);
+                    if (Q8) {
+                        const float2 b2 = make_float2(back, back);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 k4 = ks[c * 8 + j / 4];
+                            const float2 y0 = mul2(make_float2(x[j], x[j + 1]), mul2(make_float2(k4.x, k4.y), b2));
+                            const float2 y1 = mul2(make_float2(x[j + 2], x[j + 3]), mul2(make_float2(k4.z, k4.w), b2));
+                            x[j] = y0.x;
+                            x[j + 1] = y0.y;
+                            x[j + 2] = y1.x;
+                            x[j + 3] = y1.y;
+                        }
+                    }
+                };
                 const auto admitted = [&](int c) {
-                    const uint32_t g = there >> (2 * c);
-                    return seen_bits(sight, int32_t(r.start), sinks, key0 + c * 32) &
+                    const uint32_t g = there >> (4 * h + 2 * c);
+                    return seen_bits(sight, int32_t(r.start), sinks, key0 + h * kHalf + c * 32) &
                            ((g & 1u ? 0xffffu : 0u) | (g & 2u ? 0xffff0000u : 0u));
                 };
-                // the row's maximum
-                float top = kMinusInf;
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t sv[32];
-                    tc::tmem_ld32(tS + uint32_t(c * 32), sv);
-                    tc::tmem_ld_wait();
-                    const uint32_t adm = full ? kAll : admitted(c);
-                    float mx[4] = {kMinusInf, kMinusInf, kMinusInf, kMinusInf};
+                const auto mask = [&](uint32_t adm, float *x) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        float x[4];
+                    for (int j = 0; j < 32; ++j)
+                        if (!((adm >> j) & 1u)) x[j] = kMinusInf;
+                };
+                // 16-bit pages: held from the maximum to the weights; 8-bit
+                // pages need the registers for the scales and read them twice
+                float x[kHalf];
+                float mx[4] = {kMinusInf, kMinusInf, kMinusInf, kMinusInf};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(sv[j + e]);
-                        if (Q8) {
-                            const float4 k4 = ks[c * 8 + j / 4];
-                            x[0] *= k4.x * back;
-                            x[1] *= k4.y * back;
-                            x[2] *= k4.z * back;
-                            x[3] *= k4.w * back;
-                        }
+                for (int c = 0; c < 2; ++c) {
+                    float *y = x + (Q8 ? 0 : c * 32);
+                    scores(c, y);
+                    if (!full) mask(admitted(c), y);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            mx[e] = fmaxf(mx[e], full || ((adm >> (j + e)) & 1u) ? x[e] : kMinusInf);
-                    }
-                    top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                    for (int j = 0; j < 32; j += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], y[j + e], y[j + 4 + e]);
                 }
+                // the row's maximum, once one half's has grown enough
+                float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
                 if (!Q8) top *= back;
                 float corr = 1.f;
-                if (top > m + kLazy || m == kMinusInf) {
-                    const float mn = fmaxf(m, top);
-                    corr = mn == kMinusInf ? 1.f : exp2_ftz(m - mn);
-                    m = mn;
+                if (!tc::named_bar_and(both, 64, !(top > m + kLazy || m == kMinusInf))) {
+                    swap[h * kRows] = top;
+                    tc::named_bar_sync(both, 64);
+                    top = fmaxf(top, swap[(1 - h) * kRows]);
+                    if (top > m + kLazy || m == kMinusInf) {
+                        const float mn = fmaxf(m, top);
+                        corr = mn == kMinusInf ? 1.f : exp2_ftz(m - mn);
+                        m = mn;
+                    }
                 }
                 l *= corr;
                 float vf = 1.f;
@@ -384,65 +454,56 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 if (t > 0 && __any_sync(kAll, corr != 1.f)) {
                     // the product of the last step is done: this one's scores came after it
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tc::tmem_ld32(tO + uint32_t(c), o);
+                    for (int c = h * (D / 2); c < (h + 1) * (D / 2); c += 16) {
+                        uint32_t o[16];
+                        tc::tmem_ld16(tO + uint32_t(c), o);
                         tc::tmem_ld_wait();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
-                        uint32_t h[16];
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) h[j] = o[16 * k + j];
-                            tc::tmem_st16(tO + uint32_t(c + 16 * k), h);
-                        }
+                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
+                        tc::tmem_st16(tO + uint32_t(c), o);
                     }
                 }
                 const float base = m == kMinusInf ? 0.f : m;
-                float ls[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t sv[32], pk[16], lo[16];
-                    tc::tmem_ld32(tS + uint32_t(c * 32), sv);
-                    tc::tmem_ld_wait();
-                    const uint32_t adm = full ? kAll : admitted(c);
+                const float2 b2 = make_float2(back, back), n2 = make_float2(-base, -base);
+                float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t pk[16], lo[16];
+                    const uint32_t adm = Q8 && !full ? admitted(c) : kAll;
+                    if (Q8) {
+                        scores(c, x);
+                        if (!full) mask(adm, x);
+                    }
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
-                        float x[4];
-                        float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (Q8) k4 = ks[c * 8 + j / 4];
-                        const float kk[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            x[e] = exp2_ftz(fmaf(__uint_as_float(sv[j + e]), Q8 ? kk[e] * back : back, -base));
-                            if (!full && !((adm >> (j + e)) & 1u)) x[e] = 0.f;
-                            ls[e] += x[e];
-                        }
-                        if (Q8) {
-                            const float4 v4 = vs[c * 8 + j / 4];
-                            const float vv[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                x[e] *= vv[e] * vf;
-                                if (!full && !((adm >> (j + e)) & 1u)) x[e] = 0.f;
-                            }
-                            pk[j / 2] = pack_f16x2(x[0], x[1]);
-                            pk[j / 2 + 1] = pack_f16x2(x[2], x[3]);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 4; e += 2) {
-                                const uint32_t w = pack_bf16x2(x[e], x[e + 1]);
+                        for (int e = 0; e < 4; e += 2) {
+                            const int k = c * 32 + j + e, at = Q8 ? j + e : k;
+                            float2 y = make_float2(x[at], x[at + 1]);
+                            y = Q8 ? add2(y, n2) : fma2(y, b2, n2);
+                            y.x = exp2_ftz(y.x);
+                            y.y = exp2_ftz(y.y);
+                            ls[e / 2] = add2(ls[e / 2], y);
+                            if (Q8) {
+                                const float2 v2 = vs[k / 2];
+                                y = mul2(y, mul2(v2, make_float2(vf, vf)));
+                                if (!full) {                // the scale of a masked key may be anything
+                                    if (!((adm >> (j + e)) & 1u)) y.x = 0.f;
+                                    if (!((adm >> (j + e + 1)) & 1u)) y.y = 0.f;
+                                }
+                                pk[(j + e) / 2] = pack_f16x2(y.x, y.y);
+                            } else {
+                                const uint32_t w = pack_bf16x2(y.x, y.y);
                                 pk[(j + e) / 2] = w;
-                                if (!kPair) lo[(j + e) / 2] = pack_bf16x2(x[e] - bf16_low_half(w), x[e + 1] - bf16_high_half(w));
+                                if (!kPair) lo[(j + e) / 2] = pack_bf16x2(y.x - bf16_low_half(w), y.y - bf16_high_half(w));
                             }
                         }
                     }
-                    // P over the scores just read, what its rounding left behind it
-                    tc::tmem_st16(tS + uint32_t(c * 32), pk);
-                    if (!kPair && !Q8) tc::tmem_st16(tS + uint32_t(c * 32 + 16), lo);
+                    // P over the scores, and what its rounding left behind it
+                    tc::tmem_st16(tS + uint32_t(h * kHalf + c * 32), pk);
+                    if (!kPair && !Q8) tc::tmem_st16(tS + uint32_t(h * kHalf + c * 32 + 16), lo);
                 }
-                l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
                 tc::tmem_st_wait();
             }
             tc::tc_fence_before();
@@ -451,21 +512,22 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
         if (ok && steps > 0 && !tc::mbar_wait(bars + C::bPv + s, (steps - 1) & 1, status)) ok = false;
         tc::tc_fence_after();
         const float un = Q8 ? exp2_int(big - kWeightShift) : 1.f;
+        swap[h * kRows] = l;                                // (last read before the last step's first barrier)
+        tc::named_bar_sync(both, 64);
+        l += swap[(1 - h) * kRows];
         if (kPair) {
             const float inv = (l > 0.f || l != l ? __fdiv_rn(1.f, l) : 0.f) * un;
             bool finite = true;
             if (ok && active) {
                 uint16_t *dst = a.out + token_row(s, min(row, rows - 1), int64_t(a.q_heads) * D);
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
+                for (int c = h * (D / 2); c < (h + 1) * (D / 2); c += 32) {
                     uint32_t o[32];
-                    if (steps > 0) {
-                        tc::tmem_ld32(tO + uint32_t(c), o);
-                        tc::tmem_ld_wait();
-                    }
+                    tc::tmem_ld32(tO + uint32_t(c), o);
+                    tc::tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        const float x = steps > 0 && l != 0.f ? __uint_as_float(o[j]) * inv : 0.f;
+                        const float x = l != 0.f ? __uint_as_float(o[j]) * inv : 0.f;
                         finite = finite && fabsf(x) < -kMinusInf;
                         o[j] = __float_as_uint(x);
                     }
@@ -487,22 +549,24 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                         float x[D / 32];
                         row_alone<D>(a, r, sight_at(s, which), head, a.q + token_row(s, which, a.q_stride), x);
                         uint16_t *to = a.out + token_row(s, which, int64_t(a.q_heads) * D) + lane * (D / 32);
+                        if (lane >> 4 == h)
 #pragma unroll
-                        for (int e = 0; e < D / 32; ++e) to[e] = f32_to_bf16_bits(x[e]);
+                            for (int e = 0; e < D / 32; ++e) to[e] = f32_to_bf16_bits(x[e]);
                     }
                 }
             }
         } else {
-            // the stream's state, for the merge: the ring is no longer read once
-            // both streams' products are done
-            tc::named_bar_sync(1, 256);
-            float2 *stat = reinterpret_cast<float2 *>(sm + C::oStat) + s * kRows;
+            // the stream's state, for the merge: nothing reads Q and the rings
+            // once both streams' products are done
+            tc::named_bar_sync(9, 512);
             const bool any = ok && steps > 0 && l != 0.f;
-            stat[row] = any ? make_float2(m, l) : make_float2(kMinusInf, 0.f);
+            if (h == 0)
+                reinterpret_cast<float2 *>(sm + C::oStat)[s * kRows + row] =
+                    any ? make_float2(m, l) : make_float2(kMinusInf, 0.f);
             float *dst = reinterpret_cast<float *>(sm + C::oRing) + (s * kRows + row) * C::kOStride;
             if (ok && steps > 0 && active)
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
+                for (int c = h * (D / 2); c < (h + 1) * (D / 2); c += 32) {
                     uint32_t o[32];
                     tc::tmem_ld32(tO + uint32_t(c), o);
                     tc::tmem_ld_wait();
@@ -514,211 +578,189 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 }
         }
         tc::tc_fence_before();
-    } else if (warp == 8) {
-        // ------------------------------------------------------------ MMA
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = Q8 ? tc::idesc_f16_f32(kRows, kKeys) : tc::idesc_bf16_f32(kRows, kKeys);
-            constexpr uint32_t idesc_o = Q8 ? tc::idesc_f16_f32(kRows, D, true) : tc::idesc_bf16_f32(kRows, D, true);
-            const uint32_t ring = tc::smem_u32(sm + C::oRing);
-            const int steps[2] = {steps_of(0), steps_of(1)};
-            int s_next[2] = {0, 0}, p_next[2] = {0, 0};
-            bool ok = tc::mbar_wait(bars + C::bQ, 0, status);
-            tc::tc_fence_after();
-            uint64_t t0 = 0;
-            uint32_t idle = 0;
-            while (ok && (p_next[0] < steps[0] || p_next[1] < steps[1])) {
-                bool moved = false;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const uint32_t tS = tmem + C::cS + uint32_t(s * kKeys), tO = tmem + C::cO + uint32_t(s * D);
-                    // O += P V, once P is written and V is there
-                    if (p_next[s] < s_next[s]) {
-                        const int t = p_next[s], i = tile_of(s, t), q = 2 * i + 1, st = q % C::kStages;
-                        if (tc::mbar_test_wait(bars + C::bP + s, t & 1) &&
-                            tc::mbar_test_wait(bars + C::bFull + st, (q / C::kStages) & 1) &&
-                            (Q8 || i < n - 1 || tc::mbar_test_wait(bars + C::bTail, 0))) {
-                            tc::tc_fence_after();
-                            const uint32_t av = ring + uint32_t(st * C::kStage);
-#pragma unroll
-                            for (int k = 0; k < kKeys / 16; ++k) {
-                                const uint64_t dv = tc::smem_desc_sw128_mn(av + k * 2048, C::kPanel, 1024);
-                                const uint32_t ap = tS + uint32_t((k >> 1) * 32 + (k & 1) * 8);
-                                tc::mma_bf16_ts(tO, ap, dv, idesc_o, (t > 0 || k > 0) ? 1u : 0u);
-                                if (!kPair && !Q8) tc::mma_bf16_ts(tO, ap + 16, dv, idesc_o, 1u);
-                            }
-                            tc::mma_commit(bars + C::bPv + s);
-                            tc::mma_commit(bars + C::bEmpty + st);
-                            ++p_next[s];
-                            moved = true;
-                        }
-                    }
-                    // S = Q K^T, once the product with the P that lies there is done
-                    if (s_next[s] < steps[s] && s_next[s] == p_next[s]) {
-                        const int t = s_next[s], i = tile_of(s, t), q = 2 * i, st = q % C::kStages;
-                        if ((t == 0 || tc::mbar_test_wait(bars + C::bPv + s, (t - 1) & 1)) &&
-                            tc::mbar_test_wait(bars + C::bFull + st, (q / C::kStages) & 1)) {
-                            tc::tc_fence_after();
-                            const uint32_t ak = ring + uint32_t(st * C::kStage);
-                            const uint32_t aq = tc::smem_u32(sm + C::oQ + (kPair ? s * C::kStage : 0));
-#pragma unroll
-                            for (int k = 0; k < D / 16; ++k) {
-                                const uint32_t off = uint32_t((k >> 2) * C::kPanel + (k & 3) * 32);
-                                tc::mma_bf16(tS, tc::smem_desc_sw128(aq + off, 1024),
-                                             tc::smem_desc_sw128(ak + off, 1024), idesc_s, k > 0);
-                            }
-                            tc::mma_commit(bars + C::bS + s);
-                            tc::mma_commit(bars + C::bEmpty + st);
-                            ++s_next[s];
-                            moved = true;
-                        }
-                    }
-                }
-                if (moved) {
-                    idle = 0;
-                    t0 = 0;
-                } else if ((++idle & 1023u) == 0) {
-                    // bounded, as every wait
-                    if (*reinterpret_cast<volatile int32_t *>(status) == kStatusTimeout) break;
-                    const uint64_t now = tc::global_ns();
-                    if (t0 == 0) {
-                        t0 = now;
-                    } else if (now - t0 > tc::kWaitLimitNs) {
-                        report_status(status, kStatusTimeout);
-                        break;
-                    }
-                }
-            }
-        }
-        __syncwarp();
-    } else if (!Q8) {
-        // --------------------------------------- producer, 16-bit pages
-        const int pages = max(1, kKeys / a.c.page), per16 = a.c.page / 16;
-        int32_t next = n > 0 && lane < pages ? page_of(a, r, tiles.key0(0), lane) : -1;
-        bool ok = true;
-        for (int i = 0; i < n && ok; ++i) {
-            const int32_t mine = next;
-            if (i + 1 < n) next = lane < pages ? page_of(a, r, tiles.key0(i + 1), lane) : -1;
-            const uint32_t gone = __ballot_sync(kAll, mine == -2);
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const int q = 2 * i + v, st = q % C::kStages;
-                if (q >= C::kStages)
-                    ok = __all_sync(kAll, tc::mbar_wait(bars + C::bEmpty + st, (q / C::kStages - 1) & 1, status));
-                if (!ok) break;
-                if (lane == 0) {
-                    if (v == 0) {
-                        uint32_t there = 0xffu;
-                        for (uint32_t g = gone; g != 0; g &= g - 1)
-                            there &= ~(((1u << per16) - 1) << ((__ffs(g) - 1) * per16));
-                        notes[i % kNotes] = there;
-                    }
-                    tc::mbar_arrive_expect_tx(bars + C::bFull + st, C::kStage);
-                }
-                for (int g = 0; g < pages; ++g) {
-                    const int32_t pid = __shfl_sync(kAll, mine, g);
-                    if (lane == 0)
-#pragma unroll
-                        for (int sub = 0; sub < C::kSub; ++sub)     // what is not there arrives as zeros
-                            tc::tma_load_4d(sm + C::oRing + st * C::kStage + sub * C::kPanel + g * a.c.page * 128,
-                                            v == 0 ? &tm_k : &tm_v, bars + C::bFull + st, sub * 64, 0, head,
-                                            pid < 0 ? -1 : pid);
-                }
-            }
-        }
-        if (ok && n > 0) {
-            // rows past the last key hold anything, and 0 times NaN must not reach O
-            const int q = 2 * n - 1, st = q % C::kStages, tail = r.end - tiles.key0(n - 1);
-            if (tail < kKeys && tc::mbar_wait(bars + C::bFull + st, (q / C::kStages) & 1, status))
-                for (int i = lane; i < (kKeys - tail) * 8 * C::kSub; i += 32) {
-                    const int row = tail + i / (8 * C::kSub), c = i % (8 * C::kSub);
-                    *reinterpret_cast<uint4 *>(sm + C::oRing + st * C::kStage + (c >> 3) * C::kPanel + row * 128 +
-                                               (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                }
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(bars + C::bTail);
-        }
     } else {
-        // --------------- producers, 8-bit pages: codes to fp16 on their way
-        constexpr int kPer = D / 16;                        // 16-byte loads of a row
-        constexpr int kLoads = kKeys * kPer / 128;
-        const int w = tid - 9 * 32, page = a.c.page;
-        const int shift = 31 - __clz(page);
-        float *scales = reinterpret_cast<float *>(sm + C::oScales);
-        // pages of tile i, one for each of eight lanes
-        const auto pages_of = [&](int i) {
-            return i < n && lane < 8 ? page_of(a, r, tiles.key0(i), lane) : -1;
-        };
-        // row x of tile i in the cache, or -1 if nothing sees it
-        const auto row_in = [&](int i, int32_t ids, int x) -> int64_t {
-            const int64_t pid = __shfl_sync(kAll, ids, x >> shift);
-            const int32_t key = tiles.key0(i) + x;
-            if (pid < 0 || key >= r.end || (key >= r.sinks_end && key < r.first)) return -1;
-            return (pid * a.c.heads + head) * page + (x & (page - 1));
-        };
-        const auto load = [&](int i, int32_t ids, bool v, uint4 (&x)[kLoads]) {
+        if (warp == 16) {
+            // ---------------------------------------------- MMA of both streams
+            if (lane == 0) {
+                constexpr uint32_t idesc_s = Q8 ? tc::idesc_f16_f32(kRows, kKeys) : tc::idesc_bf16_f32(kRows, kKeys);
+                constexpr uint32_t idesc_o = Q8 ? tc::idesc_f16_f32(kRows, D, true) : tc::idesc_bf16_f32(kRows, D, true);
+                const uint32_t ring = tc::smem_u32(sm + C::oRing);
+                // S = Q K^T of a stream's step t, once the product with the P that lies there is done
+                const auto scores = [&](int s, int t) {
+                    const int q = 2 * tile_of(s, t), st = q % C::kStages;
+                    if (!tc::mbar_wait(bars + C::bFull + st, (q / C::kStages) & 1, status)) return false;
+                    if (t > 0 && !tc::mbar_wait(bars + C::bPv + s, (t - 1) & 1, status)) return false;
+                    tc::tc_fence_after();
+                    const uint32_t ak = ring + uint32_t(st * C::kStage);
+                    const uint32_t aq = tc::smem_u32(sm + C::oQ + (kPair ? s * C::kStage : 0));
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                const int c = j * 128 + w;
-                const int64_t at = row_in(i, ids, c / kPer);
-                const int8_t *base = reinterpret_cast<const int8_t *>(v ? a.c.v : a.c.k);
-                x[j] = at >= 0 ? __ldg(reinterpret_cast<const uint4 *>(base + at * D) + c % kPer)
-                               : make_uint4(0u, 0u, 0u, 0u);
-            }
-        };
-        uint4 x[kLoads], y[kLoads];
-        float sk = 0.f, sv = 0.f;
-        const auto load_scales = [&](int i, int32_t ids) {
-            const int64_t at = row_in(i, ids, w);
-            sk = at >= 0 ? __ldg(a.ks + at) : 0.f;
-            sv = at >= 0 ? __ldg(a.vs + at) : 0.f;
-        };
-        const auto store = [&](int st, const uint4 (&z)[kLoads]) {
-            uint8_t *stage = sm + C::oRing + st * C::kStage;
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = uint32_t((k >> 2) * C::kPanel + (k & 3) * 32);
+                        tc::mma_bf16(tmem + C::cS + uint32_t(s * kKeys), tc::smem_desc_sw128(aq + off, 1024),
+                                     tc::smem_desc_sw128(ak + off, 1024), idesc_s, k > 0);
+                    }
+                    tc::mma_commit(bars + C::bS + s);
+                    tc::mma_commit(bars + C::bEmpty + st);
+                    return true;
+                };
+                // O += P V, once V is there and P is written
+                const auto output = [&](int s, int t) {
+                    const int i = tile_of(s, t), q = 2 * i + 1, st = q % C::kStages;
+                    if (!tc::mbar_wait(bars + C::bFull + st, (q / C::kStages) & 1, status)) return false;
+                    if (!Q8 && i == n - 1 && !tc::mbar_wait(bars + C::bTail, 0, status)) return false;
+                    if (!tc::mbar_wait(bars + C::bP + s, t & 1, status)) return false;
+                    tc::tc_fence_after();
+                    const uint32_t av = ring + uint32_t(st * C::kStage);
+                    const uint32_t tO = tmem + C::cO + uint32_t(s * D);
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                const int c = j * 128 + w, row = c / kPer, ch = c % kPer;
-                store_codes(stage + (ch >> 2) * C::kPanel + row * 128, (ch & 3) * 2, row, z[j]);
+                    for (int k = 0; k < kKeys / 16; ++k) {
+                        const uint64_t dv = tc::smem_desc_sw128_mn(av + k * 2048, C::kPanel, 1024);
+                        const uint32_t ap = tmem + C::cS + uint32_t(s * kKeys + (k >> 1) * 32 + (k & 1) * 8);
+                        tc::mma_bf16_ts(tO, ap, dv, idesc_o, (t > 0 || k > 0) ? 1u : 0u);
+                        if (!kPair && !Q8) tc::mma_bf16_ts(tO, ap + 16, dv, idesc_o, 1u);
+                    }
+                    tc::mma_commit(bars + C::bPv + s);
+                    tc::mma_commit(bars + C::bEmpty + st);
+                    return true;
+                };
+                // A stream's product and its next scores go in one after the
+                // other, the streams in turn: issued as they come, both
+                // streams' products would interleave, end together and leave
+                // the tensor cores idle while both wait for their softmax.
+                const int steps[2] = {steps_of(0), steps_of(1)};
+                bool ok = steps[0] == 0 || tc::mbar_wait(bars + C::bQ, 0, status);
+                for (int s = 0; s < 2; ++s) ok = ok && (steps[s] == 0 || scores(s, 0));
+                for (int t = 0; ok && t < steps[0]; ++t)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        ok = ok && (t >= steps[s] || output(s, t));
+                        ok = ok && (t + 1 >= steps[s] || scores(s, t + 1));
+                    }
             }
-            tc::fence_proxy_async_smem();
-            tc::mbar_arrive(bars + C::bFull + st);
-        };
-        int32_t ids = pages_of(0);
-        bool ok = true;
-        if (n > 0) {
-            load(0, ids, false, x);
-            load_scales(0, ids);
-        }
-        for (int i = 0; i < n && ok; ++i) {
-            load(i, ids, true, y);
-            int q = 2 * i, st = q % C::kStages;
-            if (q >= C::kStages) ok = tc::mbar_wait(bars + C::bEmpty + st, (q / C::kStages - 1) & 1, status);
-            ok = __all_sync(kAll, ok);
-            if (!ok) break;
-            const uint32_t gone = __ballot_sync(kAll, ids == -2);
-            scales[(i % 8) * 2 * kKeys + w] = sk;
-            scales[((i % 8) * 2 + 1) * kKeys + w] = sv;
-            const uint32_t bits = __float_as_uint(sv) & 0x7fffffffu;
-            const uint32_t top = __reduce_max_sync(kAll, sv == sv ? bits : 0u);
-            if (lane == 0) reinterpret_cast<uint32_t *>(sm + C::oTops)[(i % kNotes) * 4 + (w >> 5)] = top;
-            if (w == 0) {
-                uint32_t there = 0xffu;
-                for (uint32_t g = gone; g != 0; g &= g - 1)
-                    there &= ~(((1u << (page / 16)) - 1) << ((__ffs(g) - 1) * (page / 16)));
-                notes[i % kNotes] = there;
+            __syncwarp();
+        } else if (warp == 18) {
+            // ------------------------------------------------------- producer
+            const int pages = kKeys / a.c.page, per16 = a.c.page / 16, tiles_at_once = 32 / pages;
+            // pages of the tiles from i on, one to a lane
+            const auto look_up = [&](int i) {
+                const int u = i + lane / pages;
+                return u < n ? page_of(a, r, tiles.key0(u), lane % pages) : -1;
+            };
+            int32_t ids = -1, next = look_up(0);
+            bool ok = true;
+            for (int i = 0; i < n && ok; ++i) {
+                const int at = i % tiles_at_once * pages;
+                if (at == 0) {
+                    ids = next;
+                    next = look_up(i + tiles_at_once);
+                }
+                const uint32_t group_bits = pages == 32 ? kAll : (1u << pages) - 1;
+                const uint32_t gone = (__ballot_sync(kAll, ids == -2) >> at) & group_bits;
+                const uint32_t here = (__ballot_sync(kAll, ids >= 0) >> at) & group_bits;
+                // groups of 16 keys: bits 0-7 not known to be gone, 8-15 copied
+                uint32_t note = 0xffu;
+                for (int g = 0; g < pages; ++g) {
+                    const uint32_t bits = ((1u << per16) - 1) << (g * per16);
+                    if ((gone >> g) & 1u) note &= ~bits;
+                    if ((here >> g) & 1u) note |= bits << 8;
+                }
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    constexpr int kSlots = Q8 ? C::kRaw : C::kStages;
+                    const int q = 2 * i + v, st = q % (Q8 ? C::kRaw : C::kStages);
+                    uint64_t *full = bars + (Q8 ? C::bRawFull : C::bFull) + st;
+                    if (q >= kSlots)
+                        ok = __all_sync(kAll, tc::mbar_wait(bars + (Q8 ? C::bRawEmpty : C::bEmpty) + st,
+                                                            (q / kSlots - 1) & 1, status));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        if (v == 0) notes[i % kNotes] = note;
+                        tc::mbar_arrive_expect_tx(
+                            full, Q8 ? uint32_t(__popc(here) * a.c.page * (D + (v == 0 ? 8 : 0))) : uint32_t(C::kStage));
+                    }
+                    __syncwarp();
+                    for (int g = 0; g < pages; ++g) {
+                        const int32_t pid = __shfl_sync(kAll, ids, at + g);
+                        if (lane != 0) continue;
+                        if (Q8) {
+                            if (pid < 0) continue;
+                            const int64_t row0 = (int64_t(pid) * a.c.heads + head) * a.c.page;
+                            uint8_t *dst = sm + C::oRaw + st * C::kRawStage;
+                            tc::bulk_g2s(dst + g * a.c.page * D,
+                                         reinterpret_cast<const int8_t *>(v == 0 ? a.c.k : a.c.v) + row0 * D,
+                                         uint32_t(a.c.page * D), full);
+                            if (v == 0) {
+                                float *sc = reinterpret_cast<float *>(dst + kKeys * D) + g * a.c.page;
+                                tc::bulk_g2s(sc, a.ks + row0, uint32_t(a.c.page * 4), full);
+                                tc::bulk_g2s(sc + kKeys, a.vs + row0, uint32_t(a.c.page * 4), full);
+                            }
+                        } else {
+#pragma unroll
+                            for (int sub = 0; sub < C::kSub; ++sub)     // what is not there arrives as zeros
+                                tc::tma_load_4d(sm + C::oRing + st * C::kStage + sub * C::kPanel + g * a.c.page * 128,
+                                                v == 0 ? &tm_k : &tm_v, full, sub * 64, 0, head, pid < 0 ? -1 : pid);
+                        }
+                    }
+                    __syncwarp();
+                }
             }
-            store(st, x);
-            ids = pages_of(i + 1);
-            if (i + 1 < n) {
-                load(i + 1, ids, false, x);
-                load_scales(i + 1, ids);
+            if (!Q8 && ok && n > 0) {
+                // rows past the last key hold anything, and 0 times NaN must not reach O
+                const int q = 2 * n - 1, st = q % C::kStages, tail = r.end - tiles.key0(n - 1);
+                if (tail < kKeys && tc::mbar_wait(bars + C::bFull + st, (q / C::kStages) & 1, status))
+                    for (int i = lane; i < (kKeys - tail) * 8 * C::kSub; i += 32) {
+                        const int row = tail + i / (8 * C::kSub), c = i % (8 * C::kSub);
+                        *reinterpret_cast<uint4 *>(sm + C::oRing + st * C::kStage + (c >> 3) * C::kPanel + row * 128 +
+                                                   (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(bars + C::bTail);
             }
-            ++q;
-            st = q % C::kStages;
-            if (q >= C::kStages) ok = tc::mbar_wait(bars + C::bEmpty + st, (q / C::kStages - 1) & 1, status);
-            ok = __all_sync(kAll, ok);
-            if (!ok) break;
-            store(st, y);
+        } else if (Q8 && warp >= 20) {
+            // --------------------------- codes to fp16, rows that nothing sees to zero
+            constexpr int kPer = D / 16;                    // 16-byte pieces of a row
+            const int w = tid - 20 * 32;
+            float *scales = reinterpret_cast<float *>(sm + C::oScales);
+            constexpr int kSlots = C::kRaw > 0 ? C::kRaw : 1;
+            for (int i = 0; i < n; ++i) {
+                const int32_t key0 = tiles.key0(i);
+                bool ok = true;
+                uint32_t note = 0u;
+                const auto seen = [&](int x) {
+                    const int32_t key = key0 + x;
+                    return ((note >> (8 + x / 16)) & 1u) && key < r.end && (key < r.sinks_end || key >= r.first);
+                };
+#pragma unroll 1
+                for (int v = 0; v < 2; ++v) {
+                    const int q = 2 * i + v, raw = q % kSlots, st = q % C::kStages;
+                    ok = tc::mbar_wait(bars + C::bRawFull + raw, (q / kSlots) & 1, status) &&
+                         (q < C::kStages || tc::mbar_wait(bars + C::bEmpty + st, (q / C::kStages - 1) & 1, status));
+                    if (!__all_sync(kAll, ok)) break;
+                    const uint8_t *src = sm + C::oRaw + raw * C::kRawStage;
+                    uint8_t *stage = sm + C::oRing + st * C::kStage;
+                    note = notes[i % kNotes];
+                    if (v == 0) {
+                        const float *sc = reinterpret_cast<const float *>(src + kKeys * D);
+                        const float sk = seen(w) ? sc[w] : 0.f, sv = seen(w) ? sc[kKeys + w] : 0.f;
+                        scales[(i % 8) * 2 * kKeys + w] = sk;
+                        scales[((i % 8) * 2 + 1) * kKeys + w] = sv;
+                        const uint32_t top = __reduce_max_sync(kAll, sv == sv ? __float_as_uint(sv) & 0x7fffffffu : 0u);
+                        if (lane == 0) reinterpret_cast<uint32_t *>(sm + C::oTops)[(i % kNotes) * 4 + (w >> 5)] = top;
+                    }
+#pragma unroll 4
+                    for (int j = 0; j < kPer; ++j) {
+                        const int c = j * 128 + w, row = c / kPer, ch = c % kPer;
+                        const uint4 x = seen(row) ? *reinterpret_cast<const uint4 *>(src + c * 16)
+                                                  : make_uint4(0u, 0u, 0u, 0u);
+                        store_codes(stage + (ch >> 2) * C::kPanel + row * 128, (ch & 3) * 2, row, x);
+                    }
+                    tc::fence_proxy_async_smem();
+                    tc::mbar_arrive(bars + C::bFull + st);
+                    tc::mbar_arrive(bars + C::bRawEmpty + raw);
+                }
+                if (!__all_sync(kAll, ok)) break;
+            }
         }
     }
 
@@ -776,7 +818,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
         if (p.cluster > 1) peers.sync();                    // peers read this CTA's shared memory
     }
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 16) {
         tc::tc_fence_after();
         tc::tmem_dealloc(tmem, 512);
     }
