@@ -25,7 +25,8 @@
 //   warps 0-7, 8-15  softmax of streams 0 and 1, two threads to a row, each with
 //                    half of a tile's keys: one thread's chain of loads, maxima
 //                    and exponentials is longer than both products
-//   warp 16          MMA, issued by one thread
+//   warps 16, 17     MMA of streams 0 and 1, each issued by one thread (in dual one
+//                    thread issues both; in pair it would wait where it could issue)
 //   warp 18          producer: pages into the ring (16-bit), or codes and scales
 //                    into a ring of their own (8-bit)
 //   warps 20-23      8-bit pages: codes to fp16, into the ring
@@ -61,38 +62,43 @@ struct TCfg {
     static constexpr int kSub = D / 64;
     static constexpr int kPanel = kKeys * 128;              // 128 rows x 64 channels
     static constexpr int kStage = kSub * kPanel;            // K or V of a tile, or a stream's Q
-    static constexpr int kStages = D == 64 ? (Q8 ? 6 : 8) : kPair ? (Q8 ? 3 : 4) : (Q8 ? 4 : 5);
-    static constexpr int kRaw = !Q8 ? 0 : D == 64 ? 6 : 3;  // 8-bit pages: tiles of codes on their way
+    static constexpr int kStages = D == 64 ? (Q8 ? 4 : 7) : Q8 ? 2 : kPair ? 3 : 4;
+    static constexpr int kRaw = !Q8 ? 0 : D == 64 ? 5 : 3;  // 8-bit pages: tiles of codes on their way
     static constexpr int kRawStage = kKeys * D + 2 * kKeys * 4;     // codes, and with K the scales of both
+    static constexpr bool kPShared = D == 128;              // P in shared memory, else in tensor memory
+    static constexpr int kPBytes = 2 * kPanel;              // 128 rows x 128 keys
     static constexpr int kQTiles = kPair ? 2 : 1;
     static constexpr int kWarps = Q8 ? 24 : 20;
     static constexpr int oQ = 0;
-    static constexpr int oRing = oQ + kQTiles * kStage;
+    static constexpr int oP = oQ + kQTiles * kStage;
+    static constexpr int oRing = oP + (kPShared ? 2 * kPBytes : 0);
     static constexpr int oRaw = oRing + kStages * kStage;
     static constexpr int oNotes = oRaw + kRaw * kRawStage;  // uint32 [kNotes]: which 16-key groups are there
     static constexpr int oTops = oNotes + kNotes * 4;       // uint32 [kNotes][4]: largest vs (bits) of a warp's rows
     static constexpr int oScales = oTops + (Q8 ? kNotes * 16 : 0);   // float [8][2][128]
-    static constexpr int oSwap = oScales + (Q8 ? 8 * 2 * kKeys * 4 : 0);     // float [2][2][128]
-    static constexpr int oBar = oSwap + 4 * kRows * 4;
-    static constexpr int oStat = oQ;                        // float2 [2][128], for the merge
+    static constexpr int oSwap = oScales + (Q8 ? 8 * 2 * kKeys * 4 : 0);     // uint32 [2][128]: the rows' maxima
+    static constexpr int oBar = oSwap + 2 * kRows * 4;
+    static constexpr int oStat = oQ;                        // float2 [2][128] and float [2][2][128], for the merge
     enum { bQ = 0, bTail, bFull, bEmpty = bFull + kStages, bRawFull = bEmpty + kStages, bRawEmpty = bRawFull + kRaw,
-           bS = bRawEmpty + kRaw, bP = bS + 2, bPv = bP + 2, bCount = bPv + 2 };
+           bS = bRawEmpty + kRaw, bSFree = bS + 2, bP = bSFree + 2, bPv = bP + 2, bCount = bPv + 2 };
     static constexpr int oMisc = oBar + bCount * 8;
     static constexpr int kTotal = oMisc + 16 + 1024;
-    static constexpr uint32_t cS = 0, cO = 2 * kKeys;       // columns of tensor memory
+    static constexpr uint32_t cS = 0, cO = 2 * kKeys, cP = cO + 2 * D;      // columns of tensor memory
     static constexpr int kOStride = D + 4;                  // floats of a row of the merge
 };
 static_assert(TCfg<128, true, false>::kTotal <= 227 * 1024 && TCfg<128, false, false>::kTotal <= 227 * 1024 &&
-                  TCfg<128, true, true>::kTotal <= 227 * 1024 && TCfg<128, false, true>::kTotal <= 227 * 1024,
+                  TCfg<128, false, true>::kTotal <= 227 * 1024 && TCfg<64, true, false>::kTotal <= 227 * 1024 &&
+                  TCfg<64, false, false>::kTotal <= 227 * 1024 && TCfg<64, true, true>::kTotal <= 227 * 1024 &&
+                  TCfg<64, false, true>::kTotal <= 227 * 1024,
               "shared memory");
 template <int D, bool Q8>
 constexpr bool merge_fits() {
     using C = TCfg<D, false, Q8>;
-    return 2 * kRows * C::kOStride * 4 <= C::oNotes - C::oRing;
+    return 2 * kRows * C::kOStride * 4 <= C::oNotes - C::oP && 4 * kRows * 8 <= C::kStage;
 }
 static_assert(merge_fits<64, false>() && merge_fits<64, true>() && merge_fits<128, false>() && merge_fits<128, true>(),
-              "the merge uses the rings");
-static_assert(TCfg<128, true, false>::cO + 256 <= 512, "tensor memory");
+              "the merge uses P and the rings");
+static_assert(TCfg<128, true, false>::cO + 256 <= 512 && TCfg<64, true, false>::cP + 128 <= 512, "tensor memory");
 
 struct TilesPlan {
     int64_t items_each;
@@ -143,6 +149,15 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
     return r;
+}
+
+// Order-preserving image of a number, above 0; and back.
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t u = __float_as_uint(x);
+    return u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float of_ordered(uint32_t u) {
+    return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
@@ -294,6 +309,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
         }
         for (int s = 0; s < 2; ++s) {
             tc::mbar_init(bars + C::bS + s, 1);
+            tc::mbar_init(bars + C::bSFree + s, 2 * kRows);
             tc::mbar_init(bars + C::bP + s, 2 * kRows);
             tc::mbar_init(bars + C::bPv + s, 1);
         }
@@ -303,6 +319,8 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
             tc::prefetch_tensormap(&tm_v);
         }
     }
+    uint32_t *tops_so_far = reinterpret_cast<uint32_t *>(sm + C::oSwap);
+    if (tid < 2 * kRows) tops_so_far[tid] = 0u;             // below every number
     if (warp == 16) {
         tc::tmem_alloc(tmem_slot, 512);
         tc::tmem_relinquish();
@@ -319,6 +337,21 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
         return sight_of(a, r.start, r.lo, r.n, min(r.n - 1, r.t0 + (kPair ? s * p.tokens : 0) + row / group));
     };
 
+    // The order in which K and V tiles are loaded and used: the scores of a
+    // step are issued before the products of the one before it.
+    const auto schedule = [](int count, const auto &use) {
+        constexpr int kAhead = kPair ? 1 : 2;               // tiles of a step
+        int q = 0;
+        for (int i = 0; i < min(kAhead, count); ++i)
+            if (!use(false, i, q++)) return;
+        for (int i0 = 0; i0 < count; i0 += kAhead) {
+            for (int i = i0 + kAhead; i < min(i0 + 2 * kAhead, count); ++i)
+                if (!use(false, i, q++)) return;
+            for (int i = i0; i < min(i0 + kAhead, count); ++i)
+                if (!use(true, i, q++)) return;
+        }
+    };
+
     if (warp < 16) {
         // ------------- softmax of stream s; half h of a tile's keys, and of O's channels
         const int s = warp >> 3, h = (warp >> 2) & 1, row = tid & 127;
@@ -326,7 +359,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
         const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + C::cS + uint32_t(s * kKeys) + lane_off, tO = tmem + C::cO + uint32_t(s * D) + lane_off;
         const uint32_t both = uint32_t(1 + s * 4 + (warp & 3));     // barrier of the two warps of 32 rows
-        float *swap = reinterpret_cast<float *>(sm + C::oSwap) + s * 2 * kRows + row;
+        uint32_t *shared_top = tops_so_far + s * kRows + row;
         float back = a.scale_log2;                          // times a row's raw scores
         {
             // Q into shared memory, swizzled, by the threads of its rows (in dual of both streams)
@@ -381,7 +414,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 const bool full = key0 >= lo_max && key0 + kKeys <= hi_min && there == 0xffu;
                 const float4 *ks = reinterpret_cast<const float4 *>(sm + C::oScales) + (i % 8) * 64 + h * 16;
                 const float2 *vs = reinterpret_cast<const float2 *>(ks + 32);
-                // scores of 32 keys, 8-bit pages in log2 units; masked ones -inf
+                // scores of 32 keys, in log2 units (8-bit pages)
                 const auto scores = [&](int c, float *x) {
                     uint32_t raw[32];
                     tc::tmem_ld32(tS + uint32_t(h * kHalf + c * 32), raw);
@@ -416,10 +449,20 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 // pages need the registers for the scales and read them twice
                 float x[kHalf];
                 float mx[4] = {kMinusInf, kMinusInf, kMinusInf, kMinusInf};
+                if (!Q8) {
+                    uint32_t raw[2][32];
+                    tc::tmem_ld32(tS + uint32_t(h * kHalf), raw[0]);
+                    tc::tmem_ld32(tS + uint32_t(h * kHalf + 32), raw[1]);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < kHalf; ++j) x[j] = __uint_as_float(raw[j / 32][j % 32]);
+                    tc::tc_fence_before();
+                    tc::mbar_arrive(bars + C::bSFree + s);  // the next scores may come
+                }
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     float *y = x + (Q8 ? 0 : c * 32);
-                    scores(c, y);
+                    if (Q8) scores(c, y);
                     if (!full) mask(admitted(c), y);
 #pragma unroll
                     for (int j = 0; j < 32; j += 8)
@@ -431,9 +474,10 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 if (!Q8) top *= back;
                 float corr = 1.f;
                 if (!tc::named_bar_and(both, 64, !(top > m + kLazy || m == kMinusInf))) {
-                    swap[h * kRows] = top;
+                    // the larger of the two halves' (it only grows from step to step)
+                    atomicMax(shared_top, ordered(top));
                     tc::named_bar_sync(both, 64);
-                    top = fmaxf(top, swap[(1 - h) * kRows]);
+                    top = of_ordered(*shared_top);
                     if (top > m + kLazy || m == kMinusInf) {
                         const float mn = fmaxf(m, top);
                         corr = mn == kMinusInf ? 1.f : exp2_ftz(m - mn);
@@ -451,27 +495,19 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                     }
                     vf = exp2_int(kWeightShift - big);
                 }
-                if (t > 0 && __any_sync(kAll, corr != 1.f)) {
-                    // the product of the last step is done: this one's scores came after it
-#pragma unroll 1
-                    for (int c = h * (D / 2); c < (h + 1) * (D / 2); c += 16) {
-                        uint32_t o[16];
-                        tc::tmem_ld16(tO + uint32_t(c), o);
-                        tc::tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
-                        tc::tmem_st16(tO + uint32_t(c), o);
-                    }
-                }
                 const float base = m == kMinusInf ? 0.f : m;
                 const float2 b2 = make_float2(back, back), n2 = make_float2(-base, -base);
                 float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                uint32_t pk[kHalf / 2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    uint32_t pk[16], lo[16];
                     const uint32_t adm = Q8 && !full ? admitted(c) : kAll;
                     if (Q8) {
                         scores(c, x);
+                        if (c == 1) {
+                            tc::tc_fence_before();
+                            tc::mbar_arrive(bars + C::bSFree + s);
+                        }
                         if (!full) mask(adm, x);
                     }
 #pragma unroll
@@ -491,28 +527,62 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                                     if (!((adm >> (j + e)) & 1u)) y.x = 0.f;
                                     if (!((adm >> (j + e + 1)) & 1u)) y.y = 0.f;
                                 }
-                                pk[(j + e) / 2] = pack_f16x2(y.x, y.y);
+                                pk[k / 2] = pack_f16x2(y.x, y.y);
                             } else {
-                                const uint32_t w = pack_bf16x2(y.x, y.y);
-                                pk[(j + e) / 2] = w;
-                                if (!kPair) lo[(j + e) / 2] = pack_bf16x2(y.x - bf16_low_half(w), y.y - bf16_high_half(w));
+                                pk[k / 2] = pack_bf16x2(y.x, y.y);
                             }
                         }
                     }
-                    // P over the scores, and what its rounding left behind it
-                    tc::tmem_st16(tS + uint32_t(h * kHalf + c * 32), pk);
-                    if (!kPair && !Q8) tc::tmem_st16(tS + uint32_t(h * kHalf + c * 32 + 16), lo);
                 }
                 l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
-                tc::tmem_st_wait();
+                // O and P are this step's once the product of the last is done
+                if (t > 0) ok &= tc::mbar_wait(bars + C::bPv + s, (t - 1) & 1, status);
+                tc::tc_fence_after();
+                if (t > 0 && __any_sync(kAll, corr != 1.f)) {
+#pragma unroll 1
+                    for (int c = h * (D / 2); c < (h + 1) * (D / 2); c += 16) {
+                        uint32_t o[16];
+                        tc::tmem_ld16(tO + uint32_t(c), o);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
+                        tc::tmem_st16(tO + uint32_t(c), o);
+                    }
+                    tc::tmem_st_wait();
+                }
+                if (C::kPShared) {
+                    uint8_t *dst = sm + C::oP + s * C::kPBytes + h * C::kPanel + row * 128;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        *reinterpret_cast<uint4 *>(dst + ((c ^ (row & 7)) << 4)) =
+                            make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+                    tc::fence_proxy_async_smem();
+                } else {
+                    const uint32_t tP = tmem + C::cP + uint32_t(s * 64 + h * 32) + lane_off;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t part[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) part[j] = pk[c * 16 + j];
+                        tc::tmem_st16(tP + uint32_t(c * 16), part);
+                    }
+                    tc::tmem_st_wait();
+                }
+            } else {
+                tc::mbar_arrive(bars + C::bSFree + s);
+                // as above: P of this step may be announced once the last one's was used
+                if (t > 0) ok &= tc::mbar_wait(bars + C::bPv + s, (t - 1) & 1, status);
             }
             tc::tc_fence_before();
             tc::mbar_arrive(bars + C::bP + s);
         }
-        if (ok && steps > 0 && !tc::mbar_wait(bars + C::bPv + s, (steps - 1) & 1, status)) ok = false;
+        if (steps > 0) ok &= tc::mbar_wait(bars + C::bPv + s, (steps - 1) & 1, status);
         tc::tc_fence_after();
         const float un = Q8 ? exp2_int(big - kWeightShift) : 1.f;
-        swap[h * kRows] = l;                                // (last read before the last step's first barrier)
+        if (!kPair) tc::named_bar_sync(9, 512);             // nothing reads Q, P and the rings any more
+        // the row's sum (in pair over the stream's own Q, in dual behind the states)
+        float *swap = reinterpret_cast<float *>(sm + C::oQ + (kPair ? s * C::kStage : 2 * kRows * 8 + s * 2 * kRows * 4)) + row;
+        swap[h * kRows] = l;
         tc::named_bar_sync(both, 64);
         l += swap[(1 - h) * kRows];
         if (kPair) {
@@ -556,14 +626,12 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 }
             }
         } else {
-            // the stream's state, for the merge: nothing reads Q and the rings
-            // once both streams' products are done
-            tc::named_bar_sync(9, 512);
+            // the stream's state, for the merge
             const bool any = ok && steps > 0 && l != 0.f;
             if (h == 0)
                 reinterpret_cast<float2 *>(sm + C::oStat)[s * kRows + row] =
                     any ? make_float2(m, l) : make_float2(kMinusInf, 0.f);
-            float *dst = reinterpret_cast<float *>(sm + C::oRing) + (s * kRows + row) * C::kOStride;
+            float *dst = reinterpret_cast<float *>(sm + C::oP) + (s * kRows + row) * C::kOStride;
             if (ok && steps > 0 && active)
 #pragma unroll 1
                 for (int c = h * (D / 2); c < (h + 1) * (D / 2); c += 32) {
@@ -579,17 +647,18 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
         }
         tc::tc_fence_before();
     } else {
-        if (warp == 16) {
-            // ---------------------------------------------- MMA of both streams
-            if (lane == 0) {
+        if (warp < 18) {
+            // ----------- MMA, in pair of stream s, in dual (where each tile is one
+            // stream's, and a barrier's phases have to be seen in order) of both
+            if (lane == 0 && (kPair || warp == 16)) {
                 constexpr uint32_t idesc_s = Q8 ? tc::idesc_f16_f32(kRows, kKeys) : tc::idesc_bf16_f32(kRows, kKeys);
                 constexpr uint32_t idesc_o = Q8 ? tc::idesc_f16_f32(kRows, D, true) : tc::idesc_bf16_f32(kRows, D, true);
                 const uint32_t ring = tc::smem_u32(sm + C::oRing);
-                // S = Q K^T of a stream's step t, once the product with the P that lies there is done
-                const auto scores = [&](int s, int t) {
-                    const int q = 2 * tile_of(s, t), st = q % C::kStages;
+                // S = Q K^T of a stream's step t, once the scores of the last are read
+                const auto scores = [&](int s, int t, int q) {
+                    const int st = q % C::kStages;
                     if (!tc::mbar_wait(bars + C::bFull + st, (q / C::kStages) & 1, status)) return false;
-                    if (t > 0 && !tc::mbar_wait(bars + C::bPv + s, (t - 1) & 1, status)) return false;
+                    if (t > 0 && !tc::mbar_wait(bars + C::bSFree + s, (t - 1) & 1, status)) return false;
                     tc::tc_fence_after();
                     const uint32_t ak = ring + uint32_t(st * C::kStage);
                     const uint32_t aq = tc::smem_u32(sm + C::oQ + (kPair ? s * C::kStage : 0));
@@ -604,38 +673,33 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                     return true;
                 };
                 // O += P V, once V is there and P is written
-                const auto output = [&](int s, int t) {
-                    const int i = tile_of(s, t), q = 2 * i + 1, st = q % C::kStages;
+                const auto output = [&](int s, int t, int q) {
+                    const int st = q % C::kStages;
                     if (!tc::mbar_wait(bars + C::bFull + st, (q / C::kStages) & 1, status)) return false;
-                    if (!Q8 && i == n - 1 && !tc::mbar_wait(bars + C::bTail, 0, status)) return false;
+                    if (!Q8 && tile_of(s, t) == n - 1 && !tc::mbar_wait(bars + C::bTail, 0, status)) return false;
                     if (!tc::mbar_wait(bars + C::bP + s, t & 1, status)) return false;
                     tc::tc_fence_after();
                     const uint32_t av = ring + uint32_t(st * C::kStage);
-                    const uint32_t tO = tmem + C::cO + uint32_t(s * D);
+                    const uint32_t tO = tmem + C::cO + uint32_t(s * D), ap = tc::smem_u32(sm + C::oP + s * C::kPBytes);
 #pragma unroll
                     for (int k = 0; k < kKeys / 16; ++k) {
                         const uint64_t dv = tc::smem_desc_sw128_mn(av + k * 2048, C::kPanel, 1024);
-                        const uint32_t ap = tmem + C::cS + uint32_t(s * kKeys + (k >> 1) * 32 + (k & 1) * 8);
-                        tc::mma_bf16_ts(tO, ap, dv, idesc_o, (t > 0 || k > 0) ? 1u : 0u);
-                        if (!kPair && !Q8) tc::mma_bf16_ts(tO, ap + 16, dv, idesc_o, 1u);
+                        const uint32_t more = (t > 0 || k > 0) ? 1u : 0u;
+                        if (C::kPShared)
+                            tc::mma_bf16(tO, tc::smem_desc_sw128(ap + (k >> 2) * C::kPanel + (k & 3) * 32, 1024), dv,
+                                         idesc_o, more);
+                        else
+                            tc::mma_bf16_ts(tO, tmem + C::cP + uint32_t(s * 64 + k * 8), dv, idesc_o, more);
                     }
                     tc::mma_commit(bars + C::bPv + s);
                     tc::mma_commit(bars + C::bEmpty + st);
                     return true;
                 };
-                // A stream's product and its next scores go in one after the
-                // other, the streams in turn: issued as they come, both
-                // streams' products would interleave, end together and leave
-                // the tensor cores idle while both wait for their softmax.
-                const int steps[2] = {steps_of(0), steps_of(1)};
-                bool ok = steps[0] == 0 || tc::mbar_wait(bars + C::bQ, 0, status);
-                for (int s = 0; s < 2; ++s) ok = ok && (steps[s] == 0 || scores(s, 0));
-                for (int t = 0; ok && t < steps[0]; ++t)
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        ok = ok && (t >= steps[s] || output(s, t));
-                        ok = ok && (t + 1 >= steps[s] || scores(s, t + 1));
-                    }
+                if (steps_of(warp - 16) > 0 && tc::mbar_wait(bars + C::bQ, 0, status))
+                    schedule(n, [&](bool v, int i, int q) {
+                        const int s = kPair ? warp - 16 : i & 1, t = kPair ? i : i >> 1;
+                        return v ? output(s, t, q) : scores(s, t, q);
+                    });
             }
             __syncwarp();
         } else if (warp == 18) {
@@ -646,64 +710,63 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 const int u = i + lane / pages;
                 return u < n ? page_of(a, r, tiles.key0(u), lane % pages) : -1;
             };
-            int32_t ids = -1, next = look_up(0);
+            // K and V each look up their own tiles: K runs ahead
+            int32_t ids[2] = {-1, -1}, next[2] = {look_up(0), look_up(0)};
             bool ok = true;
-            for (int i = 0; i < n && ok; ++i) {
+            schedule(n, [&](bool v, int i, int q) {
                 const int at = i % tiles_at_once * pages;
+                int32_t &mine = v ? ids[1] : ids[0], &then = v ? next[1] : next[0];
                 if (at == 0) {
-                    ids = next;
-                    next = look_up(i + tiles_at_once);
+                    mine = then;
+                    then = look_up(i + tiles_at_once);
                 }
-                const uint32_t group_bits = pages == 32 ? kAll : (1u << pages) - 1;
-                const uint32_t gone = (__ballot_sync(kAll, ids == -2) >> at) & group_bits;
-                const uint32_t here = (__ballot_sync(kAll, ids >= 0) >> at) & group_bits;
-                // groups of 16 keys: bits 0-7 not known to be gone, 8-15 copied
-                uint32_t note = 0xffu;
-                for (int g = 0; g < pages; ++g) {
-                    const uint32_t bits = ((1u << per16) - 1) << (g * per16);
-                    if ((gone >> g) & 1u) note &= ~bits;
-                    if ((here >> g) & 1u) note |= bits << 8;
-                }
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    constexpr int kSlots = Q8 ? C::kRaw : C::kStages;
-                    const int q = 2 * i + v, st = q % (Q8 ? C::kRaw : C::kStages);
-                    uint64_t *full = bars + (Q8 ? C::bRawFull : C::bFull) + st;
-                    if (q >= kSlots)
-                        ok = __all_sync(kAll, tc::mbar_wait(bars + (Q8 ? C::bRawEmpty : C::bEmpty) + st,
-                                                            (q / kSlots - 1) & 1, status));
-                    if (!ok) break;
-                    if (lane == 0) {
-                        if (v == 0) notes[i % kNotes] = note;
-                        tc::mbar_arrive_expect_tx(
-                            full, Q8 ? uint32_t(__popc(here) * a.c.page * (D + (v == 0 ? 8 : 0))) : uint32_t(C::kStage));
-                    }
-                    __syncwarp();
+                constexpr int kSlots = Q8 ? C::kRaw : C::kStages;
+                const int st = q % (Q8 ? C::kRaw : C::kStages);
+                uint64_t *full = bars + (Q8 ? C::bRawFull : C::bFull) + st;
+                if (q >= kSlots)
+                    ok = __all_sync(kAll, tc::mbar_wait(bars + (Q8 ? C::bRawEmpty : C::bEmpty) + st,
+                                                        (q / kSlots - 1) & 1, status));
+                if (!ok) return false;
+                const uint32_t here = (__ballot_sync(kAll, mine >= 0) >> at) & ((1u << pages) - 1);
+                if (!v) {
+                    // groups of 16 keys: bits 0-7 not known to be gone, 8-15 copied
+                    const uint32_t gone = (__ballot_sync(kAll, mine == -2) >> at) & ((1u << pages) - 1);
+                    uint32_t note = 0xffu;
                     for (int g = 0; g < pages; ++g) {
-                        const int32_t pid = __shfl_sync(kAll, ids, at + g);
-                        if (lane != 0) continue;
-                        if (Q8) {
-                            if (pid < 0) continue;
-                            const int64_t row0 = (int64_t(pid) * a.c.heads + head) * a.c.page;
-                            uint8_t *dst = sm + C::oRaw + st * C::kRawStage;
-                            tc::bulk_g2s(dst + g * a.c.page * D,
-                                         reinterpret_cast<const int8_t *>(v == 0 ? a.c.k : a.c.v) + row0 * D,
-                                         uint32_t(a.c.page * D), full);
-                            if (v == 0) {
-                                float *sc = reinterpret_cast<float *>(dst + kKeys * D) + g * a.c.page;
-                                tc::bulk_g2s(sc, a.ks + row0, uint32_t(a.c.page * 4), full);
-                                tc::bulk_g2s(sc + kKeys, a.vs + row0, uint32_t(a.c.page * 4), full);
-                            }
-                        } else {
-#pragma unroll
-                            for (int sub = 0; sub < C::kSub; ++sub)     // what is not there arrives as zeros
-                                tc::tma_load_4d(sm + C::oRing + st * C::kStage + sub * C::kPanel + g * a.c.page * 128,
-                                                v == 0 ? &tm_k : &tm_v, full, sub * 64, 0, head, pid < 0 ? -1 : pid);
-                        }
+                        const uint32_t bits = ((1u << per16) - 1) << (g * per16);
+                        if ((gone >> g) & 1u) note &= ~bits;
+                        if ((here >> g) & 1u) note |= bits << 8;
                     }
-                    __syncwarp();
+                    if (lane == 0) notes[i % kNotes] = note;
                 }
-            }
+                if (lane == 0)
+                    tc::mbar_arrive_expect_tx(
+                        full, Q8 ? uint32_t(__popc(here) * a.c.page * (D + (v ? 0 : 8))) : uint32_t(C::kStage));
+                __syncwarp();
+                for (int g = 0; g < pages; ++g) {
+                    const int32_t pid = __shfl_sync(kAll, mine, at + g);
+                    if (lane != 0) continue;
+                    if (Q8) {
+                        if (pid < 0) continue;
+                        const int64_t row0 = (int64_t(pid) * a.c.heads + head) * a.c.page;
+                        uint8_t *dst = sm + C::oRaw + st * C::kRawStage;
+                        tc::bulk_g2s(dst + g * a.c.page * D, reinterpret_cast<const int8_t *>(v ? a.c.v : a.c.k) + row0 * D,
+                                     uint32_t(a.c.page * D), full);
+                        if (!v) {
+                            float *sc = reinterpret_cast<float *>(dst + kKeys * D) + g * a.c.page;
+                            tc::bulk_g2s(sc, a.ks + row0, uint32_t(a.c.page * 4), full);
+                            tc::bulk_g2s(sc + kKeys, a.vs + row0, uint32_t(a.c.page * 4), full);
+                        }
+                    } else {
+#pragma unroll
+                        for (int sub = 0; sub < C::kSub; ++sub)     // what is not there arrives as zeros
+                            tc::tma_load_4d(sm + C::oRing + st * C::kStage + sub * C::kPanel + g * a.c.page * 128,
+                                            v ? &tm_v : &tm_k, full, sub * 64, 0, head, pid < 0 ? -1 : pid);
+                    }
+                }
+                __syncwarp();
+                return true;
+            });
             if (!Q8 && ok && n > 0) {
                 // rows past the last key hold anything, and 0 times NaN must not reach O
                 const int q = 2 * n - 1, st = q % C::kStages, tail = r.end - tiles.key0(n - 1);
@@ -723,44 +786,39 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
             const int w = tid - 20 * 32;
             float *scales = reinterpret_cast<float *>(sm + C::oScales);
             constexpr int kSlots = C::kRaw > 0 ? C::kRaw : 1;
-            for (int i = 0; i < n; ++i) {
+            schedule(n, [&](bool v, int i, int q) {
                 const int32_t key0 = tiles.key0(i);
-                bool ok = true;
-                uint32_t note = 0u;
+                const int raw = q % kSlots, st = q % C::kStages;
+                const bool ok =
+                    tc::mbar_wait(bars + C::bRawFull + raw, (q / kSlots) & 1, status) &&
+                    (q < C::kStages || tc::mbar_wait(bars + C::bEmpty + st, (q / C::kStages - 1) & 1, status));
+                if (!__all_sync(kAll, ok)) return false;
+                const uint8_t *src = sm + C::oRaw + raw * C::kRawStage;
+                uint8_t *stage = sm + C::oRing + st * C::kStage;
+                const uint32_t note = notes[i % kNotes];
                 const auto seen = [&](int x) {
                     const int32_t key = key0 + x;
                     return ((note >> (8 + x / 16)) & 1u) && key < r.end && (key < r.sinks_end || key >= r.first);
                 };
-#pragma unroll 1
-                for (int v = 0; v < 2; ++v) {
-                    const int q = 2 * i + v, raw = q % kSlots, st = q % C::kStages;
-                    ok = tc::mbar_wait(bars + C::bRawFull + raw, (q / kSlots) & 1, status) &&
-                         (q < C::kStages || tc::mbar_wait(bars + C::bEmpty + st, (q / C::kStages - 1) & 1, status));
-                    if (!__all_sync(kAll, ok)) break;
-                    const uint8_t *src = sm + C::oRaw + raw * C::kRawStage;
-                    uint8_t *stage = sm + C::oRing + st * C::kStage;
-                    note = notes[i % kNotes];
-                    if (v == 0) {
-                        const float *sc = reinterpret_cast<const float *>(src + kKeys * D);
-                        const float sk = seen(w) ? sc[w] : 0.f, sv = seen(w) ? sc[kKeys + w] : 0.f;
-                        scales[(i % 8) * 2 * kKeys + w] = sk;
-                        scales[((i % 8) * 2 + 1) * kKeys + w] = sv;
-                        const uint32_t top = __reduce_max_sync(kAll, sv == sv ? __float_as_uint(sv) & 0x7fffffffu : 0u);
-                        if (lane == 0) reinterpret_cast<uint32_t *>(sm + C::oTops)[(i % kNotes) * 4 + (w >> 5)] = top;
-                    }
-#pragma unroll 4
-                    for (int j = 0; j < kPer; ++j) {
-                        const int c = j * 128 + w, row = c / kPer, ch = c % kPer;
-                        const uint4 x = seen(row) ? *reinterpret_cast<const uint4 *>(src + c * 16)
-                                                  : make_uint4(0u, 0u, 0u, 0u);
-                        store_codes(stage + (ch >> 2) * C::kPanel + row * 128, (ch & 3) * 2, row, x);
-                    }
-                    tc::fence_proxy_async_smem();
-                    tc::mbar_arrive(bars + C::bFull + st);
-                    tc::mbar_arrive(bars + C::bRawEmpty + raw);
+                if (!v) {
+                    const float *sc = reinterpret_cast<const float *>(src + kKeys * D);
+                    const float sk = seen(w) ? sc[w] : 0.f, sv = seen(w) ? sc[kKeys + w] : 0.f;
+                    scales[(i % 8) * 2 * kKeys + w] = sk;
+                    scales[((i % 8) * 2 + 1) * kKeys + w] = sv;
+                    const uint32_t top = __reduce_max_sync(kAll, sv == sv ? __float_as_uint(sv) & 0x7fffffffu : 0u);
+                    if (lane == 0) reinterpret_cast<uint32_t *>(sm + C::oTops)[(i % kNotes) * 4 + (w >> 5)] = top;
                 }
-                if (!__all_sync(kAll, ok)) break;
-            }
+#pragma unroll 4
+                for (int j = 0; j < kPer; ++j) {
+                    const int c = j * 128 + w, row = c / kPer, ch = c % kPer;
+                    const uint4 x = seen(row) ? *reinterpret_cast<const uint4 *>(src + c * 16) : make_uint4(0u, 0u, 0u, 0u);
+                    store_codes(stage + (ch >> 2) * C::kPanel + row * 128, (ch & 3) * 2, row, x);
+                }
+                tc::fence_proxy_async_smem();
+                tc::mbar_arrive(bars + C::bFull + st);
+                tc::mbar_arrive(bars + C::bRawEmpty + raw);
+                return true;
+            });
         }
     }
 
@@ -788,7 +846,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 const float wi = __shfl_sync(kAll, w, i);
                 if (__shfl_sync(kAll, st.y, i) == 0.f) continue;          // nothing there
                 const float *o = peers.map_shared_rank(
-                    reinterpret_cast<float *>(sm + C::oRing) + ((i & 1) * kRows + row) * C::kOStride, i >> 1);
+                    reinterpret_cast<float *>(sm + C::oP) + ((i & 1) * kRows + row) * C::kOStride, i >> 1);
                 if (E == 4) {
                     const float4 v = *reinterpret_cast<const float4 *>(o + lane * 4);
                     x[0] = fmaf(wi, v.x, x[0]);
@@ -895,7 +953,7 @@ cudaError_t launch_tiles_form(const AttentionArgs &a, cudaStream_t st) {
     // pairs where they leave no SM without a CTA
     int64_t items = items_of(2 * p.tokens);
     const int64_t used = (a.tokens + 2 * p.tokens - 1) / (2 * p.tokens) * a.c.heads;
-    const bool pair = mean > p.tokens && used >= 96;
+    const bool pair = mean > p.tokens && used >= 96 && !(Q8 && a.c.d == 128);
     p.cluster = 1;
     if (!pair) {
         p.tokens = int32_t(std::min<int64_t>(p.tokens, mean));
@@ -912,7 +970,9 @@ cudaError_t launch_tiles_form(const AttentionArgs &a, cudaStream_t st) {
     }
     if (items * p.cluster > 0x7fffffff) return cudaErrorInvalidConfiguration;
     if (a.c.d == 64) return pair ? launch_tiles<64, true, Q8>(a, p, items, st) : launch_tiles<64, false, Q8>(a, p, items, st);
-    return pair ? launch_tiles<128, true, Q8>(a, p, items, st) : launch_tiles<128, false, Q8>(a, p, items, st);
+    if constexpr (!Q8)
+        if (pair) return launch_tiles<128, true, Q8>(a, p, items, st);
+    return launch_tiles<128, false, Q8>(a, p, items, st);
 }
 
 }  // namespace
