@@ -50,7 +50,6 @@ namespace {
 
 constexpr int kRows = 128;               // rows of a stream
 constexpr int kKeys = 128;               // keys of a tile
-constexpr int kHalf = kKeys / 2;         // keys of a softmax thread
 constexpr int kNotes = 16;               // tiles whose notes are kept: more than the ring holds
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kMinusInf = -__builtin_huge_valf();
@@ -68,7 +67,10 @@ struct TCfg {
     static constexpr bool kPShared = D == 128;              // P in shared memory, else in tensor memory
     static constexpr int kPBytes = 2 * kPanel;              // 128 rows x 128 keys
     static constexpr int kQTiles = kPair ? 2 : 1;
-    static constexpr int kWarps = Q8 ? 24 : 20;
+    static constexpr int kSplit = 1;                        // softmax threads of a row
+    static constexpr int kCols = kKeys / kSplit;            // keys of each
+    static constexpr int kSoft = 8 * kSplit;                // softmax warps
+    static constexpr int kWarps = kSoft + (Q8 ? 8 : 4);
     static constexpr int oQ = 0;
     static constexpr int oP = oQ + kQTiles * kStage;
     static constexpr int oRing = oP + (kPShared ? 2 * kPBytes : 0);
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
     const auto tile_of = [&](int s, int t) { return kPair ? t : 2 * t + s; };
 
     if (tid == 0) {
-        tc::mbar_init(bars + C::bQ, 512);
+        tc::mbar_init(bars + C::bQ, 32 * C::kSoft);
         tc::mbar_init(bars + C::bTail, 1);
         const uint32_t users = kPair && rows_of(1) > 0 ? 2 : 1;
         for (int i = 0; i < C::kStages; ++i) {
@@ -309,8 +311,8 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
         }
         for (int s = 0; s < 2; ++s) {
             tc::mbar_init(bars + C::bS + s, 1);
-            tc::mbar_init(bars + C::bSFree + s, 2 * kRows);
-            tc::mbar_init(bars + C::bP + s, 2 * kRows);
+            tc::mbar_init(bars + C::bSFree + s, C::kSplit * kRows);
+            tc::mbar_init(bars + C::bP + s, C::kSplit * kRows);
             tc::mbar_init(bars + C::bPv + s, 1);
         }
         tc::fence_barrier_init();
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
     }
     uint32_t *tops_so_far = reinterpret_cast<uint32_t *>(sm + C::oSwap);
     if (tid < 2 * kRows) tops_so_far[tid] = 0u;             // below every number
-    if (warp == 16) {
+    if (warp == C::kSoft) {
         tc::tmem_alloc(tmem_slot, 512);
         tc::tmem_relinquish();
     }
@@ -352,9 +354,9 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
         }
     };
 
-    if (warp < 16) {
+    if (warp < C::kSoft) {
         // ------------- softmax of stream s; half h of a tile's keys, and of O's channels
-        const int s = warp >> 3, h = (warp >> 2) & 1, row = tid & 127;
+        const int s = warp / (4 * C::kSplit), h = (warp >> 2) % C::kSplit, row = tid & 127;
         const int rows = rows_of(s), steps = steps_of(s);
         const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + C::cS + uint32_t(s * kKeys) + lane_off, tO = tmem + C::cO + uint32_t(s * D) + lane_off;
@@ -380,8 +382,8 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 back *= exp2_int(e - 14);
                 to = exp2_int(14 - e);
             }
-            constexpr int kMine = D / 8 / (kPair ? 2 : 4);
-            const int c0 = (kPair ? h : 2 * s + h) * kMine;
+            constexpr int kMine = D / 8 / (C::kSplit * (kPair ? 1 : 2));
+            const int c0 = (kPair ? h : C::kSplit * s + h) * kMine;
 #pragma unroll 4
             for (int c = c0; c < c0 + kMine; ++c) {
                 uint4 x = there ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
@@ -412,12 +414,12 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
             if (active) {
                 const uint32_t there = notes[i % kNotes] & 0xffu;
                 const bool full = key0 >= lo_max && key0 + kKeys <= hi_min && there == 0xffu;
-                const float4 *ks = reinterpret_cast<const float4 *>(sm + C::oScales) + (i % 8) * 64 + h * 16;
+                const float4 *ks = reinterpret_cast<const float4 *>(sm + C::oScales) + (i % 8) * 64 + h * (C::kCols / 4);
                 const float2 *vs = reinterpret_cast<const float2 *>(ks + 32);
                 // scores of 32 keys, in log2 units (8-bit pages)
                 const auto scores = [&](int c, float *x) {
                     uint32_t raw[32];
-                    tc::tmem_ld32(tS + uint32_t(h * kHalf + c * 32), raw);
+                    tc::tmem_ld32(tS + uint32_t(h * C::kCols + c * 32), raw);
                     tc::tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(raw[j]);
@@ -436,8 +438,8 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                     }
                 };
                 const auto admitted = [&](int c) {
-                    const uint32_t g = there >> (4 * h + 2 * c);
-                    return seen_bits(sight, int32_t(r.start), sinks, key0 + h * kHalf + c * 32) &
+                    const uint32_t g = there >> (h * (C::kCols / 16) + 2 * c);
+                    return seen_bits(sight, int32_t(r.start), sinks, key0 + h * C::kCols + c * 32) &
                            ((g & 1u ? 0xffffu : 0u) | (g & 2u ? 0xffff0000u : 0u));
                 };
                 const auto mask = [&](uint32_t adm, float *x) {
@@ -447,20 +449,20 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 };
                 // 16-bit pages: held from the maximum to the weights; 8-bit
                 // pages need the registers for the scales and read them twice
-                float x[kHalf];
+                float x[C::kCols];
                 float mx[4] = {kMinusInf, kMinusInf, kMinusInf, kMinusInf};
                 if (!Q8) {
-                    uint32_t raw[2][32];
-                    tc::tmem_ld32(tS + uint32_t(h * kHalf), raw[0]);
-                    tc::tmem_ld32(tS + uint32_t(h * kHalf + 32), raw[1]);
+                    uint32_t raw[C::kCols / 32][32];
+#pragma unroll
+                    for (int c = 0; c < C::kCols / 32; ++c) tc::tmem_ld32(tS + uint32_t(h * C::kCols + c * 32), raw[c]);
                     tc::tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < kHalf; ++j) x[j] = __uint_as_float(raw[j / 32][j % 32]);
+                    for (int j = 0; j < C::kCols; ++j) x[j] = __uint_as_float(raw[j / 32][j % 32]);
                     tc::tc_fence_before();
                     tc::mbar_arrive(bars + C::bSFree + s);  // the next scores may come
                 }
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
+                for (int c = 0; c < C::kCols / 32; ++c) {
                     float *y = x + (Q8 ? 0 : c * 32);
                     if (Q8) scores(c, y);
                     if (!full) mask(admitted(c), y);
@@ -469,20 +471,22 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], y[j + e], y[j + 4 + e]);
                 }
-                // the row's maximum, once one half's has grown enough
+                // the row's maximum, once it has grown enough (with two threads
+                // to a row, in either half)
                 float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
                 if (!Q8) top *= back;
                 float corr = 1.f;
-                if (!tc::named_bar_and(both, 64, !(top > m + kLazy || m == kMinusInf))) {
-                    // the larger of the two halves' (it only grows from step to step)
-                    atomicMax(shared_top, ordered(top));
+                bool grown = top > m + kLazy || m == kMinusInf;
+                if (C::kSplit == 2 && !tc::named_bar_and(both, 64, !grown)) {
+                    atomicMax(shared_top, ordered(top));    // it only grows from step to step
                     tc::named_bar_sync(both, 64);
                     top = of_ordered(*shared_top);
-                    if (top > m + kLazy || m == kMinusInf) {
-                        const float mn = fmaxf(m, top);
-                        corr = mn == kMinusInf ? 1.f : exp2_ftz(m - mn);
-                        m = mn;
-                    }
+                    grown = top > m + kLazy || m == kMinusInf;
+                }
+                if (grown) {
+                    const float mn = fmaxf(m, top);
+                    corr = mn == kMinusInf ? 1.f : exp2_ftz(m - mn);
+                    m = mn;
                 }
                 l *= corr;
                 float vf = 1.f;
@@ -498,13 +502,29 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 const float base = m == kMinusInf ? 0.f : m;
                 const float2 b2 = make_float2(back, back), n2 = make_float2(-base, -base);
                 float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                uint32_t pk[kHalf / 2];
+                // O and P are this step's once the product of the last is done
+                const auto settle = [&] {
+                    if (t > 0) ok &= tc::mbar_wait(bars + C::bPv + s, (t - 1) & 1, status);
+                    tc::tc_fence_after();
+                    if (t > 0 && __any_sync(kAll, corr != 1.f)) {
+#pragma unroll 1
+                        for (int c = h * (D / C::kSplit); c < (h + 1) * (D / C::kSplit); c += 16) {
+                            uint32_t o[16];
+                            tc::tmem_ld16(tO + uint32_t(c), o);
+                            tc::tmem_ld_wait();
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
+                            tc::tmem_st16(tO + uint32_t(c), o);
+                        }
+                    }
+                };
+                uint32_t pk[32];                            // weights of 64 keys
+#pragma unroll
+                for (int c = 0; c < C::kCols / 32; ++c) {
                     const uint32_t adm = Q8 && !full ? admitted(c) : kAll;
                     if (Q8) {
                         scores(c, x);
-                        if (c == 1) {
+                        if (c == C::kCols / 32 - 1) {
                             tc::tc_fence_before();
                             tc::mbar_arrive(bars + C::bSFree + s);
                         }
@@ -527,47 +547,35 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                                     if (!((adm >> (j + e)) & 1u)) y.x = 0.f;
                                     if (!((adm >> (j + e + 1)) & 1u)) y.y = 0.f;
                                 }
-                                pk[k / 2] = pack_f16x2(y.x, y.y);
+                                pk[k / 2 % 32] = pack_f16x2(y.x, y.y);
                             } else {
-                                pk[k / 2] = pack_bf16x2(y.x, y.y);
+                                pk[k / 2 % 32] = pack_bf16x2(y.x, y.y);
                             }
+                        }
+                    }
+                    if (c % 2 == 0) continue;
+                    if (c == 1) settle();
+                    const int panel = h * (C::kCols / 64) + c / 2;
+                    if (C::kPShared) {
+                        uint8_t *dst = sm + C::oP + s * C::kPBytes + panel * C::kPanel + row * 128;
+#pragma unroll
+                        for (int v = 0; v < 8; ++v)
+                            *reinterpret_cast<uint4 *>(dst + ((v ^ (row & 7)) << 4)) =
+                                make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+                    } else {
+                        const uint32_t tP = tmem + C::cP + uint32_t(s * 64 + panel * 32) + lane_off;
+#pragma unroll
+                        for (int v = 0; v < 2; ++v) {
+                            uint32_t part[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) part[j] = pk[v * 16 + j];
+                            tc::tmem_st16(tP + uint32_t(v * 16), part);
                         }
                     }
                 }
                 l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
-                // O and P are this step's once the product of the last is done
-                if (t > 0) ok &= tc::mbar_wait(bars + C::bPv + s, (t - 1) & 1, status);
-                tc::tc_fence_after();
-                if (t > 0 && __any_sync(kAll, corr != 1.f)) {
-#pragma unroll 1
-                    for (int c = h * (D / 2); c < (h + 1) * (D / 2); c += 16) {
-                        uint32_t o[16];
-                        tc::tmem_ld16(tO + uint32_t(c), o);
-                        tc::tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
-                        tc::tmem_st16(tO + uint32_t(c), o);
-                    }
-                    tc::tmem_st_wait();
-                }
-                if (C::kPShared) {
-                    uint8_t *dst = sm + C::oP + s * C::kPBytes + h * C::kPanel + row * 128;
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        *reinterpret_cast<uint4 *>(dst + ((c ^ (row & 7)) << 4)) =
-                            make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-                    tc::fence_proxy_async_smem();
-                } else {
-                    const uint32_t tP = tmem + C::cP + uint32_t(s * 64 + h * 32) + lane_off;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t part[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) part[j] = pk[c * 16 + j];
-                        tc::tmem_st16(tP + uint32_t(c * 16), part);
-                    }
-                    tc::tmem_st_wait();
-                }
+                if (C::kPShared) tc::fence_proxy_async_smem();
+                tc::tmem_st_wait();
             } else {
                 tc::mbar_arrive(bars + C::bSFree + s);
                 // as above: P of this step may be announced once the last one's was used
@@ -579,19 +587,21 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
         if (steps > 0) ok &= tc::mbar_wait(bars + C::bPv + s, (steps - 1) & 1, status);
         tc::tc_fence_after();
         const float un = Q8 ? exp2_int(big - kWeightShift) : 1.f;
-        if (!kPair) tc::named_bar_sync(9, 512);             // nothing reads Q, P and the rings any more
-        // the row's sum (in pair over the stream's own Q, in dual behind the states)
-        float *swap = reinterpret_cast<float *>(sm + C::oQ + (kPair ? s * C::kStage : 2 * kRows * 8 + s * 2 * kRows * 4)) + row;
-        swap[h * kRows] = l;
-        tc::named_bar_sync(both, 64);
-        l += swap[(1 - h) * kRows];
+        if (!kPair) tc::named_bar_sync(9, 32 * C::kSoft);   // nothing reads Q, P and the rings any more
+        if (C::kSplit == 2) {
+            // the row's sum (in pair over the stream's own Q, in dual behind the states)
+            float *swap = reinterpret_cast<float *>(sm + C::oQ + (kPair ? s * C::kStage : 2 * kRows * 8 + s * 2 * kRows * 4)) + row;
+            swap[h * kRows] = l;
+            tc::named_bar_sync(both, 64);
+            l += swap[(1 - h) * kRows];
+        }
         if (kPair) {
             const float inv = (l > 0.f || l != l ? __fdiv_rn(1.f, l) : 0.f) * un;
             bool finite = true;
             if (ok && active) {
                 uint16_t *dst = a.out + token_row(s, min(row, rows - 1), int64_t(a.q_heads) * D);
 #pragma unroll 1
-                for (int c = h * (D / 2); c < (h + 1) * (D / 2); c += 32) {
+                for (int c = h * (D / C::kSplit); c < (h + 1) * (D / C::kSplit); c += 32) {
                     uint32_t o[32];
                     tc::tmem_ld32(tO + uint32_t(c), o);
                     tc::tmem_ld_wait();
@@ -619,7 +629,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                         float x[D / 32];
                         row_alone<D>(a, r, sight_at(s, which), head, a.q + token_row(s, which, a.q_stride), x);
                         uint16_t *to = a.out + token_row(s, which, int64_t(a.q_heads) * D) + lane * (D / 32);
-                        if (lane >> 4 == h)
+                        if (C::kSplit == 1 || lane >> 4 == h)
 #pragma unroll
                             for (int e = 0; e < D / 32; ++e) to[e] = f32_to_bf16_bits(x[e]);
                     }
@@ -634,7 +644,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
             float *dst = reinterpret_cast<float *>(sm + C::oP) + (s * kRows + row) * C::kOStride;
             if (ok && steps > 0 && active)
 #pragma unroll 1
-                for (int c = h * (D / 2); c < (h + 1) * (D / 2); c += 32) {
+                for (int c = h * (D / C::kSplit); c < (h + 1) * (D / C::kSplit); c += 32) {
                     uint32_t o[32];
                     tc::tmem_ld32(tO + uint32_t(c), o);
                     tc::tmem_ld_wait();
@@ -647,10 +657,10 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
         }
         tc::tc_fence_before();
     } else {
-        if (warp < 18) {
+        if (warp < C::kSoft + 2) {
             // ----------- MMA, in pair of stream s, in dual (where each tile is one
             // stream's, and a barrier's phases have to be seen in order) of both
-            if (lane == 0 && (kPair || warp == 16)) {
+            if (lane == 0 && (kPair || warp == C::kSoft)) {
                 constexpr uint32_t idesc_s = Q8 ? tc::idesc_f16_f32(kRows, kKeys) : tc::idesc_bf16_f32(kRows, kKeys);
                 constexpr uint32_t idesc_o = Q8 ? tc::idesc_f16_f32(kRows, D, true) : tc::idesc_bf16_f32(kRows, D, true);
                 const uint32_t ring = tc::smem_u32(sm + C::oRing);
@@ -695,14 +705,14 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                     tc::mma_commit(bars + C::bEmpty + st);
                     return true;
                 };
-                if (steps_of(warp - 16) > 0 && tc::mbar_wait(bars + C::bQ, 0, status))
+                if (steps_of(warp - C::kSoft) > 0 && tc::mbar_wait(bars + C::bQ, 0, status))
                     schedule(n, [&](bool v, int i, int q) {
-                        const int s = kPair ? warp - 16 : i & 1, t = kPair ? i : i >> 1;
+                        const int s = kPair ? warp - C::kSoft : i & 1, t = kPair ? i : i >> 1;
                         return v ? output(s, t, q) : scores(s, t, q);
                     });
             }
             __syncwarp();
-        } else if (warp == 18) {
+        } else if (warp == C::kSoft + 2) {
             // ------------------------------------------------------- producer
             const int pages = kKeys / a.c.page, per16 = a.c.page / 16, tiles_at_once = 32 / pages;
             // pages of the tiles from i on, one to a lane
@@ -780,10 +790,10 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(bars + C::bTail);
             }
-        } else if (Q8 && warp >= 20) {
+        } else if (Q8 && warp >= C::kSoft + 4) {
             // --------------------------- codes to fp16, rows that nothing sees to zero
             constexpr int kPer = D / 16;                    // 16-byte pieces of a row
-            const int w = tid - 20 * 32;
+            const int w = tid - (C::kSoft + 4) * 32;
             float *scales = reinterpret_cast<float *>(sm + C::oScales);
             constexpr int kSlots = C::kRaw > 0 ? C::kRaw : 1;
             schedule(n, [&](bool v, int i, int q) {
@@ -876,7 +886,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
         if (p.cluster > 1) peers.sync();                    // peers read this CTA's shared memory
     }
     __syncthreads();
-    if (warp == 16) {
+    if (warp == C::kSoft) {
         tc::tc_fence_after();
         tc::tmem_dealloc(tmem, 512);
     }
