@@ -415,28 +415,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 const uint32_t there = notes[i % kNotes] & 0xffu;
                 const bool full = key0 >= lo_max && key0 + kKeys <= hi_min && there == 0xffu;
                 const float4 *ks = reinterpret_cast<const float4 *>(sm + C::oScales) + (i % 8) * 64 + h * (C::kCols / 4);
-                const float2 *vs = reinterpret_cast<const float2 *>(ks + 32);
-                // scores of 32 keys, in log2 units (8-bit pages)
-                const auto scores = [&](int c, float *x) {
-                    uint32_t raw[32];
-                    tc::tmem_ld32(tS + uint32_t(h * C::kCols + c * 32), raw);
-                    tc::tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(raw[j]);
-                    if (Q8) {
-                        const float2 b2 = make_float2(back, back);
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            const float4 k4 = ks[c * 8 + j / 4];
-                            const float2 y0 = mul2(make_float2(x[j], x[j + 1]), mul2(make_float2(k4.x, k4.y), b2));
-                            const float2 y1 = mul2(make_float2(x[j + 2], x[j + 3]), mul2(make_float2(k4.z, k4.w), b2));
-                            x[j] = y0.x;
-                            x[j + 1] = y0.y;
-                            x[j + 2] = y1.x;
-                            x[j + 3] = y1.y;
-                        }
-                    }
-                };
+                const float4 *vs = ks + 32;
                 const auto admitted = [&](int c) {
                     const uint32_t g = there >> (h * (C::kCols / 16) + 2 * c);
                     return seen_bits(sight, int32_t(r.start), sinks, key0 + h * C::kCols + c * 32) &
@@ -447,11 +426,43 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                     for (int j = 0; j < 32; ++j)
                         if (!((adm >> j) & 1u)) x[j] = kMinusInf;
                 };
-                // 16-bit pages: held from the maximum to the weights; 8-bit
-                // pages need the registers for the scales and read them twice
-                float x[C::kCols];
+                const float2 back2 = make_float2(back, back);
+                // 8-bit pages: scores of 32 keys in log2 units
+                const auto scores8 = [&](int c, float *x) {
+                    uint32_t raw[32];
+                    tc::tmem_ld32(tS + uint32_t(h * C::kCols + c * 32), raw);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 k4 = ks[c * 8 + j / 4];
+                        const float2 y0 = mul2(make_float2(__uint_as_float(raw[j]), __uint_as_float(raw[j + 1])),
+                                               mul2(make_float2(k4.x, k4.y), back2));
+                        const float2 y1 = mul2(make_float2(__uint_as_float(raw[j + 2]), __uint_as_float(raw[j + 3])),
+                                               mul2(make_float2(k4.z, k4.w), back2));
+                        x[j] = y0.x;
+                        x[j + 1] = y0.y;
+                        x[j + 2] = y1.x;
+                        x[j + 3] = y1.y;
+                    }
+                };
                 float mx[4] = {kMinusInf, kMinusInf, kMinusInf, kMinusInf};
-                if (!Q8) {
+                const auto largest = [&](const float *x) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[j + e], x[j + 4 + e]);
+                };
+                // 16-bit pages: the scores are held from the maximum to the
+                // weights; 8-bit pages read them twice (the scales need registers)
+                float x[Q8 ? 32 : C::kCols];
+                if constexpr (Q8) {
+#pragma unroll 1
+                    for (int c = 0; c < C::kCols / 32; ++c) {
+                        scores8(c, x);
+                        if (!full) mask(admitted(c), x);
+                        largest(x);
+                    }
+                } else {
                     uint32_t raw[C::kCols / 32][32];
 #pragma unroll
                     for (int c = 0; c < C::kCols / 32; ++c) tc::tmem_ld32(tS + uint32_t(h * C::kCols + c * 32), raw[c]);
@@ -460,16 +471,11 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                     for (int j = 0; j < C::kCols; ++j) x[j] = __uint_as_float(raw[j / 32][j % 32]);
                     tc::tc_fence_before();
                     tc::mbar_arrive(bars + C::bSFree + s);  // the next scores may come
-                }
+                    if (!full)
 #pragma unroll
-                for (int c = 0; c < C::kCols / 32; ++c) {
-                    float *y = x + (Q8 ? 0 : c * 32);
-                    if (Q8) scores(c, y);
-                    if (!full) mask(admitted(c), y);
+                        for (int c = 0; c < C::kCols / 32; ++c) mask(admitted(c), x + c * 32);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], y[j + e], y[j + 4 + e]);
+                    for (int c = 0; c < C::kCols / 32; ++c) largest(x + c * 32);
                 }
                 // the row's maximum, once it has grown enough (with two threads
                 // to a row, in either half)
@@ -500,7 +506,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                     vf = exp2_int(kWeightShift - big);
                 }
                 const float base = m == kMinusInf ? 0.f : m;
-                const float2 b2 = make_float2(back, back), n2 = make_float2(-base, -base);
+                const float2 n2 = make_float2(-base, -base), f2 = make_float2(vf, vf);
                 float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 // O and P are this step's once the product of the last is done
                 const auto settle = [&] {
@@ -519,43 +525,28 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                     }
                 };
                 uint32_t pk[32];                            // weights of 64 keys
-#pragma unroll
-                for (int c = 0; c < C::kCols / 32; ++c) {
-                    const uint32_t adm = Q8 && !full ? admitted(c) : kAll;
-                    if (Q8) {
-                        scores(c, x);
-                        if (c == C::kCols / 32 - 1) {
-                            tc::tc_fence_before();
-                            tc::mbar_arrive(bars + C::bSFree + s);
-                        }
-                        if (!full) mask(adm, x);
-                    }
+                const auto weights = [&](int c, const float *x, uint32_t *to) {
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
+                        const float4 v4 = Q8 ? vs[c * 8 + j / 4] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                         for (int e = 0; e < 4; e += 2) {
-                            const int k = c * 32 + j + e, at = Q8 ? j + e : k;
-                            float2 y = make_float2(x[at], x[at + 1]);
-                            y = Q8 ? add2(y, n2) : fma2(y, b2, n2);
+                            float2 y = make_float2(x[j + e], x[j + e + 1]);
+                            y = Q8 ? add2(y, n2) : fma2(y, back2, n2);
                             y.x = exp2_ftz(y.x);
                             y.y = exp2_ftz(y.y);
                             ls[e / 2] = add2(ls[e / 2], y);
                             if (Q8) {
-                                const float2 v2 = vs[k / 2];
-                                y = mul2(y, mul2(v2, make_float2(vf, vf)));
-                                if (!full) {                // the scale of a masked key may be anything
-                                    if (!((adm >> (j + e)) & 1u)) y.x = 0.f;
-                                    if (!((adm >> (j + e + 1)) & 1u)) y.y = 0.f;
-                                }
-                                pk[k / 2 % 32] = pack_f16x2(y.x, y.y);
+                                y = mul2(y, mul2(e == 0 ? make_float2(v4.x, v4.y) : make_float2(v4.z, v4.w), f2));
+                                to[(j + e) / 2] = pack_f16x2(y.x, y.y);
                             } else {
-                                pk[k / 2 % 32] = pack_bf16x2(y.x, y.y);
+                                to[(j + e) / 2] = pack_bf16x2(y.x, y.y);
                             }
                         }
                     }
-                    if (c % 2 == 0) continue;
-                    if (c == 1) settle();
-                    const int panel = h * (C::kCols / 64) + c / 2;
+                };
+                const auto publish = [&](int p64) {         // of the thread's p64-th 64 keys
+                    const int panel = h * (C::kCols / 64) + p64;
                     if (C::kPShared) {
                         uint8_t *dst = sm + C::oP + s * C::kPBytes + panel * C::kPanel + row * 128;
 #pragma unroll
@@ -564,13 +555,39 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                                 make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
                     } else {
                         const uint32_t tP = tmem + C::cP + uint32_t(s * 64 + panel * 32) + lane_off;
+                        tc::tmem_st32(tP, pk);
+                    }
+                };
+                if constexpr (Q8) {
+#pragma unroll 1
+                    for (int p64 = 0; p64 < C::kCols / 64; ++p64) {
 #pragma unroll
-                        for (int v = 0; v < 2; ++v) {
-                            uint32_t part[16];
+                        for (int k = 0; k < 2; ++k) {
+                            const int c = 2 * p64 + k;
+                            scores8(c, x);
+                            const uint32_t adm = full ? kAll : admitted(c);
+                            if (!full) mask(adm, x);
+                            weights(c, x, pk + 16 * k);
+                            if (!full)                      // the scale of a masked key may be anything
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) part[j] = pk[v * 16 + j];
-                            tc::tmem_st16(tP + uint32_t(v * 16), part);
+                                for (int j = 0; j < 16; ++j)
+                                    pk[16 * k + j] &= (((adm >> (2 * j)) & 1u) ? 0xffffu : 0u) |
+                                                      (((adm >> (2 * j + 1)) & 1u) ? 0xffff0000u : 0u);
                         }
+                        if (p64 == C::kCols / 64 - 1) {
+                            tc::tc_fence_before();
+                            tc::mbar_arrive(bars + C::bSFree + s);
+                        }
+                        if (p64 == 0) settle();
+                        publish(p64);
+                    }
+                } else {
+#pragma unroll
+                    for (int p64 = 0; p64 < C::kCols / 64; ++p64) {
+                        weights(2 * p64, x + p64 * 64, pk);
+                        weights(2 * p64 + 1, x + p64 * 64 + 32, pk + 16);
+                        if (p64 == 0) settle();
+                        publish(p64);
                     }
                 }
                 l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
