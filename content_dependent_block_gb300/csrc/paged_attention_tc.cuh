@@ -22,14 +22,12 @@
 // the prompt's sparse forward), since a second product would cost a third of
 // the tensor time.  8-bit pages: P in fp16 as in paged_tiles.cuh.
 //
-//   warps 0-7, 8-15  softmax of streams 0 and 1, two threads to a row, each with
-//                    half of a tile's keys: one thread's chain of loads, maxima
-//                    and exponentials is longer than both products
-//   warps 16, 17     MMA of streams 0 and 1, each issued by one thread (in dual one
+//   warps 0-3, 4-7   softmax of streams 0 and 1
+//   warps 8, 9       MMA of streams 0 and 1, each issued by one thread (in dual one
 //                    thread issues both; in pair it would wait where it could issue)
-//   warp 18          producer: pages into the ring (16-bit), or codes and scales
-//                    into a ring of their own (8-bit)
-//   warps 20-23      8-bit pages: codes to fp16, into the ring
+//   warps 10, 11     producers: of K and of V, page by page into the ring (16-bit
+//                    pages); codes and scales into a ring of their own (8-bit)
+//   warps 12-15      8-bit pages: codes to fp16, into the ring
 #pragma once
 
 #include <algorithm>
@@ -67,9 +65,7 @@ struct TCfg {
     static constexpr bool kPShared = D == 128;              // P in shared memory, else in tensor memory
     static constexpr int kPBytes = 2 * kPanel;              // 128 rows x 128 keys
     static constexpr int kQTiles = kPair ? 2 : 1;
-    static constexpr int kSplit = 1;                        // softmax threads of a row
-    static constexpr int kCols = kKeys / kSplit;            // keys of each
-    static constexpr int kSoft = 8 * kSplit;                // softmax warps
+    static constexpr int kSoft = 8;                         // softmax warps
     static constexpr int kWarps = kSoft + (Q8 ? 8 : 4);
     static constexpr int oQ = 0;
     static constexpr int oP = oQ + kQTiles * kStage;
@@ -78,9 +74,8 @@ struct TCfg {
     static constexpr int oNotes = oRaw + kRaw * kRawStage;  // uint32 [kNotes]: which 16-key groups are there
     static constexpr int oTops = oNotes + kNotes * 4;       // uint32 [kNotes][4]: largest vs (bits) of a warp's rows
     static constexpr int oScales = oTops + (Q8 ? kNotes * 16 : 0);   // float [8][2][128]
-    static constexpr int oSwap = oScales + (Q8 ? 8 * 2 * kKeys * 4 : 0);     // uint32 [2][128]: the rows' maxima
-    static constexpr int oBar = oSwap + 2 * kRows * 4;
-    static constexpr int oStat = oQ;                        // float2 [2][128] and float [2][2][128], for the merge
+    static constexpr int oBar = oScales + (Q8 ? 8 * 2 * kKeys * 4 : 0);
+    static constexpr int oStat = oQ;                        // float2 [2][128], for the merge
     enum { bQ = 0, bTail, bFull, bEmpty = bFull + kStages, bRawFull = bEmpty + kStages, bRawEmpty = bRawFull + kRaw,
            bS = bRawEmpty + kRaw, bSFree = bS + 2, bP = bSFree + 2, bPv = bP + 2, bCount = bPv + 2 };
     static constexpr int oMisc = oBar + bCount * 8;
@@ -96,7 +91,7 @@ static_assert(TCfg<128, true, false>::kTotal <= 227 * 1024 && TCfg<128, false, f
 template <int D, bool Q8>
 constexpr bool merge_fits() {
     using C = TCfg<D, false, Q8>;
-    return 2 * kRows * C::kOStride * 4 <= C::oNotes - C::oP && 4 * kRows * 8 <= C::kStage;
+    return 2 * kRows * C::kOStride * 4 <= C::oNotes - C::oP && 2 * kRows * 8 <= C::kStage;
 }
 static_assert(merge_fits<64, false>() && merge_fits<64, true>() && merge_fits<128, false>() && merge_fits<128, true>(),
               "the merge uses P and the rings");
@@ -153,15 +148,6 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     return r;
 }
 
-// Order-preserving image of a number, above 0; and back.
-__device__ __forceinline__ uint32_t ordered(float x) {
-    const uint32_t u = __float_as_uint(x);
-    return u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float of_ordered(uint32_t u) {
-    return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
-}
-
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 
 // Bits [lo, hi) of a word, the bounds clamped to [0, 32].
@@ -197,13 +183,47 @@ struct KeyTiles {
     }
 };
 
-// Page of a tile's `i`-th page of `page` keys: -1 where no row sees any of it
-// (not looked up), -2 where it is not in the cache.
-__device__ __forceinline__ int32_t page_of(const AttentionArgs &a, const Reach &r, int32_t key0, int i) {
+// The order in which K and V tiles are loaded and used: the scores of a step
+// are issued before the products of the one before it.  kTiles: of a step.
+template <int kTiles>
+struct Order {
+    int n, i0 = -kTiles, i = 0;
+    bool v = false;
+    __device__ __forceinline__ explicit Order(int count) : n(count) {}
+    __device__ __forceinline__ bool next(bool *is_v, int *tile) {
+        for (;;) {
+            if (i < min(i0 + (v ? kTiles : 2 * kTiles), n)) {
+                *is_v = v;
+                *tile = i++;
+                return true;
+            }
+            if (!v && i0 >= 0) {
+                v = true;
+                i = i0;
+            } else {
+                i0 += kTiles;
+                if (i0 >= n) return false;
+                v = false;
+                i = i0 + kTiles;
+            }
+        }
+    }
+};
+
+// A tile's `i`-th page: whether some row sees any of it, and if so its entry in
+// the table (0 where not, without a look).
+__device__ __forceinline__ bool page_seen(const AttentionArgs &a, const Reach &r, int32_t key0, int i) {
     const int32_t k0 = key0 + i * a.c.page;
-    if (i * a.c.page >= kKeys || k0 >= r.end || (k0 >= r.sinks_end && k0 + a.c.page <= r.first)) return -1;
-    const int32_t pid = __ldg(a.table + r.seq * a.width + k0 / a.c.page);
-    if (pid >= 0 && pid < a.c.num_pages) return pid;
+    return i * a.c.page < kKeys && k0 < r.end && (k0 < r.sinks_end || k0 + a.c.page > r.first);
+}
+__device__ __forceinline__ int32_t page_entry(const AttentionArgs &a, const Reach &r, int32_t key0, int i) {
+    return page_seen(a, r, key0, i) ? __ldg(a.table + r.seq * a.width + (key0 / a.c.page + i)) : 0;
+}
+
+// The page of an entry: -1 where no row sees it, -2 where it is not in the cache.
+__device__ __forceinline__ int32_t page_checked(const AttentionArgs &a, bool seen, int32_t entry) {
+    if (!seen) return -1;
+    if (entry >= 0 && entry < a.c.num_pages) return entry;
     report_status(a.status, kStatusBadIndex);
     return -2;
 }
@@ -306,13 +326,13 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
             tc::mbar_init(bars + C::bEmpty + i, users);
         }
         for (int i = 0; i < C::kRaw; ++i) {
-            tc::mbar_init(bars + C::bRawFull + i, 1);
+            tc::mbar_init(bars + C::bRawFull + i, 32);
             tc::mbar_init(bars + C::bRawEmpty + i, 128);
         }
         for (int s = 0; s < 2; ++s) {
             tc::mbar_init(bars + C::bS + s, 1);
-            tc::mbar_init(bars + C::bSFree + s, C::kSplit * kRows);
-            tc::mbar_init(bars + C::bP + s, C::kSplit * kRows);
+            tc::mbar_init(bars + C::bSFree + s, kRows);
+            tc::mbar_init(bars + C::bP + s, kRows);
             tc::mbar_init(bars + C::bPv + s, 1);
         }
         tc::fence_barrier_init();
@@ -321,8 +341,6 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
             tc::prefetch_tensormap(&tm_v);
         }
     }
-    uint32_t *tops_so_far = reinterpret_cast<uint32_t *>(sm + C::oSwap);
-    if (tid < 2 * kRows) tops_so_far[tid] = 0u;             // below every number
     if (warp == C::kSoft) {
         tc::tmem_alloc(tmem_slot, 512);
         tc::tmem_relinquish();
@@ -339,29 +357,20 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
         return sight_of(a, r.start, r.lo, r.n, min(r.n - 1, r.t0 + (kPair ? s * p.tokens : 0) + row / group));
     };
 
-    // The order in which K and V tiles are loaded and used: the scores of a
-    // step are issued before the products of the one before it.
+    using TileOrder = Order<kPair ? 1 : 2>;
     const auto schedule = [](int count, const auto &use) {
-        constexpr int kAhead = kPair ? 1 : 2;               // tiles of a step
-        int q = 0;
-        for (int i = 0; i < min(kAhead, count); ++i)
-            if (!use(false, i, q++)) return;
-        for (int i0 = 0; i0 < count; i0 += kAhead) {
-            for (int i = i0 + kAhead; i < min(i0 + 2 * kAhead, count); ++i)
-                if (!use(false, i, q++)) return;
-            for (int i = i0; i < min(i0 + kAhead, count); ++i)
-                if (!use(true, i, q++)) return;
+        TileOrder order(count);
+        bool v;
+        for (int i, q = 0; order.next(&v, &i) && use(v, i, q); ++q) {
         }
     };
 
     if (warp < C::kSoft) {
-        // ------------- softmax of stream s; half h of a tile's keys, and of O's channels
-        const int s = warp / (4 * C::kSplit), h = (warp >> 2) % C::kSplit, row = tid & 127;
+        // ---------------------------------------------------- softmax of stream s
+        const int s = warp >> 2, row = tid & 127;
         const int rows = rows_of(s), steps = steps_of(s);
         const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + C::cS + uint32_t(s * kKeys) + lane_off, tO = tmem + C::cO + uint32_t(s * D) + lane_off;
-        const uint32_t both = uint32_t(1 + s * 4 + (warp & 3));     // barrier of the two warps of 32 rows
-        uint32_t *shared_top = tops_so_far + s * kRows + row;
         float back = a.scale_log2;                          // times a row's raw scores
         {
             // Q into shared memory, swizzled, by the threads of its rows (in dual of both streams)
@@ -382,8 +391,8 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 back *= exp2_int(e - 14);
                 to = exp2_int(14 - e);
             }
-            constexpr int kMine = D / 8 / (C::kSplit * (kPair ? 1 : 2));
-            const int c0 = (kPair ? h : C::kSplit * s + h) * kMine;
+            constexpr int kMine = D / 8 / (kPair ? 1 : 2);
+            const int c0 = kPair ? 0 : s * kMine;
 #pragma unroll 4
             for (int c = c0; c < c0 + kMine; ++c) {
                 uint4 x = there ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
@@ -399,9 +408,9 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
             tc::mbar_arrive(bars + C::bQ);
         }
         const Sight sight = sight_at(s, max(0, min(row, rows - 1)));
-        const bool active = (warp & 3) * 32 < rows;         // any row in this warp (and its other half)
+        const bool active = (warp & 3) * 32 < rows;         // any row in this warp
         const int32_t lo_max = __reduce_max_sync(kAll, sight.lo), hi_min = __reduce_min_sync(kAll, sight.hi);
-        float m = kMinusInf, l = 0.f;                       // l over this thread's keys
+        float m = kMinusInf, l = 0.f;
         int big = -110;                                     // E of the weights (8-bit pages)
         bool ok = true;
         for (int t = 0; t < steps; ++t) {
@@ -412,13 +421,13 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
             ok &= tc::mbar_wait(bars + C::bS + s, t & 1, status);
             tc::tc_fence_after();
             if (active) {
-                const uint32_t there = notes[i % kNotes] & 0xffu;
+                const uint32_t there = notes[i % kNotes];
                 const bool full = key0 >= lo_max && key0 + kKeys <= hi_min && there == 0xffu;
-                const float4 *ks = reinterpret_cast<const float4 *>(sm + C::oScales) + (i % 8) * 64 + h * (C::kCols / 4);
+                const float4 *ks = reinterpret_cast<const float4 *>(sm + C::oScales) + (i % 8) * 64;
                 const float4 *vs = ks + 32;
                 const auto admitted = [&](int c) {
-                    const uint32_t g = there >> (h * (C::kCols / 16) + 2 * c);
-                    return seen_bits(sight, int32_t(r.start), sinks, key0 + h * C::kCols + c * 32) &
+                    const uint32_t g = there >> (2 * c);
+                    return seen_bits(sight, int32_t(r.start), sinks, key0 + c * 32) &
                            ((g & 1u ? 0xffffu : 0u) | (g & 2u ? 0xffff0000u : 0u));
                 };
                 const auto mask = [&](uint32_t adm, float *x) {
@@ -430,7 +439,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 // 8-bit pages: scores of 32 keys in log2 units
                 const auto scores8 = [&](int c, float *x) {
                     uint32_t raw[32];
-                    tc::tmem_ld32(tS + uint32_t(h * C::kCols + c * 32), raw);
+                    tc::tmem_ld32(tS + uint32_t(c * 32), raw);
                     tc::tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
@@ -453,79 +462,72 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                         for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[j + e], x[j + 4 + e]);
                 };
                 // 16-bit pages: the scores are held from the maximum to the
-                // weights; 8-bit pages read them twice (the scales need registers)
-                float x[Q8 ? 32 : C::kCols];
-                if constexpr (Q8) {
-#pragma unroll 1
-                    for (int c = 0; c < C::kCols / 32; ++c) {
-                        scores8(c, x);
-                        if (!full) mask(admitted(c), x);
-                        largest(x);
-                    }
-                } else {
-                    uint32_t raw[C::kCols / 32][32];
+                // weights; 8-bit pages read them with their scales, find the
+                // maximum on the way and start again where it had grown
+                float x[Q8 ? 32 : kKeys];
+                if constexpr (!Q8) {
+                    uint32_t raw[kKeys / 32][32];
 #pragma unroll
-                    for (int c = 0; c < C::kCols / 32; ++c) tc::tmem_ld32(tS + uint32_t(h * C::kCols + c * 32), raw[c]);
+                    for (int c = 0; c < kKeys / 32; ++c) tc::tmem_ld32(tS + uint32_t(c * 32), raw[c]);
                     tc::tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < C::kCols; ++j) x[j] = __uint_as_float(raw[j / 32][j % 32]);
+                    for (int j = 0; j < kKeys; ++j) x[j] = __uint_as_float(raw[j / 32][j % 32]);
                     tc::tc_fence_before();
                     tc::mbar_arrive(bars + C::bSFree + s);  // the next scores may come
                     if (!full)
 #pragma unroll
-                        for (int c = 0; c < C::kCols / 32; ++c) mask(admitted(c), x + c * 32);
+                        for (int c = 0; c < kKeys / 32; ++c) mask(admitted(c), x + c * 32);
 #pragma unroll
-                    for (int c = 0; c < C::kCols / 32; ++c) largest(x + c * 32);
+                    for (int c = 0; c < kKeys / 32; ++c) largest(x + c * 32);
                 }
-                // the row's maximum, once it has grown enough (with two threads
-                // to a row, in either half)
-                float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-                if (!Q8) top *= back;
-                float corr = 1.f;
-                bool grown = top > m + kLazy || m == kMinusInf;
-                if (C::kSplit == 2 && !tc::named_bar_and(both, 64, !grown)) {
-                    atomicMax(shared_top, ordered(top));    // it only grows from step to step
-                    tc::named_bar_sync(both, 64);
-                    top = of_ordered(*shared_top);
-                    grown = top > m + kLazy || m == kMinusInf;
-                }
-                if (grown) {
-                    const float mn = fmaxf(m, top);
-                    corr = mn == kMinusInf ? 1.f : exp2_ftz(m - mn);
-                    m = mn;
-                }
-                l *= corr;
+                // The row's maximum, once it has grown enough.
+                float corr = 1.f, base;
+                const auto follow = [&] {
+                    float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+                    if (!Q8) top *= back;
+                    const bool grown = top > m + kLazy || (m == kMinusInf && top > kMinusInf);
+                    if (grown) {
+                        const float c = exp2_ftz(m - top);
+                        corr *= c;
+                        l *= c;
+                        m = top;
+                    }
+                    base = m == kMinusInf ? 0.f : m;
+                    return grown;
+                };
                 float vf = 1.f;
                 if (Q8) {
                     const uint4 tops = *reinterpret_cast<const uint4 *>(sm + C::oTops + (i % kNotes) * 16);
                     const int e = min(int(max(max(tops.x, tops.y), max(tops.z, tops.w)) >> 23), 254) - 127;
                     if (e > big) {
-                        corr *= exp2_int(max(big - e, -126));
+                        corr = exp2_int(max(big - e, -126));
                         big = e;
                     }
                     vf = exp2_int(kWeightShift - big);
                 }
-                const float base = m == kMinusInf ? 0.f : m;
-                const float2 n2 = make_float2(-base, -base), f2 = make_float2(vf, vf);
-                float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                follow();                                   // (8-bit pages: nothing yet, the base as it is)
                 // O and P are this step's once the product of the last is done
+                const auto rescale = [&] {
+                    if (t == 0 || !__any_sync(kAll, corr != 1.f)) return;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tc::tmem_ld16(tO + uint32_t(c), o);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
+                        tc::tmem_st16(tO + uint32_t(c), o);
+                    }
+                };
                 const auto settle = [&] {
                     if (t > 0) ok &= tc::mbar_wait(bars + C::bPv + s, (t - 1) & 1, status);
                     tc::tc_fence_after();
-                    if (t > 0 && __any_sync(kAll, corr != 1.f)) {
-#pragma unroll 1
-                        for (int c = h * (D / C::kSplit); c < (h + 1) * (D / C::kSplit); c += 16) {
-                            uint32_t o[16];
-                            tc::tmem_ld16(tO + uint32_t(c), o);
-                            tc::tmem_ld_wait();
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
-                            tc::tmem_st16(tO + uint32_t(c), o);
-                        }
-                    }
                 };
+                const float2 f2 = make_float2(vf, vf);
+                float2 ls[2];
                 uint32_t pk[32];                            // weights of 64 keys
                 const auto weights = [&](int c, const float *x, uint32_t *to) {
+                    const float2 n2 = make_float2(-base, -base);
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
                         const float4 v4 = Q8 ? vs[c * 8 + j / 4] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -545,8 +547,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                         }
                     }
                 };
-                const auto publish = [&](int p64) {         // of the thread's p64-th 64 keys
-                    const int panel = h * (C::kCols / 64) + p64;
+                const auto publish = [&](int panel) {       // 64 keys
                     if (C::kPShared) {
                         uint8_t *dst = sm + C::oP + s * C::kPBytes + panel * C::kPanel + row * 128;
 #pragma unroll
@@ -559,34 +560,44 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                     }
                 };
                 if constexpr (Q8) {
+                    settle();
+                    for (;;) {
+                        rescale();
+                        corr = 1.f;
+                        ls[0] = ls[1] = make_float2(0.f, 0.f);
 #pragma unroll 1
-                    for (int p64 = 0; p64 < C::kCols / 64; ++p64) {
+                        for (int p64 = 0; p64 < kKeys / 64; ++p64) {
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int c = 2 * p64 + k;
-                            scores8(c, x);
-                            const uint32_t adm = full ? kAll : admitted(c);
-                            if (!full) mask(adm, x);
-                            weights(c, x, pk + 16 * k);
-                            if (!full)                      // the scale of a masked key may be anything
+                            for (int k = 0; k < 2; ++k) {
+                                const int c = 2 * p64 + k;
+                                scores8(c, x);
+                                const uint32_t adm = full ? kAll : admitted(c);
+                                if (!full) mask(adm, x);
+                                largest(x);
+                                weights(c, x, pk + 16 * k);
+                                if (!full)                  // the scale of a masked key may be anything
 #pragma unroll
-                                for (int j = 0; j < 16; ++j)
-                                    pk[16 * k + j] &= (((adm >> (2 * j)) & 1u) ? 0xffffu : 0u) |
-                                                      (((adm >> (2 * j + 1)) & 1u) ? 0xffff0000u : 0u);
+                                    for (int j = 0; j < 16; ++j)
+                                        pk[16 * k + j] &= (((adm >> (2 * j)) & 1u) ? 0xffffu : 0u) |
+                                                          (((adm >> (2 * j + 1)) & 1u) ? 0xffff0000u : 0u);
+                            }
+                            publish(p64);
                         }
-                        if (p64 == C::kCols / 64 - 1) {
-                            tc::tc_fence_before();
-                            tc::mbar_arrive(bars + C::bSFree + s);
-                        }
-                        if (p64 == 0) settle();
-                        publish(p64);
+                        // once more at most: the maximum is that of all keys now
+                        if (!__any_sync(kAll, follow())) break;
                     }
+                    tc::tc_fence_before();
+                    tc::mbar_arrive(bars + C::bSFree + s);
                 } else {
+                    ls[0] = ls[1] = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int p64 = 0; p64 < C::kCols / 64; ++p64) {
+                    for (int p64 = 0; p64 < kKeys / 64; ++p64) {
                         weights(2 * p64, x + p64 * 64, pk);
                         weights(2 * p64 + 1, x + p64 * 64 + 32, pk + 16);
-                        if (p64 == 0) settle();
+                        if (p64 == 0) {
+                            settle();
+                            rescale();
+                        }
                         publish(p64);
                     }
                 }
@@ -604,21 +615,14 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
         if (steps > 0) ok &= tc::mbar_wait(bars + C::bPv + s, (steps - 1) & 1, status);
         tc::tc_fence_after();
         const float un = Q8 ? exp2_int(big - kWeightShift) : 1.f;
-        if (!kPair) tc::named_bar_sync(9, 32 * C::kSoft);   // nothing reads Q, P and the rings any more
-        if (C::kSplit == 2) {
-            // the row's sum (in pair over the stream's own Q, in dual behind the states)
-            float *swap = reinterpret_cast<float *>(sm + C::oQ + (kPair ? s * C::kStage : 2 * kRows * 8 + s * 2 * kRows * 4)) + row;
-            swap[h * kRows] = l;
-            tc::named_bar_sync(both, 64);
-            l += swap[(1 - h) * kRows];
-        }
+        if (!kPair) tc::named_bar_sync(1, 32 * C::kSoft);   // nothing reads Q, P and the rings any more
         if (kPair) {
             const float inv = (l > 0.f || l != l ? __fdiv_rn(1.f, l) : 0.f) * un;
             bool finite = true;
             if (ok && active) {
                 uint16_t *dst = a.out + token_row(s, min(row, rows - 1), int64_t(a.q_heads) * D);
 #pragma unroll 1
-                for (int c = h * (D / C::kSplit); c < (h + 1) * (D / C::kSplit); c += 32) {
+                for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
                     tc::tmem_ld32(tO + uint32_t(c), o);
                     tc::tmem_ld_wait();
@@ -646,7 +650,6 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                         float x[D / 32];
                         row_alone<D>(a, r, sight_at(s, which), head, a.q + token_row(s, which, a.q_stride), x);
                         uint16_t *to = a.out + token_row(s, which, int64_t(a.q_heads) * D) + lane * (D / 32);
-                        if (C::kSplit == 1 || lane >> 4 == h)
 #pragma unroll
                             for (int e = 0; e < D / 32; ++e) to[e] = f32_to_bf16_bits(x[e]);
                     }
@@ -655,13 +658,12 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
         } else {
             // the stream's state, for the merge
             const bool any = ok && steps > 0 && l != 0.f;
-            if (h == 0)
-                reinterpret_cast<float2 *>(sm + C::oStat)[s * kRows + row] =
-                    any ? make_float2(m, l) : make_float2(kMinusInf, 0.f);
+            reinterpret_cast<float2 *>(sm + C::oStat)[s * kRows + row] =
+                any ? make_float2(m, l) : make_float2(kMinusInf, 0.f);
             float *dst = reinterpret_cast<float *>(sm + C::oP) + (s * kRows + row) * C::kOStride;
             if (ok && steps > 0 && active)
 #pragma unroll 1
-                for (int c = h * (D / C::kSplit); c < (h + 1) * (D / C::kSplit); c += 32) {
+                for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
                     tc::tmem_ld32(tO + uint32_t(c), o);
                     tc::tmem_ld_wait();
@@ -729,72 +731,51 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                     });
             }
             __syncwarp();
-        } else if (warp == C::kSoft + 2) {
-            // ------------------------------------------------------- producer
+        } else if (!Q8) {
+            // ------------------------------- producers, one of K and one of V
+            const bool of_v = warp == C::kSoft + 3;
             const int pages = kKeys / a.c.page, per16 = a.c.page / 16, tiles_at_once = 32 / pages;
-            // pages of the tiles from i on, one to a lane
+            // entries of the tiles from i on, one to a lane
             const auto look_up = [&](int i) {
                 const int u = i + lane / pages;
-                return u < n ? page_of(a, r, tiles.key0(u), lane % pages) : -1;
+                return u < n ? page_entry(a, r, tiles.key0(u), lane % pages) : 0;
             };
-            // K and V each look up their own tiles: K runs ahead
-            int32_t ids[2] = {-1, -1}, next[2] = {look_up(0), look_up(0)};
+            int32_t ids = -1, next = look_up(0);
             bool ok = true;
             schedule(n, [&](bool v, int i, int q) {
-                const int at = i % tiles_at_once * pages;
-                int32_t &mine = v ? ids[1] : ids[0], &then = v ? next[1] : next[0];
+                if (v != of_v) return true;
+                const int at = i % tiles_at_once * pages, st = q % C::kStages;
                 if (at == 0) {
-                    mine = then;
-                    then = look_up(i + tiles_at_once);
+                    const int u = i + lane / pages;
+                    ids = page_checked(a, u < n && page_seen(a, r, tiles.key0(u), lane % pages), next);
+                    next = look_up(i + tiles_at_once);
                 }
-                constexpr int kSlots = Q8 ? C::kRaw : C::kStages;
-                const int st = q % (Q8 ? C::kRaw : C::kStages);
-                uint64_t *full = bars + (Q8 ? C::bRawFull : C::bFull) + st;
-                if (q >= kSlots)
-                    ok = __all_sync(kAll, tc::mbar_wait(bars + (Q8 ? C::bRawEmpty : C::bEmpty) + st,
-                                                        (q / kSlots - 1) & 1, status));
+                if (q >= C::kStages)
+                    ok = __all_sync(kAll, tc::mbar_wait(bars + C::bEmpty + st, (q / C::kStages - 1) & 1, status));
                 if (!ok) return false;
-                const uint32_t here = (__ballot_sync(kAll, mine >= 0) >> at) & ((1u << pages) - 1);
-                if (!v) {
-                    // groups of 16 keys: bits 0-7 not known to be gone, 8-15 copied
-                    const uint32_t gone = (__ballot_sync(kAll, mine == -2) >> at) & ((1u << pages) - 1);
-                    uint32_t note = 0xffu;
-                    for (int g = 0; g < pages; ++g) {
-                        const uint32_t bits = ((1u << per16) - 1) << (g * per16);
-                        if ((gone >> g) & 1u) note &= ~bits;
-                        if ((here >> g) & 1u) note |= bits << 8;
+                const uint32_t gone = (__ballot_sync(kAll, ids == -2) >> at) & ((1u << pages) - 1);
+                if (lane == 0) {
+                    if (!v) {
+                        uint32_t there = 0xffu;
+                        for (uint32_t g = gone; g != 0; g &= g - 1)
+                            there &= ~(((1u << per16) - 1) << ((__ffs(g) - 1) * per16));
+                        notes[i % kNotes] = there;
                     }
-                    if (lane == 0) notes[i % kNotes] = note;
+                    tc::mbar_arrive_expect_tx(bars + C::bFull + st, C::kStage);
                 }
-                if (lane == 0)
-                    tc::mbar_arrive_expect_tx(
-                        full, Q8 ? uint32_t(__popc(here) * a.c.page * (D + (v ? 0 : 8))) : uint32_t(C::kStage));
                 __syncwarp();
                 for (int g = 0; g < pages; ++g) {
-                    const int32_t pid = __shfl_sync(kAll, mine, at + g);
-                    if (lane != 0) continue;
-                    if (Q8) {
-                        if (pid < 0) continue;
-                        const int64_t row0 = (int64_t(pid) * a.c.heads + head) * a.c.page;
-                        uint8_t *dst = sm + C::oRaw + st * C::kRawStage;
-                        tc::bulk_g2s(dst + g * a.c.page * D, reinterpret_cast<const int8_t *>(v ? a.c.v : a.c.k) + row0 * D,
-                                     uint32_t(a.c.page * D), full);
-                        if (!v) {
-                            float *sc = reinterpret_cast<float *>(dst + kKeys * D) + g * a.c.page;
-                            tc::bulk_g2s(sc, a.ks + row0, uint32_t(a.c.page * 4), full);
-                            tc::bulk_g2s(sc + kKeys, a.vs + row0, uint32_t(a.c.page * 4), full);
-                        }
-                    } else {
+                    const int32_t pid = __shfl_sync(kAll, ids, at + g);
+                    if (lane == 0)
 #pragma unroll
                         for (int sub = 0; sub < C::kSub; ++sub)     // what is not there arrives as zeros
                             tc::tma_load_4d(sm + C::oRing + st * C::kStage + sub * C::kPanel + g * a.c.page * 128,
-                                            v ? &tm_v : &tm_k, full, sub * 64, 0, head, pid < 0 ? -1 : pid);
-                    }
+                                            v ? &tm_v : &tm_k, bars + C::bFull + st, sub * 64, 0, head, pid < 0 ? -1 : pid);
                 }
                 __syncwarp();
                 return true;
             });
-            if (!Q8 && ok && n > 0) {
+            if (of_v && ok && n > 0) {
                 // rows past the last key hold anything, and 0 times NaN must not reach O
                 const int q = 2 * n - 1, st = q % C::kStages, tail = r.end - tiles.key0(n - 1);
                 if (tail < kKeys && tc::mbar_wait(bars + C::bFull + st, (q / C::kStages) & 1, status))
@@ -807,39 +788,88 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(bars + C::bTail);
             }
-        } else if (Q8 && warp >= C::kSoft + 4) {
-            // --------------------------- codes to fp16, rows that nothing sees to zero
-            constexpr int kPer = D / 16;                    // 16-byte pieces of a row
+        } else if (warp < C::kSoft + 4) {
+            // ---- 8-bit pages: codes and scales into a ring of their own, a warp for K
+            // and one for V, in pieces of 16 and 4 bytes (bulk copies, one for
+            // each page and its scales, take one thread 200 cycles each)
+            const bool of_v = warp == C::kSoft + 3;
+            constexpr int kPer = D / 16;                    // pieces of a row
+            constexpr int kRaw = C::kRaw > 0 ? C::kRaw : 1;
+            const int page = a.c.page, shift = 31 - __clz(page);
+            // entries of tile i, one to each of eight lanes; used a tile later
+            const auto entries = [&](int i) { return i < n && lane < 8 ? page_entry(a, r, tiles.key0(i), lane) : 0; };
+            int32_t next = entries(0);
+            schedule(n, [&](bool v, int i, int q) {
+                if (v != of_v) return true;
+                const int32_t key0 = tiles.key0(i);
+                const int raw = q % kRaw;
+                const int32_t ids = page_checked(a, lane < 8 && page_seen(a, r, key0, lane), next);
+                next = entries(i + 1);
+                const uint32_t gone = __ballot_sync(kAll, ids == -2);
+                // this lane's page: its first row in the cache
+                const int64_t base = ids < 0 ? -1 : (int64_t(ids) * a.c.heads + head) * page;
+                const int end = r.end - key0, hide = r.sinks_end - key0, show = r.first - key0;
+                const auto row_in = [&](int x) -> int64_t { // -1: nothing sees it
+                    const int64_t row0 = __shfl_sync(kAll, base, x >> shift);
+                    return row0 < 0 || x >= end || (x >= hide && x < show) ? -1 : row0 + (x & (page - 1));
+                };
+                if (q >= kRaw &&
+                    !__all_sync(kAll, tc::mbar_wait(bars + C::bRawEmpty + raw, (q / kRaw - 1) & 1, status)))
+                    return false;
+                uint8_t *dst = sm + C::oRaw + raw * C::kRawStage;
+                const int8_t *src = reinterpret_cast<const int8_t *>(v ? a.c.v : a.c.k);
+#pragma unroll
+                for (int j = 0; j < kPer * 4; ++j) {
+                    const int c = j * 32 + lane;
+                    const int64_t at = row_in(c / kPer);
+                    tc::cp_async16_zfill(dst + c * 16, src + (at < 0 ? 0 : at) * D + c % kPer * 16, at >= 0);
+                }
+                if (!v) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int64_t at = row_in(lane + 32 * j);
+                        float *sc = reinterpret_cast<float *>(dst + kKeys * D) + lane + 32 * j;
+                        tc::cp_async4_zfill(sc, a.ks + (at < 0 ? 0 : at), at >= 0);
+                        tc::cp_async4_zfill(sc + kKeys, a.vs + (at < 0 ? 0 : at), at >= 0);
+                    }
+                    if (lane == 0) {
+                        uint32_t there = 0xffu;
+                        for (uint32_t g = gone; g != 0; g &= g - 1)
+                            there &= ~(((1u << (page / 16)) - 1) << ((__ffs(g) - 1) * (page / 16)));
+                        notes[i % kNotes] = there;
+                    }
+                }
+                tc::cp_async_arrive(bars + C::bRawFull + raw);
+                return true;
+            });
+            tc::cp_async_wait_all();
+        } else {
+            // ----------------------------------------- codes to fp16, into the ring
+            constexpr int kPer = D / 16;
+            constexpr int kRaw = C::kRaw > 0 ? C::kRaw : 1;
             const int w = tid - (C::kSoft + 4) * 32;
             float *scales = reinterpret_cast<float *>(sm + C::oScales);
-            constexpr int kSlots = C::kRaw > 0 ? C::kRaw : 1;
             schedule(n, [&](bool v, int i, int q) {
-                const int32_t key0 = tiles.key0(i);
-                const int raw = q % kSlots, st = q % C::kStages;
+                const int st = q % C::kStages, raw = q % kRaw;
                 const bool ok =
-                    tc::mbar_wait(bars + C::bRawFull + raw, (q / kSlots) & 1, status) &&
+                    tc::mbar_wait(bars + C::bRawFull + raw, (q / kRaw) & 1, status) &&
                     (q < C::kStages || tc::mbar_wait(bars + C::bEmpty + st, (q / C::kStages - 1) & 1, status));
                 if (!__all_sync(kAll, ok)) return false;
                 const uint8_t *src = sm + C::oRaw + raw * C::kRawStage;
                 uint8_t *stage = sm + C::oRing + st * C::kStage;
-                const uint32_t note = notes[i % kNotes];
-                const auto seen = [&](int x) {
-                    const int32_t key = key0 + x;
-                    return ((note >> (8 + x / 16)) & 1u) && key < r.end && (key < r.sinks_end || key >= r.first);
-                };
                 if (!v) {
-                    const float *sc = reinterpret_cast<const float *>(src + kKeys * D);
-                    const float sk = seen(w) ? sc[w] : 0.f, sv = seen(w) ? sc[kKeys + w] : 0.f;
-                    scales[(i % 8) * 2 * kKeys + w] = sk;
+                    const float *sc = reinterpret_cast<const float *>(src + kKeys * D) + w;
+                    const float sv = sc[kKeys];
+                    scales[(i % 8) * 2 * kKeys + w] = sc[0];
                     scales[((i % 8) * 2 + 1) * kKeys + w] = sv;
                     const uint32_t top = __reduce_max_sync(kAll, sv == sv ? __float_as_uint(sv) & 0x7fffffffu : 0u);
                     if (lane == 0) reinterpret_cast<uint32_t *>(sm + C::oTops)[(i % kNotes) * 4 + (w >> 5)] = top;
                 }
-#pragma unroll 4
+#pragma unroll
                 for (int j = 0; j < kPer; ++j) {
                     const int c = j * 128 + w, row = c / kPer, ch = c % kPer;
-                    const uint4 x = seen(row) ? *reinterpret_cast<const uint4 *>(src + c * 16) : make_uint4(0u, 0u, 0u, 0u);
-                    store_codes(stage + (ch >> 2) * C::kPanel + row * 128, (ch & 3) * 2, row, x);
+                    store_codes(stage + (ch >> 2) * C::kPanel + row * 128, (ch & 3) * 2, row,
+                                *reinterpret_cast<const uint4 *>(src + c * 16));
                 }
                 tc::fence_proxy_async_smem();
                 tc::mbar_arrive(bars + C::bFull + st);

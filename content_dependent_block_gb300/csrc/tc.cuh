@@ -345,6 +345,16 @@ __device__ __forceinline__ void cp_async16_zfill(void *dst, const void *src, boo
                  "r"(valid ? 16u : 0u)
                  : "memory");
 }
+// The same with 4 bytes.
+__device__ __forceinline__ void cp_async4_zfill(void *dst, const void *src, bool valid) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),
+                 "r"(valid ? 4u : 0u)
+                 : "memory");
+}
+// Arrive on `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 // Order this thread's earlier generic-proxy accesses of global memory before
 // its later async-proxy (bulk copy / TMA) accesses.
 __device__ __forceinline__ void fence_proxy_async_global() {
