@@ -183,33 +183,6 @@ struct KeyTiles {
     }
 };
 
-// The order in which K and V tiles are loaded and used: the scores of a step
-// are issued before the products of the one before it.  kTiles: of a step.
-template <int kTiles>
-struct Order {
-    int n, i0 = -kTiles, i = 0;
-    bool v = false;
-    __device__ __forceinline__ explicit Order(int count) : n(count) {}
-    __device__ __forceinline__ bool next(bool *is_v, int *tile) {
-        for (;;) {
-            if (i < min(i0 + (v ? kTiles : 2 * kTiles), n)) {
-                *is_v = v;
-                *tile = i++;
-                return true;
-            }
-            if (!v && i0 >= 0) {
-                v = true;
-                i = i0;
-            } else {
-                i0 += kTiles;
-                if (i0 >= n) return false;
-                v = false;
-                i = i0 + kTiles;
-            }
-        }
-    }
-};
-
 // A tile's `i`-th page: whether some row sees any of it, and if so its entry in
 // the table (0 where not, without a look).
 __device__ __forceinline__ bool page_seen(const AttentionArgs &a, const Reach &r, int32_t key0, int i) {
@@ -357,11 +330,36 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
         return sight_of(a, r.start, r.lo, r.n, min(r.n - 1, r.t0 + (kPair ? s * p.tokens : 0) + row / group));
     };
 
-    using TileOrder = Order<kPair ? 1 : 2>;
+    // The order in which K and V tiles are loaded and used: the scores of a
+    // step are issued before the products of the one before it.
+    constexpr int kAhead = kPair ? 1 : 2;                   // tiles of a step
+    // for the thread that issues products, with as little as possible between them
     const auto schedule = [](int count, const auto &use) {
-        TileOrder order(count);
-        bool v;
-        for (int i, q = 0; order.next(&v, &i) && use(v, i, q); ++q) {
+        int q = 0;
+        for (int i = 0; i < min(kAhead, count); ++i)
+            if (!use(false, i, q++)) return;
+        for (int i0 = 0; i0 < count; i0 += kAhead) {
+            for (int i = i0 + kAhead; i < min(i0 + 2 * kAhead, count); ++i)
+                if (!use(false, i, q++)) return;
+            for (int i = i0; i < min(i0 + kAhead, count); ++i)
+                if (!use(true, i, q++)) return;
+        }
+    };
+    // the same for larger bodies, which it has once (24 trees over 8-bit pages:
+    // 342 us with three copies, 267 us)
+    const auto schedule_once = [](int count, const auto &use) {
+        bool v = false;
+        for (int q = 0, i = 0, i0 = -kAhead; q < 2 * count;) {
+            if (i < min(i0 + (v ? kAhead : 2 * kAhead), count)) {
+                if (!use(v, i++, q++)) return;
+            } else if (!v && i0 >= 0) {
+                v = true;
+                i = i0;
+            } else {
+                i0 += kAhead;
+                v = false;
+                i = i0 + kAhead;
+            }
         }
     };
 
@@ -742,7 +740,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
             };
             int32_t ids = -1, next = look_up(0);
             bool ok = true;
-            schedule(n, [&](bool v, int i, int q) {
+            schedule_once(n, [&](bool v, int i, int q) {
                 if (v != of_v) return true;
                 const int at = i % tiles_at_once * pages, st = q % C::kStages;
                 if (at == 0) {
@@ -799,7 +797,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
             // entries of tile i, one to each of eight lanes; used a tile later
             const auto entries = [&](int i) { return i < n && lane < 8 ? page_entry(a, r, tiles.key0(i), lane) : 0; };
             int32_t next = entries(0);
-            schedule(n, [&](bool v, int i, int q) {
+            schedule_once(n, [&](bool v, int i, int q) {
                 if (v != of_v) return true;
                 const int32_t key0 = tiles.key0(i);
                 const int raw = q % kRaw;
@@ -849,7 +847,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
             constexpr int kRaw = C::kRaw > 0 ? C::kRaw : 1;
             const int w = tid - (C::kSoft + 4) * 32;
             float *scales = reinterpret_cast<float *>(sm + C::oScales);
-            schedule(n, [&](bool v, int i, int q) {
+            schedule_once(n, [&](bool v, int i, int q) {
                 const int st = q % C::kStages, raw = q % kRaw;
                 const bool ok =
                     tc::mbar_wait(bars + C::bRawFull + raw, (q / kRaw) & 1, status) &&
@@ -1020,7 +1018,7 @@ cudaError_t launch_tiles_form(const AttentionArgs &a, cudaStream_t st) {
         int64_t keys = int64_t(a.width) * a.c.page;
         if (a.window > 0) keys = std::min<int64_t>(keys, int64_t(a.window) + a.sinks + p.tokens);
         const int64_t busy = a.cu != nullptr ? (a.tokens / p.tokens + a.seqs) * a.c.heads : items;
-        const int limit[4] = {152, 76, 36, 15};
+        const int limit[4] = {152, 152, 152, 76};
         int log = 0;
         while (log < 3 && busy <= limit[log + 1] && keys >= (int64_t(kKeys) << (log + 2))) ++log;
         p.cluster = 1 << log;
