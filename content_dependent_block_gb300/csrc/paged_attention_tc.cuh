@@ -722,6 +722,10 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                     tc::mma_commit(bars + C::bEmpty + st);
                     return true;
                 };
+                // Stream 1 starts once stream 0 has read its first scores: out of
+                // step, one's exponentials run under the other's loads and maxima
+                // (3 prompts: 446 -> 430 us; a longer delay gains nothing more).
+                if (kPair && warp == C::kSoft + 1) tc::mbar_wait(bars + C::bSFree, 0, status);
                 if (steps_of(warp - C::kSoft) > 0 && tc::mbar_wait(bars + C::bQ, 0, status))
                     schedule(n, [&](bool v, int i, int q) {
                         const int s = kPair ? warp - C::kSoft : i & 1, t = kPair ? i : i >> 1;

@@ -60,10 +60,42 @@ __device__ __forceinline__ bool find_span(const int32_t *cu, int64_t seqs, int64
     return true;
 }
 
+// Two numbers at a time.
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+    uint64_t a, b, c, r;
+    float2 o;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(x.x), "f"(x.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(y.x), "f"(y.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(z.x), "f"(z.y));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+    return o;
+}
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+    uint64_t a, b, r;
+    float2 o;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(x.x), "f"(x.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(y.x), "f"(y.y));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+    return o;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+    uint64_t a, b, r;
+    float2 o;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(x.x), "f"(x.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(y.x), "f"(y.y));
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+    return o;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 // Quantises a row of which each of the CH lanes of a group has 8 channels;
-// every lane of the warp takes part.  Returns the row's scale.
+// every lane of the warp takes part.  Returns the row's scale, and the codes also
+// as floats.
 template <int CH>
-__device__ __forceinline__ float quantise(const uint4 &x, uint2 *codes) {
+__device__ __forceinline__ float quantise(const uint4 &x, uint2 *codes, float2 (&value)[4]) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     uint32_t m = 0u;
 #pragma unroll
@@ -73,6 +105,8 @@ __device__ __forceinline__ float quantise(const uint4 &x, uint2 *codes) {
     for (int o = CH / 2; o > 0; o /= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float a = __uint_as_float(m << 16);
     *codes = make_uint2(0u, 0u);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) value[e] = make_float2(0.f, 0.f);
     if (m == 0u) return 0.f;
     if (m >= 0x7f80u) return __uint_as_float(0x7fc00000u);      // an infinity or a NaN: all of it is NaN
     // times 2^(120 - E), E the exponent's field: a comes to [2^-14, 2^-6), and
@@ -80,21 +114,30 @@ __device__ __forceinline__ float quantise(const uint4 &x, uint2 *codes) {
     const int exponent = max(int(m >> 7), 1);
     const float factor = exponent <= 246 ? __uint_as_float(uint32_t(247 - exponent) << 23)
                                          : __uint_as_float(1u << (22 - (exponent - 247)));
-    const float as = a * factor, r = __frcp_rn(as), c = 127.f * factor;
+    const float as = a * factor;
+    float r;                            // within an ulp or two is enough for the correction
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(as));
+    const float2 c2 = both(127.f * factor), r2 = both(r), n2 = both(-as);
+    const float2 shift = both(12582912.f), back = both(-12582912.f);   // 1.5 * 2^23: the low byte is the code
     uint32_t q[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float t = ((e & 1) ? bf16_high_half(w[e / 2]) : bf16_low_half(w[e / 2])) * c;
-        const float y0 = __fmul_rn(t, r);
-        const float y = __fmaf_rn(__fmaf_rn(-y0, as, t), r, y0);
-        q[e] = __float_as_uint(__fadd_rn(y, 12582912.f));       // 1.5 * 2^23: the low byte is the code
+    for (int e = 0; e < 4; ++e) {
+        const float2 t = mul2(make_float2(bf16_low_half(w[e]), bf16_high_half(w[e])), c2);
+        const float2 y0 = mul2(t, r2);
+        const float2 y = add2(fma2(fma2(y0, n2, t), r2, y0), shift);
+        value[e] = add2(y, back);
+        q[2 * e] = __float_as_uint(y.x);
+        q[2 * e + 1] = __float_as_uint(y.y);
     }
     const auto bytes = [&](int e) {
         return __byte_perm(__byte_perm(q[e], q[e + 1], 0x0040), __byte_perm(q[e + 2], q[e + 3], 0x0040),
                            0x5410);
     };
     *codes = make_uint2(bytes(0), bytes(4));
-    return __fdiv_rn(a, 127.f);
+    if (exponent < 32) return __fdiv_rn(a, 127.f);              // a scale that may be subnormal
+    // a / 127, corrected the same way: 1 / 127 to the nearest, then the residual
+    const float s0 = __fmul_rn(a, 1.f / 127.f);
+    return __fmaf_rn(__fmaf_rn(s0, -127.f, a), 1.f / 127.f, s0);
 }
 
 // The i-th signed byte of eight, as a float.
@@ -112,7 +155,7 @@ __global__ void __launch_bounds__(kThreads) append8_kernel(Append8Args a, int64_
     constexpr int CH = D / 8;
     constexpr int RG = kThreads / CH;       // rows per pass
     constexpr int U = 4;
-    __shared__ float part[RG][D];
+    __shared__ __align__(8) float part[RG][D];
     Span sp;
     if (!find_span(a.cu, a.seqs, a.tokens, items_each, a.start, a.table, a.width, a.c.page, a.c.num_pages,
                    a.status, &sp))
@@ -122,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) append8_kernel(Append8Args a, int64_
     const int64_t row0 = (sp.pid * a.c.heads + head) * page;     // of the page's scales
     const uint16_t *kn = a.k + (sp.tok - sp.r0) * a.k_stride + int64_t(head) * D + ch * 8;
     const uint16_t *vn = a.v + (sp.tok - sp.r0) * a.v_stride + int64_t(head) * D + ch * 8;
-    float acc[8] = {};
+    float2 acc[4] = {};
     for (int32_t base = 0; base < sp.r1; base += U * RG) {       // the same passes for every warp
         uint4 x[U], y[U];
         uint2 old[U];
@@ -142,9 +185,11 @@ __global__ void __launch_bounds__(kThreads) append8_kernel(Append8Args a, int64_
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int32_t r = base + u * RG + rg;
+            if (base + u * RG >= sp.r1) break;                  // for the whole CTA
             uint2 kc, vc;
-            float ks = quantise<CH>(x[u], &kc);
-            const float vs = quantise<CH>(y[u], &vc);
+            float2 kv[4], vv[4];
+            float ks = quantise<CH>(x[u], &kc, kv);
+            const float vs = quantise<CH>(y[u], &vc, vv);
             if (r >= sp.r1) continue;
             if (r >= sp.r0) {
                 *reinterpret_cast<uint2 *>(a.c.k + (row0 + r) * D + ch * 8) = kc;
@@ -154,15 +199,17 @@ __global__ void __launch_bounds__(kThreads) append8_kernel(Append8Args a, int64_
                     a.c.vs[row0 + r] = vs;
                 }
             } else {
-                kc = old[u];
                 ks = scale[u];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    kv[e] = make_float2(code_value(old[u], 2 * e), code_value(old[u], 2 * e + 1));
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = fmaf(code_value(kc, e), ks, acc[e]);
+            for (int e = 0; e < 4; ++e) acc[e] = fma2(kv[e], both(ks), acc[e]);
         }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) part[rg][ch * 8 + e] = acc[e];
+    for (int e = 0; e < 4; ++e) *reinterpret_cast<float2 *>(&part[rg][ch * 8 + 2 * e]) = acc[e];
     __syncthreads();
     if (threadIdx.x < D) {
         float s = 0.f;
