@@ -259,23 +259,36 @@ cudaError_t launch_rows_form(const AttentionArgs &a, cudaStream_t st) {
     const int64_t tiles = a.cu != nullptr ? a.tokens / p.size + 2 * a.seqs : a.seqs * p.items_each;
     const int64_t items = tiles * a.c.heads * p.parts;
     // Few items: large CTAs, one to an SM, in the largest clusters that fit the
-    // card all at once; many: small CTAs, several to an SM, in clusters as
-    // large as leave all of them on the card at once.  No more warps than have
-    // two 16-key tiles each, as far as the host knows the lengths.
+    // card all at once, no more warps than have two 16-key tiles each.  Many:
+    // small CTAs, several to an SM, in clusters of C.  A CTA costs what its
+    // keys do and about as much as 600 keys besides.  With a window the keys
+    // are much the same everywhere, and the turns that the card takes count;
+    // without one lengths are ragged, of which the host knows only the table's
+    // width, and what counts is the longest CTA and the sum of all.  (4096 keys,
+    // 64 sequences over 8 heads: C 1, 2, 4, 8: 228, 197, 189, 228 us; 20: 98, 66,
+    // 74, 85 us.  24 sequences of 4096 to 32768 keys over 8: 668, 386, 314, 303.)
     const bool large = items <= kRowsFewItems;
     const int warps = large ? (nt == 1 ? rows_warps_large<1>() : rows_warps_large<2>()) : kRowsWarpsSmall;
     int64_t keys = int64_t(a.width) * a.c.page;
     if (a.window > 0) keys = std::min<int64_t>(keys, int64_t(a.window) + a.sinks + p.size);
-    const int64_t pairs = keys / 32;
     p.cluster = 1;
     if (large) {
+        const int64_t pairs = keys / 32;
         p.cluster = kMaxCluster;
         while (p.cluster > 5 && kRowsClustersFit[p.cluster] < items) --p.cluster;
         while (p.cluster > 1 && (p.cluster - 1) * warps >= pairs) --p.cluster;
     } else {
-        while (p.cluster < 8 && p.cluster * warps < pairs &&
-               items * p.cluster * 2 <= 152 * rows_ctas_per_sm(a.c.d, nt))
-            p.cluster *= 2;
+        const int64_t slots = 152 * rows_ctas_per_sm(a.c.d, nt), besides = 600;
+        int64_t least = INT64_MAX;
+        for (int c = 1; c <= 8; c *= 2) {
+            const int64_t one = keys / c + besides;
+            const int64_t cost = a.window > 0 ? (items * c + slots - 1) / slots * one
+                                              : std::max(one, items * (keys * 3 / 5 + besides * c) / slots);
+            if (cost < least) {
+                least = cost;
+                p.cluster = c;
+            }
+        }
     }
     if (items * p.cluster > 0x7fffffff) return cudaErrorInvalidConfiguration;
     p.takers = p.cluster >= 8 ? 8 : p.cluster >= 4 ? 4 : p.cluster >= 2 ? 2 : 1;

@@ -91,24 +91,31 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// Quantises a row of which each of the CH lanes of a group has 8 channels;
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+}
+
+// Quantises a row of which each of the CH lanes of a group has twice 8 channels;
 // every lane of the warp takes part.  Returns the row's scale, and the codes also
 // as floats.
 template <int CH>
-__device__ __forceinline__ float quantise(const uint4 &x, uint2 *codes, float2 (&value)[4]) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+__device__ __forceinline__ float quantise(const uint4 (&x)[2], uint2 (&codes)[2], float2 (&value)[8]) {
+    const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
     uint32_t m = 0u;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) m = __vmaxu2(m, w[e] & 0x7fff7fffu);
+    for (int e = 0; e < 8; ++e) m = max_u16x2(m, w[e] & 0x7fff7fffu);
+#pragma unroll
+    for (int o = CH / 2; o > 0; o /= 2) m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
     m = max(m & 0xffffu, m >> 16);
-#pragma unroll
-    for (int o = CH / 2; o > 0; o /= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float a = __uint_as_float(m << 16);
-    *codes = make_uint2(0u, 0u);
+    if (m == 0u || m >= 0x7f80u) {      // zeros; or an infinity or a NaN: all of the row is NaN
+        codes[0] = codes[1] = make_uint2(0u, 0u);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) value[e] = make_float2(0.f, 0.f);
-    if (m == 0u) return 0.f;
-    if (m >= 0x7f80u) return __uint_as_float(0x7fc00000u);      // an infinity or a NaN: all of it is NaN
+        for (int e = 0; e < 8; ++e) value[e] = make_float2(0.f, 0.f);
+        return m == 0u ? 0.f : __uint_as_float(0x7fc00000u);
+    }
     // times 2^(120 - E), E the exponent's field: a comes to [2^-14, 2^-6), and
     // neither its reciprocal nor the residuals leave the normal range
     const int exponent = max(int(m >> 7), 1);
@@ -119,9 +126,9 @@ __device__ __forceinline__ float quantise(const uint4 &x, uint2 *codes, float2 (
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(as));
     const float2 c2 = both(127.f * factor), r2 = both(r), n2 = both(-as);
     const float2 shift = both(12582912.f), back = both(-12582912.f);   // 1.5 * 2^23: the low byte is the code
-    uint32_t q[8];
+    uint32_t q[16];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 8; ++e) {
         const float2 t = mul2(make_float2(bf16_low_half(w[e]), bf16_high_half(w[e])), c2);
         const float2 y0 = mul2(t, r2);
         const float2 y = add2(fma2(fma2(y0, n2, t), r2, y0), shift);
@@ -133,7 +140,8 @@ __device__ __forceinline__ float quantise(const uint4 &x, uint2 *codes, float2 (
         return __byte_perm(__byte_perm(q[e], q[e + 1], 0x0040), __byte_perm(q[e + 2], q[e + 3], 0x0040),
                            0x5410);
     };
-    *codes = make_uint2(bytes(0), bytes(4));
+    codes[0] = make_uint2(bytes(0), bytes(4));
+    codes[1] = make_uint2(bytes(8), bytes(12));
     if (exponent < 32) return __fdiv_rn(a, 127.f);              // a scale that may be subnormal
     // a / 127, corrected the same way: 1 / 127 to the nearest, then the residual
     const float s0 = __fmul_rn(a, 1.f / 127.f);
@@ -149,51 +157,62 @@ __device__ __forceinline__ float code_value(const uint2 &u, int i) {
 // One CTA per (touched page, head): new rows are quantised into the page, and
 // the mean of the page's filled rows is taken of the values that they (and the
 // rows that were there, read back) stand for, in fp32 and a fixed order, so a
-// call can be repeated.  A row is 8 or 16 lanes of 16 bytes.
+// call can be repeated.  A row is 4 or 8 lanes of twice 8 channels (of 8
+// channels, 8 or 16 lanes share what a row costs: 97 us where this takes 81; the
+// bound of five CTAs keeps the compiler from 120 registers: 89 us).
 template <int D>
-__global__ void __launch_bounds__(kThreads) append8_kernel(Append8Args a, int64_t items_each) {
-    constexpr int CH = D / 8;
+__global__ void __launch_bounds__(kThreads, 5) append8_kernel(Append8Args a, int64_t items_each) {
+    constexpr int CH = D / 16;
     constexpr int RG = kThreads / CH;       // rows per pass
-    constexpr int U = 4;
+    constexpr int U = 2;
     __shared__ __align__(8) float part[RG][D];
     Span sp;
     if (!find_span(a.cu, a.seqs, a.tokens, items_each, a.start, a.table, a.width, a.c.page, a.c.num_pages,
                    a.status, &sp))
         return;
     const int32_t head = blockIdx.y, page = a.c.page;
-    const int ch = threadIdx.x % CH, rg = threadIdx.x / CH;
+    const int ch = threadIdx.x % CH * 8, rg = threadIdx.x / CH;  // channels ch and D / 2 + ch on
     const int64_t row0 = (sp.pid * a.c.heads + head) * page;     // of the page's scales
-    const uint16_t *kn = a.k + (sp.tok - sp.r0) * a.k_stride + int64_t(head) * D + ch * 8;
-    const uint16_t *vn = a.v + (sp.tok - sp.r0) * a.v_stride + int64_t(head) * D + ch * 8;
-    float2 acc[4] = {};
+    const uint16_t *kn = a.k + (sp.tok - sp.r0) * a.k_stride + int64_t(head) * D + ch;
+    const uint16_t *vn = a.v + (sp.tok - sp.r0) * a.v_stride + int64_t(head) * D + ch;
+    int8_t *kp = a.c.k + row0 * D + ch, *vp = a.c.v + row0 * D + ch;
+    float2 acc[8] = {};
     for (int32_t base = 0; base < sp.r1; base += U * RG) {       // the same passes for every warp
-        uint4 x[U], y[U];
-        uint2 old[U];
+        uint4 x[U][2], y[U][2];
         float scale[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int32_t r = base + u * RG + rg;
-            x[u] = y[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (r >= sp.r0 && r < sp.r1) {
-                x[u] = *reinterpret_cast<const uint4 *>(kn + r * a.k_stride);
-                y[u] = *reinterpret_cast<const uint4 *>(vn + r * a.v_stride);
-            } else if (r < sp.r0) {
-                old[u] = *reinterpret_cast<const uint2 *>(a.c.k + (row0 + r) * D + ch * 8);
-                scale[u] = a.c.ks[row0 + r];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                x[u][i] = y[u][i] = make_uint4(0u, 0u, 0u, 0u);
+                if (r >= sp.r0 && r < sp.r1) {
+                    x[u][i] = *reinterpret_cast<const uint4 *>(kn + r * a.k_stride + i * (D / 2));
+                    y[u][i] = *reinterpret_cast<const uint4 *>(vn + r * a.v_stride + i * (D / 2));
+                } else if (r < sp.r0) {                          // codes, in y
+                    const uint2 c = *reinterpret_cast<const uint2 *>(kp + r * D + i * (D / 2));
+                    y[u][i].x = c.x;
+                    y[u][i].y = c.y;
+                    scale[u] = a.c.ks[row0 + r];
+                }
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int32_t r = base + u * RG + rg;
-            if (base + u * RG >= sp.r1) break;                  // for the whole CTA
-            uint2 kc, vc;
-            float2 kv[4], vv[4];
-            float ks = quantise<CH>(x[u], &kc, kv);
-            const float vs = quantise<CH>(y[u], &vc, vv);
+            if (base + u * RG >= sp.r1) break;                   // for the whole CTA
+            uint2 kc[2], vc[2];
+            float2 kv[8], vv[8];
+            float ks = quantise<CH>(x[u], kc, kv);
+            const uint4 old[2] = {y[u][0], y[u][1]};
+            const float vs = quantise<CH>(y[u], vc, vv);
             if (r >= sp.r1) continue;
             if (r >= sp.r0) {
-                *reinterpret_cast<uint2 *>(a.c.k + (row0 + r) * D + ch * 8) = kc;
-                *reinterpret_cast<uint2 *>(a.c.v + (row0 + r) * D + ch * 8) = vc;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    *reinterpret_cast<uint2 *>(kp + r * D + i * (D / 2)) = kc[i];
+                    *reinterpret_cast<uint2 *>(vp + r * D + i * (D / 2)) = vc[i];
+                }
                 if (ch == 0) {
                     a.c.ks[row0 + r] = ks;
                     a.c.vs[row0 + r] = vs;
@@ -201,15 +220,18 @@ __global__ void __launch_bounds__(kThreads) append8_kernel(Append8Args a, int64_
             } else {
                 ks = scale[u];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    kv[e] = make_float2(code_value(old[u], 2 * e), code_value(old[u], 2 * e + 1));
+                for (int e = 0; e < 8; ++e) {
+                    const uint2 c = make_uint2(old[e / 4].x, old[e / 4].y);
+                    kv[e] = make_float2(code_value(c, 2 * (e % 4)), code_value(c, 2 * (e % 4) + 1));
+                }
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[e] = fma2(kv[e], both(ks), acc[e]);
+            for (int e = 0; e < 8; ++e) acc[e] = fma2(kv[e], both(ks), acc[e]);
         }
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) *reinterpret_cast<float2 *>(&part[rg][ch * 8 + 2 * e]) = acc[e];
+    for (int e = 0; e < 8; ++e)
+        *reinterpret_cast<float2 *>(&part[rg][ch + e / 4 * (D / 2) + 2 * (e % 4)]) = acc[e];
     __syncthreads();
     if (threadIdx.x < D) {
         float s = 0.f;
