@@ -120,10 +120,12 @@ struct Seen {
 template <int NT>
 constexpr int rows_warps_large() { return NT == 1 ? 12 : 8; }
 constexpr int kRowsWarpsSmall = 4;
-constexpr int rows_ctas_per_sm(int d, int nt) { return nt == 2 ? 2 : d == 64 ? 4 : 3; }
+// (8-bit pages at d 128 leave registers for a fourth: 151 -> 131 us for 64
+// windows of 4096 keys)
+constexpr int rows_ctas_per_sm(int d, int nt, bool q8) { return nt == 2 ? 2 : d == 64 || q8 ? 4 : 3; }
 
 template <int D, int NT, int W, bool Q8>
-__global__ void __launch_bounds__(W * 32, W == kRowsWarpsSmall ? rows_ctas_per_sm(D, NT) : 1)
+__global__ void __launch_bounds__(W * 32, W == kRowsWarpsSmall ? rows_ctas_per_sm(D, NT, Q8) : 1)
     attention_rows_kernel(AttentionArgs a, RowsPlan p) {
     extern __shared__ __align__(16) char smem[];
     RowsFixed &f = *reinterpret_cast<RowsFixed *>(smem);
@@ -278,7 +280,7 @@ cudaError_t launch_rows_form(const AttentionArgs &a, cudaStream_t st) {
         while (p.cluster > 5 && kRowsClustersFit[p.cluster] < items) --p.cluster;
         while (p.cluster > 1 && (p.cluster - 1) * warps >= pairs) --p.cluster;
     } else {
-        const int64_t slots = 152 * rows_ctas_per_sm(a.c.d, nt), besides = 600;
+        const int64_t slots = 152 * rows_ctas_per_sm(a.c.d, nt, Q8), besides = 600;
         int64_t least = INT64_MAX;
         for (int c = 1; c <= 8; c *= 2) {
             const int64_t one = keys / c + besides;

@@ -88,12 +88,14 @@ static_assert(TCfg<128, true, false>::kTotal <= 227 * 1024 && TCfg<128, false, f
                   TCfg<64, false, false>::kTotal <= 227 * 1024 && TCfg<64, true, true>::kTotal <= 227 * 1024 &&
                   TCfg<64, false, true>::kTotal <= 227 * 1024,
               "shared memory");
-template <int D, bool Q8>
+template <int D, bool kPair, bool Q8>
 constexpr bool merge_fits() {
-    using C = TCfg<D, false, Q8>;
+    using C = TCfg<D, kPair, Q8>;
     return 2 * kRows * C::kOStride * 4 <= C::oNotes - C::oP && 2 * kRows * 8 <= C::kStage;
 }
-static_assert(merge_fits<64, false>() && merge_fits<64, true>() && merge_fits<128, false>() && merge_fits<128, true>(),
+static_assert(merge_fits<64, false, false>() && merge_fits<64, false, true>() && merge_fits<128, false, false>() &&
+                  merge_fits<128, false, true>() && merge_fits<64, true, false>() && merge_fits<64, true, true>() &&
+                  merge_fits<128, true, false>(),
               "the merge uses P and the rings");
 static_assert(TCfg<128, true, false>::cO + 256 <= 512 && TCfg<64, true, false>::cP + 128 <= 512, "tensor memory");
 
@@ -289,6 +291,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
     };
     const auto steps_of = [&](int s) { return kPair ? (rows_of(s) > 0 ? n : 0) : (n + 1 - s) / 2; };
     const auto tile_of = [&](int s, int t) { return kPair ? t : 2 * t + s; };
+    const bool merges = !kPair || p.cluster > 1;            // of states: of both streams, or of the cluster
 
     if (tid == 0) {
         tc::mbar_init(bars + C::bQ, 32 * C::kSoft);
@@ -613,8 +616,8 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
         if (steps > 0) ok &= tc::mbar_wait(bars + C::bPv + s, (steps - 1) & 1, status);
         tc::tc_fence_after();
         const float un = Q8 ? exp2_int(big - kWeightShift) : 1.f;
-        if (!kPair) tc::named_bar_sync(1, 32 * C::kSoft);   // nothing reads Q, P and the rings any more
-        if (kPair) {
+        if (merges) tc::named_bar_sync(1, 32 * C::kSoft);   // nothing reads Q, P and the rings any more
+        if (!merges) {
             const float inv = (l > 0.f || l != l ? __fdiv_rn(1.f, l) : 0.f) * un;
             bool finite = true;
             if (ok && active) {
@@ -725,8 +728,8 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 // Stream 1 starts once stream 0 has read its first scores: out of
                 // step, one's exponentials run under the other's loads and maxima
                 // (3 prompts: 446 -> 430 us; a longer delay gains nothing more).
-                if (kPair && warp == C::kSoft + 1) tc::mbar_wait(bars + C::bSFree, 0, status);
-                if (steps_of(warp - C::kSoft) > 0 && tc::mbar_wait(bars + C::bQ, 0, status))
+                if (steps_of(warp - C::kSoft) > 0 && tc::mbar_wait(bars + C::bQ, 0, status) &&
+                    (!kPair || warp == C::kSoft || tc::mbar_wait(bars + C::bSFree, 0, status)))
                     schedule(n, [&](bool v, int i, int q) {
                         const int s = kPair ? warp - C::kSoft : i & 1, t = kPair ? i : i >> 1;
                         return v ? output(s, t, q) : scores(s, t, q);
@@ -881,31 +884,34 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
         }
     }
 
-    if (!kPair) {
+    if (merges) {
         // rows are dealt to the cluster's CTAs and their warps; each merges the
-        // states of both streams of every CTA
+        // states of every CTA, in dual of both streams
         cg::cluster_group peers = cg::this_cluster();
         if (p.cluster > 1)
             peers.sync();
         else
             __syncthreads();
-        const int rows = rows_of(0);
+        const int rows0 = rows_of(0), rows = kPair ? rows0 + rows_of(1) : rows0;
+        constexpr int kOf = kPair ? 1 : 2;                  // states of a row in a CTA
         constexpr int E = D / 32;
-        for (int row = rank + p.cluster * warp; row < rows; row += p.cluster * C::kWarps) {
+        for (int u = rank + p.cluster * warp; u < rows; u += p.cluster * C::kWarps) {
+            const int s = u < rows0 ? 0 : 1, row = u - s * rows0;
             float2 st = make_float2(kMinusInf, 0.f);
-            if (lane < 2 * p.cluster)
-                st = *peers.map_shared_rank(reinterpret_cast<float2 *>(sm + C::oStat) + (lane & 1) * kRows + row, lane >> 1);
+            if (lane < kOf * p.cluster)
+                st = *peers.map_shared_rank(
+                    reinterpret_cast<float2 *>(sm + C::oStat) + (kPair ? s : lane & 1) * kRows + row, lane / kOf);
             const float top = warp_max(st.x);
             const float w = st.x == kMinusInf && st.y == 0.f ? 0.f : exp2_ftz(st.x - (top == kMinusInf ? 0.f : top));
             const float l = warp_sum(w * st.y);
             float x[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) x[e] = 0.f;
-            for (int i = 0; i < 2 * p.cluster; ++i) {
+            for (int i = 0; i < kOf * p.cluster; ++i) {
                 const float wi = __shfl_sync(kAll, w, i);
                 if (__shfl_sync(kAll, st.y, i) == 0.f) continue;          // nothing there
                 const float *o = peers.map_shared_rank(
-                    reinterpret_cast<float *>(sm + C::oP) + ((i & 1) * kRows + row) * C::kOStride, i >> 1);
+                    reinterpret_cast<float *>(sm + C::oP) + ((kPair ? s : i & 1) * kRows + row) * C::kOStride, i / kOf);
                 if (E == 4) {
                     const float4 v = *reinterpret_cast<const float4 *>(o + lane * 4);
                     x[0] = fmaf(wi, v.x, x[0]);
@@ -927,8 +933,8 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
             }
             // a sum that is not a number comes from the row's own scores
             if (!Q8 && l == l && !__all_sync(kAll, finite))
-                row_alone<D>(a, r, sight_at(0, row), head, a.q + token_row(0, row, a.q_stride), x);
-            uint16_t *to = a.out + token_row(0, row, int64_t(a.q_heads) * D) + lane * E;
+                row_alone<D>(a, r, sight_at(s, row), head, a.q + token_row(s, row, a.q_stride), x);
+            uint16_t *to = a.out + token_row(s, row, int64_t(a.q_heads) * D) + lane * E;
 #pragma unroll
             for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t *>(to + e) = pack_bf16x2(x[e], x[e + 1]);
         }
@@ -1003,30 +1009,37 @@ cudaError_t launch_tiles_form(const AttentionArgs &a, cudaStream_t st) {
     const int group = a.q_heads / a.c.heads;
     const int64_t mean = (a.tokens + a.seqs - 1) / a.seqs;
     TilesPlan p;
-    const auto items_of = [&](int size) {
-        p.size = size;
-        p.items_each = (a.tokens / a.seqs + size - 1) / size;
-        return (a.cu != nullptr ? a.tokens / size + 2 * a.seqs : a.seqs * p.items_each) * a.c.heads;
-    };
+    // A CTA costs what its key tiles do (a tile of a dual one as much as of a
+    // pair, which has twice the rows) and about as much as three besides.  With a window
+    // the keys are much the same everywhere, and the turns that the card
+    // takes count; without one lengths are ragged, of which the host knows
+    // only the table's width, and what counts is the longest CTA and the sum of all.
     p.tokens = std::max(1, kRows / group);
-    // pairs where they leave no SM without a CTA
-    int64_t items = items_of(2 * p.tokens);
-    const int64_t used = (a.tokens + 2 * p.tokens - 1) / (2 * p.tokens) * a.c.heads;
-    const bool pair = mean > p.tokens && used >= 96 && !(Q8 && a.c.d == 128);
-    p.cluster = 1;
-    if (!pair) {
-        p.tokens = int32_t(std::min<int64_t>(p.tokens, mean));
-        items = items_of(p.tokens);
-        // the keys dealt to as many CTAs as leave all of them on the card at
-        // once, two tiles of keys for each at least
-        int64_t keys = int64_t(a.width) * a.c.page;
-        if (a.window > 0) keys = std::min<int64_t>(keys, int64_t(a.window) + a.sinks + p.tokens);
-        const int64_t busy = a.cu != nullptr ? (a.tokens / p.tokens + a.seqs) * a.c.heads : items;
-        const int limit[4] = {152, 152, 152, 76};
-        int log = 0;
-        while (log < 3 && busy <= limit[log + 1] && keys >= (int64_t(kKeys) << (log + 2))) ++log;
-        p.cluster = 1 << log;
-    }
+    int64_t keys = int64_t(a.width) * a.c.page;
+    if (a.window > 0) keys = std::min<int64_t>(keys, int64_t(a.window) + a.sinks + p.tokens);
+    const int64_t tiles = (keys + kKeys - 1) / kKeys, slots = 152, besides = 3;
+    const auto cost = [&](int64_t ctas, int64_t one) {
+        return a.window > 0 ? (ctas + slots - 1) / slots * (one + besides)
+                            : std::max(one + besides, ctas * (one * 3 / 5 + besides) / slots);
+    };
+    // CTAs that have rows, as far as the host knows
+    const auto busy = [&](int64_t size) { return (a.tokens + size - 1) / size * a.c.heads; };
+    const int single = int(std::min<int64_t>(p.tokens, mean));
+    bool pair = false;
+    int64_t least = INT64_MAX;
+    for (int c = 1; c <= 8; c *= 2)
+        for (int two = mean > p.tokens && !(Q8 && a.c.d == 128) ? 1 : 0; two >= 0; --two) {
+            const int64_t now = cost(busy(two != 0 ? 2 * p.tokens : single) * c, (tiles + c - 1) / c);
+            if (now < least) {
+                least = now;
+                pair = two != 0;
+                p.cluster = c;
+            }
+        }
+    if (!pair) p.tokens = single;
+    p.size = pair ? 2 * p.tokens : p.tokens;
+    p.items_each = (a.tokens / a.seqs + p.size - 1) / p.size;
+    const int64_t items = (a.cu != nullptr ? a.tokens / p.size + 2 * a.seqs : a.seqs * p.items_each) * a.c.heads;
     if (items * p.cluster > 0x7fffffff) return cudaErrorInvalidConfiguration;
     if (a.c.d == 64) return pair ? launch_tiles<64, true, Q8>(a, p, items, st) : launch_tiles<64, false, Q8>(a, p, items, st);
     if constexpr (!Q8)
