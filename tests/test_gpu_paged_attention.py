@@ -162,6 +162,185 @@ def test_one_long_sequence(bits, group, new):
 
 
 @pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("d,group", [(64, 4), (128, 4), (64, 12), (128, 12)])
+@pytest.mark.parametrize("seqs,longest", [(300, 150), (100, 300), (40, 1000), (16, 4000)])
+def test_many_sequences(seqs, longest, d, group, bits):
+    """Small CTAs, alone and in clusters of two to eight."""
+    g = torch.Generator().manual_seed(20)
+    start = torch.randint(0, longest // 8, (seqs,), generator=g).tolist()
+    start[seqs // 2] = longest
+    step = Step(20, d, 16, 2, group, bits, start, [1] * seqs)
+    step.check(bounds=False)
+    step.check(window=longest // 3, sinks=3, bounds=False)
+    assert bsa.device_status() == 0
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("d,group,new", [(64, 8, [20, 40]), (128, 8, [20, 40]), (64, 2, [1, 64]), (128, 5, [64, 64])])
+def test_long_prefixes(d, group, new, bits):
+    """The keys of a tile of rows dealt to clusters of CTAs, some of which see
+    none of them in the shorter sequence; drafted trees and chains."""
+    step = Step(21, d, 64, 1, group, bits, [6011, 90], new)
+    step.check()
+    step.check(_trees(step.g, new))
+    step.check(window=3000, sinks=200)
+    assert bsa.device_status() == 0
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_masked_values_that_are_not_finite_in_clusters(new):
+    step = Step(22, 64, 16, 1, 4, 16, [6000], [new])
+    for j, bad in ((3, float("inf")), (4000, float("nan"))):
+        step.v[step.table[0][j // 16], 0, j % 16, 5] = bad
+    step.check(window=1500, sinks=2, bounds=False)
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("new", [1, 24])
+def test_positions_and_offsets_past_31_bits(bits, new):
+    """The last pages of a pool of more than 2^32 elements, and of a table of
+    2^24 pages; one more key than a sequence may have is reported."""
+    page, d, heads = 128, 128, 2
+    pool = (1 << 32) // (heads * page * d) + 7
+    g = torch.Generator().manual_seed(23)
+    if bits == 8:
+        cache = bsa.PagedCache8.empty(pool, heads, page, d)
+    else:
+        cache = bsa.PagedCache.empty(pool, heads, page, d)
+    most = (1 << 31) - 256
+    width = -(-most // page) + 1
+    table = torch.full((1, width), -7, dtype=torch.int32, device="cuda")
+    start = most - new
+    b0 = (start - 300) // page
+    table[0, b0:most // page + 1] = torch.arange(pool - (most // page + 1 - b0), pool, dtype=torch.int32, device="cuda")
+    rows = _randn(g, 300 + new, 2 * heads, d)
+    at = _i32([start - 300])
+    bsa.cache_append(cache, rows[:, :heads].cuda(), rows[:, heads:].cuda(), table, at)
+    k, v = bsa.cache_read(cache, table, at, 300 + new)
+    q = _randn(g, new, 4, d)
+    out = bsa.paged_attention(cache, q.cuda(), table, _i32([start]), window=280)
+    assert bsa.device_status() == 0
+    if bits == 8:
+        kv = [att.values(*att.quantise(x)) for x in (rows[:, :heads], rows[:, heads:])]
+        for got, x in zip((k, v), (rows[:, :heads], rows[:, heads:])):
+            c, s = att.quantise(x)
+            assert torch.equal(got.cpu(), (c.float() * s[..., None]).bfloat16())
+    else:
+        kv = [rows[:, :heads], rows[:, heads:]]
+        assert torch.equal(k.cpu(), kv[0]) and torch.equal(v.cpu(), kv[1])
+    # the same step at the front of a small cache
+    kk, vv = (torch.cat([x, x[:(-len(x)) % 16]]).view(-1, 16, heads, d).transpose(1, 2) for x in kv)
+    want, tol = att.attention(kk, vv, q, [list(range(kk.shape[0]))], [0, new], [300], None, 280, 0, bits=bits)
+    ref.assert_within(out, want, tol, "far")
+    out.fill_(5.0)
+    bsa.paged_attention(cache, q.cuda(), table, _i32([start + 1]), window=280, out=out)
+    assert bsa.device_status() == 1 and (out == 5).all()
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+def test_a_serving_run(bits):
+    """Prompts in chunks, a fork with copy on write, drafted trees that are
+    verified and cut back, decoding with and without selection, compaction: each
+    result against plain references over the tokens that were appended."""
+    g = torch.Generator().manual_seed(24)
+    heads, group, d, page, pool = 2, 4, 64, 16, 40
+    kind = bsa.PagedCache8 if bits == 8 else bsa.PagedCache
+    cache, pages = kind.empty(pool, heads, page, d), bsa.PageTable(pool, page, 3, 12)
+    said = [[], [], []]                          # every sequence's rows [k and v heads, d]
+
+    def stand(rows):
+        return att.values(*att.quantise(rows)) if bits == 8 else rows.double()
+
+    def step(news, words=None, window=0, sinks=0):
+        """Appends news[s] tokens and attends; returns their rows."""
+        start = [len(x) for x in said]
+        for s, n in enumerate(news):
+            if n:
+                pages.reserve(s, n)
+        copies = pages.take_copies()
+        if len(copies):
+            bsa.copy_pages(cache, copies)
+        table = _i32(pages.tables()[0])
+        cu = np.cumsum([0] + news).tolist()
+        qkv = _randn(g, cu[-1], (group + 2) * heads, d)
+        on = qkv.cuda()
+        hq = group * heads
+        bsa.cache_append(cache, on[:, hq:hq + heads], on[:, hq + heads:], table, _i32(start), cu_tokens=_i32(cu))
+        tree = None if words is None else torch.tensor(words, dtype=torch.int64, device="cuda")
+        out = bsa.paged_attention(cache, on[:, :hq], table, _i32(start), cu_tokens=_i32(cu), tree=tree,
+                                  window=window, sinks=sinks)
+        for s in range(3):
+            said[s] += list(qkv[cu[s]:cu[s + 1], hq:])
+        # the same over caches of one page a sequence
+        longest = max(map(len, said))
+        k, v = torch.zeros(3, heads, longest, d, dtype=torch.float64), torch.zeros(3, heads, longest, d, dtype=torch.float64)
+        for s, rows in enumerate(said):
+            if rows:
+                x = torch.stack(rows)
+                k[s, :, :len(rows)] = stand(x[:, :heads]).transpose(0, 1)
+                v[s, :, :len(rows)] = stand(x[:, heads:]).transpose(0, 1)
+        want, tol = att.attention(k, v, qkv[:, :hq], [[0], [1], [2]], cu, start, words, window, sinks, bits=bits)
+        ref.assert_within(out, want, tol, f"step of {news}")
+        kk, vv = bsa.cache_read(cache, table, _i32([0, 0, 0]), sum(map(len, said)),
+                                cu_tokens=_i32(np.cumsum([0] + [len(x) for x in said])))
+        rows = torch.stack([r for x in said for r in x])
+        assert torch.equal(kk.cpu(), stand(rows[:, :heads]).float().bfloat16())
+        assert torch.equal(vv.cpu(), stand(rows[:, heads:]).float().bfloat16())
+        return table
+
+    step([37, 20, 0])
+    step([5, 0, 0], window=16, sinks=2)
+    pages.fork(0, 2)
+    said[2] = list(said[0])
+    step([1, 1, 1])                              # the forked page is copied before it grows
+    words = att.tree_masks([-1, 0, 0, 1]) + att.tree_masks([-1, -1]) + att.tree_masks([-1, 0, 1, 1, 3, 0])
+    step([4, 2, 6], words, window=30, sinks=4)
+    for s, keep in enumerate((2, 0, 3)):         # drafts that were not taken
+        n = len(said[s]) - (4, 2, 6)[s] + keep
+        pages.truncate(s, n)
+        said[s] = said[s][:n]
+    step([1, 3, 1])
+    pages.free(1)
+    said[1] = []
+    bsa.copy_pages(cache, pages.compact())
+    table = step([2, 18, 1])
+    lens = [len(x) for x in said]
+    q = _randn(g, 3, group * heads, d)
+    out, idx = bsa.paged_decode(cache, q.cuda(), table, _i32(lens), 2)
+    k, v = (stand_cache(cache, x) for x in "kv")
+    # the last blocks' means are those of their filled rows
+    want, tol, ids = ref.decode(k, v, cache.kbar.cpu(), q, table.cpu(), lens, 2)
+    assert torch.equal(idx.cpu(), ids)
+    ref.assert_within(out, want, tol, "decode")
+    assert bsa.device_status() == 0
+
+
+def stand_cache(cache, name):
+    """The values that a cache's pages hold, on the host."""
+    x = getattr(cache, name).cpu()
+    return att.values(x, getattr(cache, name + "_scale").cpu()) if x.dtype is torch.int8 else x
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("new", [1, 30])
+def test_two_steps_at_once(bits, new):
+    """Two streams with their own caches share nothing."""
+    steps = [Step(25 + i, 64, 16, 2, 4, bits, [200 + 300 * i, 50], [new, new]) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in steps]
+    held = [(s.cache(), s.q.cuda(), _i32(s.table), _i32(s.start)) for s in steps]
+    want = [bsa.paged_attention(c, q, t, st).clone() for c, q, t, st in held]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for stream, (c, q, t, st) in zip(streams, held):
+            with torch.cuda.stream(stream):
+                got.append(bsa.paged_attention(c, q, t, st))
+    torch.cuda.synchronize()
+    for i, x in enumerate(got):
+        assert torch.equal(x, want[i % 2])
+
+
+@pytest.mark.parametrize("bits", [16, 8])
 @pytest.mark.parametrize("d,page,heads,group", [(128, 64, 8, 2), (64, 16, 8, 3), (128, 128, 4, 5), (64, 32, 3, 16)])
 def test_many_rows(d, page, heads, group, bits):
     """Enough rows that two tiles of them share their keys; the second may be
