@@ -14,6 +14,9 @@
 //
 // Bound: memory (each visible K and V row once).  mma.sync of 16 x 8 x 16
 // carries it, as in paged_decode.cuh: the rows are far below a tcgen05 tile's.
+// Measured: one token for each of 64 sequences, 32 heads over 8, d 128, a window of
+// 4096 and four sinks: 196 us, 5.5 TB/s (82 % of a plain copy's rate); over
+// 8-bit pages 131 us, 4.2 TB/s.
 #pragma once
 
 #include <algorithm>

