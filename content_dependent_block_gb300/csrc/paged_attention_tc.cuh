@@ -820,39 +820,55 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 const int raw = q % kRaw;
                 const int32_t ids = page_checked(a, lane < 8 && page_seen(a, r, key0, lane), next);
                 next = entries(i + 1);
-                const uint32_t gone = __ballot_sync(kAll, ids == -2);
+                const uint32_t gone = __ballot_sync(kAll, ids == -2), here = __ballot_sync(kAll, ids >= 0);
                 // this lane's page: its first row in the cache
                 const int64_t base = ids < 0 ? -1 : (int64_t(ids) * a.c.heads + head) * page;
                 const int end = r.end - key0, hide = r.sinks_end - key0, show = r.first - key0;
-                const auto row_in = [&](int x) -> int64_t { // -1: nothing sees it
-                    const int64_t row0 = __shfl_sync(kAll, base, x >> shift);
-                    return row0 < 0 || x >= end || (x >= hide && x < show) ? -1 : row0 + (x & (page - 1));
-                };
                 if (q >= kRaw &&
                     !__all_sync(kAll, tc::mbar_wait(bars + C::bRawEmpty + raw, (q / kRaw - 1) & 1, status)))
                     return false;
                 uint8_t *dst = sm + C::oRaw + raw * C::kRawStage;
                 const int8_t *src = reinterpret_cast<const int8_t *>(v ? a.c.v : a.c.k);
+                float *sc = reinterpret_cast<float *>(dst + kKeys * D);
+                if (here == (1u << (kKeys >> shift)) - 1 && end >= kKeys && (hide >= kKeys || show <= 0 || show <= hide)) {
+                    // every row is there: sixteen at a time, of one page
+                    const int8_t *mine = src + (lane / kPer) * D + lane % kPer * 16;
 #pragma unroll
-                for (int j = 0; j < kPer * 4; ++j) {
-                    const int c = j * 32 + lane;
-                    const int64_t at = row_in(c / kPer);
-                    tc::cp_async16_zfill(dst + c * 16, src + (at < 0 ? 0 : at) * D + c % kPer * 16, at >= 0);
+                    for (int g = 0; g < kKeys / 16; ++g) {
+                        const int64_t row0 = __shfl_sync(kAll, base, g * 16 >> shift) + (g * 16 & (page - 1));
+#pragma unroll
+                        for (int j = 0; j < kPer / 2; ++j)
+                            tc::cp_async16(dst + (g * 16 * kPer + j * 32 + lane) * 16, mine + row0 * D + j * (32 / kPer) * D);
+                    }
+                    if (!v) {
+                        const int64_t row0 = __shfl_sync(kAll, base, lane * 4 >> shift) + (lane * 4 & (page - 1));
+                        tc::cp_async16(sc + lane * 4, a.ks + row0);
+                        tc::cp_async16(sc + kKeys + lane * 4, a.vs + row0);
+                    }
+                } else {
+                    const auto row_in = [&](int x) -> int64_t {     // -1: nothing sees it
+                        const int64_t row0 = __shfl_sync(kAll, base, x >> shift);
+                        return row0 < 0 || x >= end || (x >= hide && x < show) ? -1 : row0 + (x & (page - 1));
+                    };
+#pragma unroll 1
+                    for (int j = 0; j < kPer * 4; ++j) {
+                        const int c = j * 32 + lane;
+                        const int64_t at = row_in(c / kPer);
+                        tc::cp_async16_zfill(dst + c * 16, src + (at < 0 ? 0 : at) * D + c % kPer * 16, at >= 0);
+                    }
+                    if (!v)
+#pragma unroll 1
+                        for (int x = lane; x < kKeys; x += 32) {
+                            const int64_t at = row_in(x);
+                            tc::cp_async4_zfill(sc + x, a.ks + (at < 0 ? 0 : at), at >= 0);
+                            tc::cp_async4_zfill(sc + kKeys + x, a.vs + (at < 0 ? 0 : at), at >= 0);
+                        }
                 }
-                if (!v) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int64_t at = row_in(lane + 32 * j);
-                        float *sc = reinterpret_cast<float *>(dst + kKeys * D) + lane + 32 * j;
-                        tc::cp_async4_zfill(sc, a.ks + (at < 0 ? 0 : at), at >= 0);
-                        tc::cp_async4_zfill(sc + kKeys, a.vs + (at < 0 ? 0 : at), at >= 0);
-                    }
-                    if (lane == 0) {
-                        uint32_t there = 0xffu;
-                        for (uint32_t g = gone; g != 0; g &= g - 1)
-                            there &= ~(((1u << (page / 16)) - 1) << ((__ffs(g) - 1) * (page / 16)));
-                        notes[i % kNotes] = there;
-                    }
+                if (!v && lane == 0) {
+                    uint32_t there = 0xffu;
+                    for (uint32_t g = gone; g != 0; g &= g - 1)
+                        there &= ~(((1u << (page / 16)) - 1) << ((__ffs(g) - 1) * (page / 16)));
+                    notes[i % kNotes] = there;
                 }
                 tc::cp_async_arrive(bars + C::bRawFull + raw);
                 return true;
