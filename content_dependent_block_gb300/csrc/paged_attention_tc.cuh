@@ -343,36 +343,29 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
         return sight_of(a, r.start, r.lo, r.n, min(r.n - 1, r.t0 + (kPair ? s * p.tokens : 0) + row / group));
     };
 
-    // The order in which K and V tiles are loaded and used: the scores of a
-    // step are issued before the products of the one before it.
+    // The order in which K and V tiles are loaded and used: a stream's scores of
+    // the next step come before the products of this one, and in dual the
+    // streams take turns.
     constexpr int kAhead = kPair ? 1 : 2;                   // tiles of a step
     // for the thread that issues products, with as little as possible between them
     const auto schedule = [](int count, const auto &use) {
         int q = 0;
         for (int i = 0; i < min(kAhead, count); ++i)
             if (!use(false, i, q++)) return;
-        for (int i0 = 0; i0 < count; i0 += kAhead) {
-            for (int i = i0 + kAhead; i < min(i0 + 2 * kAhead, count); ++i)
-                if (!use(false, i, q++)) return;
-            for (int i = i0; i < min(i0 + kAhead, count); ++i)
-                if (!use(true, i, q++)) return;
+        for (int i = 0; i < count; ++i) {
+            if (i + kAhead < count && !use(false, i + kAhead, q++)) return;
+            if (!use(true, i, q++)) return;
         }
     };
     // the same for larger bodies, which it has once (24 trees over 8-bit pages:
     // 342 us with three copies, 267 us)
     const auto schedule_once = [](int count, const auto &use) {
-        bool v = false;
-        for (int q = 0, i = 0, i0 = -kAhead; q < 2 * count;) {
-            if (i < min(i0 + (v ? kAhead : 2 * kAhead), count)) {
-                if (!use(v, i++, q++)) return;
-            } else if (!v && i0 >= 0) {
-                v = true;
-                i = i0;
-            } else {
-                i0 += kAhead;
-                v = false;
-                i = i0 + kAhead;
-            }
+        const int lead = min(kAhead, count), both = 2 * (count - lead);
+        for (int q = 0; q < 2 * count; ++q) {
+            const int j = q - lead;
+            const bool v = j >= both || (j >= 0 && (j & 1) != 0);
+            const int i = j < 0 ? q : j >= both ? count - lead + j - both : v ? j / 2 : lead + j / 2;
+            if (!use(v, i, q)) return;
         }
     };
 
