@@ -86,7 +86,7 @@ struct TCfg {
     static constexpr int oScales = oTops + (Q8 ? kNotes * 16 : 0);   // float [8][2][128]
     static constexpr int oBar = oScales + (Q8 ? 8 * 2 * kKeys * 4 : 0);
     static constexpr int oStat = oQ;                        // float2 [2][128], for the merge
-    enum { bQ = 0, bTail, bFull, bEmpty = bFull + kStages, bRawFull = bEmpty + kStages, bRawEmpty = bRawFull + kRaw,
+    enum { bQ = 0, bTail, bGo, bFull, bEmpty = bFull + kStages, bRawFull = bEmpty + kStages, bRawEmpty = bRawFull + kRaw,
            bS = bRawEmpty + kRaw, bSFree = bS + 2, bP = bSFree + 2, bPv = bP + 2, bCount = bPv + 2 };
     static constexpr int oMisc = oBar + bCount * 8;
     static constexpr int kTotal = oMisc + 16 + 1024;
@@ -306,6 +306,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
     if (tid == 0) {
         tc::mbar_init(bars + C::bQ, 32 * C::kSoft);
         tc::mbar_init(bars + C::bTail, 1);
+        tc::mbar_init(bars + C::bGo, kRows);
         const uint32_t users = kPair && rows_of(1) > 0 ? 2 : 1;
         for (int i = 0; i < C::kStages; ++i) {
             tc::mbar_init(bars + C::bFull + i, Q8 ? 128 : 1);
@@ -424,6 +425,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
             // once: the steps go on, so that the barriers below stay paired
             ok &= tc::mbar_wait(bars + C::bS + s, t & 1, status);
             tc::tc_fence_after();
+            if (kPair && s == 0 && t == 0) tc::mbar_arrive(bars + C::bGo);
             if (active) {
                 const uint32_t there = notes[i % kNotes];
                 const bool full = key0 >= lo_max && key0 + kKeys <= hi_min && there == 0xffu;
@@ -502,7 +504,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 float vf = 1.f;
                 if (Q8) {
                     const uint4 tops = *reinterpret_cast<const uint4 *>(sm + C::oTops + (i % kNotes) * 16);
-                    const int e = min(int(max(max(tops.x, tops.y), max(tops.z, tops.w)) >> 23), 254) - 127;
+                    const int e = int(max(max(tops.x, tops.y), max(tops.z, tops.w)) >> 23) - 127;
                     if (e > big) {
                         corr = exp2_int(max(big - e, -126));
                         big = e;
@@ -728,11 +730,11 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                     tc::mma_commit(bars + C::bEmpty + st);
                     return true;
                 };
-                // Stream 1 starts once stream 0 has read its first scores: out of
+                // Stream 1 starts once stream 0 has its first scores: out of
                 // step, one's exponentials run under the other's loads and maxima
                 // (3 prompts: 446 -> 430 us; a longer delay gains nothing more).
                 if (steps_of(warp - C::kSoft) > 0 && tc::mbar_wait(bars + C::bQ, 0, status) &&
-                    (!kPair || warp == C::kSoft || tc::mbar_wait(bars + C::bSFree, 0, status)))
+                    (!kPair || warp == C::kSoft || tc::mbar_wait(bars + C::bGo, 0, status)))
                     schedule(n, [&](bool v, int i, int q) {
                         const int s = kPair ? warp - C::kSoft : i & 1, t = kPair ? i : i >> 1;
                         return v ? output(s, t, q) : scores(s, t, q);
@@ -750,6 +752,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
             };
             int32_t ids = -1, next = look_up(0);
             bool ok = true;
+            uint32_t mine = 0u, odd = 0u;                   // stages last loaded by this warp, and their phases
             schedule_once(n, [&](bool v, int i, int q) {
                 if (v != of_v) return true;
                 const int at = i % tiles_at_once * pages, st = q % C::kStages;
@@ -761,6 +764,8 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 if (q >= C::kStages)
                     ok = __all_sync(kAll, tc::mbar_wait(bars + C::bEmpty + st, (q / C::kStages - 1) & 1, status));
                 if (!ok) return false;
+                mine |= 1u << st;
+                odd = (odd & ~(1u << st)) | uint32_t((q / C::kStages) & 1) << st;
                 const uint32_t gone = (__ballot_sync(kAll, ids == -2) >> at) & ((1u << pages) - 1);
                 if (lane == 0) {
                     if (!v) {
@@ -783,6 +788,10 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 __syncwarp();
                 return true;
             });
+            if (!ok)                                        // copies in flight land before the CTA ends
+                for (int st = 0; st < C::kStages; ++st)
+                    for (int poll = 0; ((mine >> st) & 1u) && poll < (1 << 20); ++poll)
+                        if (tc::mbar_test_wait(bars + C::bFull + st, (odd >> st) & 1u)) break;
             if (of_v && ok && n > 0) {
                 // rows past the last key hold anything, and 0 times NaN must not reach O
                 const int q = 2 * n - 1, st = q % C::kStages, tail = r.end - tiles.key0(n - 1);
@@ -886,7 +895,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                     const float sv = sc[kKeys];
                     scales[(i % 8) * 2 * kKeys + w] = sc[0];
                     scales[((i % 8) * 2 + 1) * kKeys + w] = sv;
-                    const uint32_t top = __reduce_max_sync(kAll, sv == sv ? __float_as_uint(sv) & 0x7fffffffu : 0u);
+                    const uint32_t top = __reduce_max_sync(kAll, fabsf(sv) < -kMinusInf ? __float_as_uint(fabsf(sv)) : 0u);
                     if (lane == 0) reinterpret_cast<uint32_t *>(sm + C::oTops)[(i % kNotes) * 4 + (w >> 5)] = top;
                 }
 #pragma unroll

@@ -225,8 +225,10 @@ __device__ __forceinline__ void attend_keys(const CacheView &c, float scale_log2
 // the largest vs so far (the sums follow when it grows): fp16 rounds them
 // to 2^-12 of themselves, those below 2^-26 of the largest to 2^-37 of that.
 // Lane (n8, kq) ends with channel n8 * D / 8 + 2 i + (e >> 1) in o[t][i][e].
-// A key that no row admits has weight 0, and 0 times a code is 0, so whatever
-// the scales of masked keys and of rows past the end are, they do not count.
+// E is that of all keys of the warp's tiles, so a row's weights are rounded by
+// what its neighbours see too.  A key that a row does not admit has weight 0 in
+// it, and 0 times a code is 0, whatever its scales are; those of rows past the
+// end, and scales that are not finite, do not count for E.
 template <int D, int NT, typename Source, typename QRow>
 __device__ __forceinline__ void attend_keys8(const CacheView &c, const float *ks_ptr,
                                              const float *vs_ptr, float scale_log2, int rows,
@@ -332,11 +334,11 @@ __device__ __forceinline__ void attend_keys8(const CacheView &c, const float *ks
         for (int i = 0; i < 2; ++i) {
             kn[i] = ks[i];
             vn[i] = vs[i];
-            if (n8 + 8 * i < now_valid && vn[i] == vn[i]) top = max(top, __float_as_uint(vn[i]) & 0x7fffffffu);
+            if (n8 + 8 * i < now_valid && fabsf(vn[i]) < -kNegInf) top = max(top, __float_as_uint(fabsf(vn[i])));
         }
         more = src.next();
         if (more) load_k();             // in flight during the softmax and P V
-        const int e_top = min(int(__reduce_max_sync(kFull, top) >> 23), 254) - 127;
+        const int e_top = int(__reduce_max_sync(kFull, top) >> 23) - 127;
         float grow = 1.f;
         if (e_top > big) {
             grow = power_of_two(max(big - e_top, -126));

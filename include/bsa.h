@@ -590,7 +590,10 @@ typedef struct {
  * bsa_cache_append, bsa_cache_copy_pages and bsa_paged_decode over the 8-bit
  * cache: arguments, results and errors are theirs.  Appending quantises the
  * bf16 rows; copies take the codes, the scales and the means; decoding attends
- * to what the rows stand for, exactly (no second rounding of K and V).
+ * to what the rows stand for (no second rounding of K and V).  A key's weight
+ * is rounded to 2^-11 of itself, or, where that is more, to 2^-29 of what the
+ * largest |v| of the keys that are attended to beside it, by any of the rows
+ * that share a tile (a token's heads, a step's tokens), would make it.
  */
 bsa_status bsa_cache8_append(bsa_cache8 cache, const void *k, int64_t k_stride, const void *v,
                              int64_t v_stride, int64_t tokens, int64_t seqs,
