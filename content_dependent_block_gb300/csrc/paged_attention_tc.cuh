@@ -25,12 +25,13 @@
 // room for it.  8-bit pages: P in fp16, as there.
 //
 // Measured: 3 prompts of 8191 tokens in all, 32 heads over 8, d 128, a window of 4096:
-// 427 us, 1.29 PFLOP/s (67 % of cuBLAS's burst); 16 trees of 64 tokens behind
-// 4096 to 32768 keys, the same heads: 311 us against 184 us of traffic; 24
-// trees of 13 tokens, 24 heads over 4, d 64, over 8-bit pages: 267 us.  A step
-// of a pair takes about 3000 cycles: the softmax (loads 200, maximum 480,
-// exponentials and P 2000, waits 400) of both streams at once, and the products,
-// which at d 128 read 128 bytes a cycle of shared memory for 2500.
+// 402 us, 1.37 PFLOP/s (71 % of cuBLAS's burst), over 8-bit pages 1250 us; 16
+// trees of 64 tokens behind 4096 to 32768 keys, the same heads: 292 us against
+// 184 us of traffic; 24 trees of 13 tokens, 24 heads over 4, d 64, over 8-bit
+// pages: 207 us against 36.  A step of a pair took about 3000 cycles with both
+// streams in step: the softmax (loads 200, maximum 480, exponentials and P 2000, waits
+// 400), and the products, which at d 128 read 128 bytes a cycle of shared
+// memory for 2500.
 //
 //   warps 0-3, 4-7   softmax of streams 0 and 1
 //   warps 8, 9       MMA of streams 0 and 1, each issued by one thread (in dual one
@@ -732,7 +733,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 };
                 // Stream 1 starts once stream 0 has its first scores: out of
                 // step, one's exponentials run under the other's loads and maxima
-                // (3 prompts: 446 -> 430 us; a longer delay gains nothing more).
+                // (3 prompts: 446 us in step, 404 so, 428 and more with later starts).
                 if (steps_of(warp - C::kSoft) > 0 && tc::mbar_wait(bars + C::bQ, 0, status) &&
                     (!kPair || warp == C::kSoft || tc::mbar_wait(bars + C::bGo, 0, status)))
                     schedule(n, [&](bool v, int i, int q) {
