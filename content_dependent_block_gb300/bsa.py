@@ -9,6 +9,7 @@ fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -771,28 +772,42 @@ def cache_read(cache: PagedCache, table, start, tokens: int, *, cu_tokens=None,
     layout, with contiguous channels.  See bsa_cache_read in bsa.h."""
     torch = _torch()
     seqs, width = table.shape
-    tokens = _whole(tokens, 64, "tokens")
-    shape = (cache.heads, tokens, cache.d) if heads_first else (tokens, cache.heads, cache.d)
+    heads, d = cache.heads, cache.d
+    if type(tokens) is not int:
+        tokens = _whole(tokens, 64, "tokens")
+    shape = (heads, tokens, d) if heads_first else (tokens, heads, d)
     if out is None:
-        k, v = (torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) for _ in range(2))
+        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device)
+        v = torch.empty_like(k)
+        st = (shape[1] * d, d)
     else:
         k, v = out
         for t in out:
             if t.shape != shape or t.dtype is not torch.bfloat16 or t.stride(2) != 1:
                 raise ValueError(f"out must be two bfloat16 {list(shape)} with contiguous channels")
-        if k.stride() != v.stride():
+        st = k.stride()
+        if v.stride() != st:
             raise ValueError("out's tensors must have one layout")
         if torch.is_grad_enabled() and (k.requires_grad or v.requires_grad):
             raise ValueError("cache_read records no history: out must not require a gradient")
-    st = k.stride()
     cu = None if cu_tokens is None else _i32(cu_tokens, "cu_tokens", (seqs + 1,))
     _check(cache._read(
         cache.struct, tokens, seqs, cu, _i32(start, "start", (seqs,)),
         _i32(table, "table", (seqs, width)), width, k.data_ptr(), v.data_ptr(),
         Strides(0, st[0], st[1]) if heads_first else Strides(0, st[1], st[0]),
         _here(cache.k, table, start, cu_tokens, k, v)))
-    _written(k, v)
+    if out is not None:
+        _written(k, v)
     return k, v
+
+
+@functools.lru_cache(maxsize=64)
+def _window(window: int, sinks: int):
+    """A reference to the bsa_window of these numbers, None for none."""
+    window, sinks = _whole(window, 32, "window"), _whole(sinks, 32, "sinks")
+    if window == 0 and sinks != 0:
+        raise ValueError("sinks without a window")
+    return None if window == 0 else ctypes.byref(Window(window, sinks))
 
 
 def paged_attention(cache: PagedCache, q, table, start, *, cu_tokens=None, tree=None,
@@ -811,10 +826,8 @@ def paged_attention(cache: PagedCache, q, table, start, *, cu_tokens=None, tree=
     if tree is not None and (tree.shape != (tokens,) or tree.dtype is not torch.int64
                              or not tree.is_contiguous()):
         raise TypeError(f"tree must be a contiguous int64 tensor {[tokens]}")
-    window, sinks = _whole(window, 32, "window"), _whole(sinks, 32, "sinks")
-    if window == 0 and sinks != 0:
-        raise ValueError("sinks without a window")
-    if out is None:
+    span, fresh = _window(window, sinks), out is None
+    if fresh:
         out = torch.empty((tokens, q_heads, d), dtype=q.dtype, device=q.device)
     elif out.dtype is not q.dtype or out.shape != (tokens, q_heads, d) or not out.is_contiguous():
         raise ValueError("out must be contiguous bfloat16 [tokens, q_heads, d]")
@@ -823,9 +836,9 @@ def paged_attention(cache: PagedCache, q, table, start, *, cu_tokens=None, tree=
     _check(cache._attention(
         cache.struct, q.data_ptr(), qs, tokens, q_heads, _i32(table, "table", (seqs, width)), width,
         seqs, cu, _i32(start, "start", (seqs,)), None if tree is None else tree.data_ptr(),
-        None if window == 0 else ctypes.byref(Window(window, sinks)), scale, out.data_ptr(),
-        _here(cache.k, q, table, start, cu_tokens, tree, out)))
-    _written(out)
+        span, scale, out.data_ptr(), _here(cache.k, q, table, start, cu_tokens, tree, out)))
+    if not fresh:
+        _written(out)
     return out
 
 
