@@ -18,7 +18,7 @@
 // by the residual t - y a (Markstein's), which reaches every quotient that is
 // representable, a half among them.
 //
-// 65521 tokens of 8 heads of 128 are appended in 81 us, 5.0 TB/s (74 % of a plain
+// 65521 tokens of 8 heads of 128 are appended in 79 us, 5.1 TB/s (76 % of a plain
 // copy's rate: over half of the issue slots go to the quantising), and read back
 // in 68 us, 6.0 TB/s; 131072 tokens in the [heads][n][d] layout in 128 us, 6.3 TB/s.
 #include "paged_common.cuh"
@@ -159,10 +159,10 @@ __device__ __forceinline__ float code_value(const uint2 &u, int i) {
 // the mean of the page's filled rows is taken of the values that they (and the
 // rows that were there, read back) stand for, in fp32 and a fixed order, so a
 // call can be repeated.  A row is 4 or 8 lanes of twice 8 channels (of 8
-// channels, 8 or 16 lanes share what a row costs: 97 us where this takes 81; the
-// bound of five CTAs keeps the compiler from 120 registers: 89 us).
+// channels, 8 or 16 lanes share what a row costs: 97 us where this takes 79; the
+// bound of six CTAs keeps the compiler from 120 registers: 89 us).
 template <int D>
-__global__ void __launch_bounds__(kThreads, 5) append8_kernel(Append8Args a, int64_t items_each) {
+__global__ void __launch_bounds__(kThreads, 6) append8_kernel(Append8Args a, int64_t items_each) {
     constexpr int CH = D / 16;
     constexpr int RG = kThreads / CH;       // rows per pass
     constexpr int U = 2;
