@@ -222,13 +222,13 @@ __device__ __forceinline__ void attend_keys(const CacheView &c, float scale_log2
 // The same over 8-bit pages, in fp16: codes are exact there, q is after a power
 // of two for each row, and a key's scales multiply its score and its weight
 // in fp32.  Weights w = p vs 2^(12 - E) enter the product, E the exponent of
-// the largest vs so far (the sums follow when it grows): fp16 rounds them
-// to 2^-12 of themselves, those below 2^-26 of the largest to 2^-37 of that.
+// the largest vs that the row has admitted so far (its sums follow when it
+// grows): fp16 rounds them to 2^-11 of themselves, those below 2^-26 of the
+// largest to 2^-37 of that.  Each row has its own E: a key that it does not admit
+// may have any scale, also where other rows of the tile admit it.  Scales that
+// are not finite do not count.  A masked key's weight is 0, and 0 times a code
+// is 0.  E seldom grows, so a vote passes over the reduction that finds it.
 // Lane (n8, kq) ends with channel n8 * D / 8 + 2 i + (e >> 1) in o[t][i][e].
-// E is that of all keys of the warp's tiles, so a row's weights are rounded by
-// what its neighbours see too.  A key that a row does not admit has weight 0 in
-// it, and 0 times a code is 0, whatever its scales are; those of rows past the
-// end, and scales that are not finite, do not count for E.
 template <int D, int NT, typename Source, typename QRow>
 __device__ __forceinline__ void attend_keys8(const CacheView &c, const float *ks_ptr,
                                              const float *vs_ptr, float scale_log2, int rows,
@@ -305,7 +305,9 @@ __device__ __forceinline__ void attend_keys8(const CacheView &c, const float *ks
             }
         }
     };
-    int big = -110;                     // E
+    int big[NT][2];                     // E of the lane's rows
+#pragma unroll
+    for (int t = 0; t < NT; ++t) big[t][0] = big[t][1] = -110;
     bool more = src.first();
     if (more) {
         load_k();
@@ -329,32 +331,45 @@ __device__ __forceinline__ void attend_keys8(const CacheView &c, const float *ks
                     mma_half(s[t], a0, a1, a2, a3, q[t][g][2 * j], q[t][g][2 * j + 1]);
             }
         float kn[2], vn[2];
-        uint32_t top = 0u;
+        int of[2];                      // exponents of vs, of which E is the largest
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             kn[i] = ks[i];
             vn[i] = vs[i];
-            if (n8 + 8 * i < now_valid && fabsf(vn[i]) < -kNegInf) top = max(top, __float_as_uint(fabsf(vn[i])));
+            of[i] = fabsf(vn[i]) < -kNegInf ? int(__float_as_uint(fabsf(vn[i])) >> 23) - 127 : -127;
         }
         more = src.next();
         if (more) load_k();             // in flight during the softmax and P V
-        const int e_top = int(__reduce_max_sync(kFull, top) >> 23) - 127;
-        float grow = 1.f;
-        if (e_top > big) {
-            grow = power_of_two(max(big - e_top, -126));
-            big = e_top;
-        }
-        const float vf = power_of_two(12 - big);
         uint32_t b0[NT], b1[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            float corr[2], x[4];
-            bool moved = grow != 1.f;
+            float corr[2], grow[2] = {1.f, 1.f}, x[4];
+            bool in[2][2], moved = false, larger = false;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    in[e][i] = n8 + 8 * i < now_valid && src.admits(tile, t * 8 + 2 * kq + e, n8 + 8 * i);
+                    larger |= in[e][i] && of[i] > big[t][e];
+                }
+            if (__any_sync(kFull, larger)) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    int top = max(in[e][0] ? of[0] : -127, in[e][1] ? of[1] : -127);
+                    top = max(top, __shfl_xor_sync(kFull, top, 4));
+                    top = max(top, __shfl_xor_sync(kFull, top, 8));
+                    top = max(top, __shfl_xor_sync(kFull, top, 16));
+                    if (top > big[t][e]) {
+                        grow[e] = power_of_two(max(big[t][e] - top, -126));
+                        big[t][e] = top;
+                        moved = true;
+                    }
+                }
+            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int row = t * 8 + 2 * kq + e;
-                const bool in0 = n8 < now_valid && src.admits(tile, row, n8);
-                const bool in1 = n8 + 8 < now_valid && src.admits(tile, row, n8 + 8);
+                const bool in0 = in[e][0], in1 = in[e][1];
+                const float vf = power_of_two(12 - big[t][e]);
                 // s[e]: key n8, s[2 + e]: key n8 + 8; the product of the
                 // factors first, which is nearer to 1 than either
                 s[t][e] = in0 ? s[t][e] * (kn[0] * back[t][e]) : kNegInf;
@@ -371,7 +386,7 @@ __device__ __forceinline__ void attend_keys8(const CacheView &c, const float *ks
                 s[t][e] = exp2_fast(s[t][e] - base);
                 s[t][2 + e] = exp2_fast(s[t][2 + e] - base);
                 l[t][e] = l[t][e] * corr[e] + (s[t][e] + s[t][2 + e]);
-                corr[e] *= grow;
+                corr[e] *= grow[e];
                 x[e] = in0 ? s[t][e] * (vn[0] * vf) : 0.f;
                 x[2 + e] = in1 ? s[t][2 + e] * (vn[1] * vf) : 0.f;
             }
@@ -404,13 +419,14 @@ __device__ __forceinline__ void attend_keys8(const CacheView &c, const float *ks
         }
         if (more) load_v(src.row0);
     }
-    const float un = power_of_two(big - 12);
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t) {
+        const float un[2] = {power_of_two(big[t][0] - 12), power_of_two(big[t][1] - 12)};
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[t][i][e] *= un;
+            for (int e = 0; e < 4; ++e) o[t][i][e] *= un[e & 1];
+    }
 }
 
 // Scratch of the merge, in shared memory.
