@@ -25,7 +25,7 @@
 // room for it.  8-bit pages: P in fp16, as there.
 //
 // Measured: 3 prompts of 8191 tokens in all, 32 heads over 8, d 128, a window of 4096:
-// 402 us, 1.37 PFLOP/s (71 % of cuBLAS's burst), over 8-bit pages 1250 us; 16
+// 402 us, 1.37 PFLOP/s (71 % of cuBLAS's burst), over 8-bit pages 1290 us; 16
 // trees of 64 tokens behind 4096 to 32768 keys, the same heads: 292 us against
 // 184 us of traffic; 24 trees of 13 tokens, 24 heads over 4, d 64, over 8-bit
 // pages: 207 us against 36.  A step of a pair took about 3000 cycles with both
@@ -83,7 +83,7 @@ struct TCfg {
     static constexpr int oRing = oP + (kPShared ? 2 * kPBytes : 0);
     static constexpr int oRaw = oRing + kStages * kStage;
     static constexpr int oNotes = oRaw + kRaw * kRawStage;  // uint32 [kNotes]: which 16-key groups are there
-    static constexpr int oTops = oNotes + kNotes * 4;       // uint32 [kNotes][4]: largest vs (bits) of a warp's rows
+    static constexpr int oTops = oNotes + kNotes * 4;       // uint32 [kNotes][4]: largest vs (bits) of a quarter's keys
     static constexpr int oScales = oTops + (Q8 ? kNotes * 16 : 0);   // float [8][2][128]
     static constexpr int oBar = oScales + (Q8 ? 8 * 2 * kKeys * 4 : 0);
     static constexpr int oStat = oQ;                        // float2 [2][128], for the merge
@@ -272,6 +272,23 @@ __device__ __forceinline__ void store_codes(uint8_t *row, int chunk, int r, cons
     *reinterpret_cast<uint4 *>(row + (((chunk + 1) ^ (r & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
 }
 
+// The largest |scale| (bits) of those of 32 keys whose bits are set.  A call: in
+// line it costs every step at d 128 registers (3 prompts over 8-bit pages 1356 us,
+// so 1290; 1251 with the largest of the whole tile, which is wrong where a key
+// that the row does not see has it).
+__device__ __noinline__ uint32_t largest_scale(const float4 *scales, uint32_t keys) {
+    uint32_t top = 0u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float4 v4 = scales[j];
+        const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (((keys >> (4 * j + k)) & 1u) && fabsf(v[k]) < -kMinusInf) top = max(top, __float_as_uint(fabsf(v[k])));
+    }
+    return top;
+}
+
 template <int D, bool kPair, bool Q8>
 __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
     attention_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -417,7 +434,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
         const bool active = (warp & 3) * 32 < rows;         // any row in this warp
         const int32_t lo_max = __reduce_max_sync(kAll, sight.lo), hi_min = __reduce_min_sync(kAll, sight.hi);
         float m = kMinusInf, l = 0.f;
-        int big = -110;                                     // E of the weights (8-bit pages)
+        int big = -110;                                     // E of the row's weights (8-bit pages)
         bool ok = true;
         for (int t = 0; t < steps; ++t) {
             const int i = tile_of(s, t);
@@ -505,7 +522,19 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                 float vf = 1.f;
                 if (Q8) {
                     const uint4 tops = *reinterpret_cast<const uint4 *>(sm + C::oTops + (i % kNotes) * 16);
-                    const int e = int(max(max(tops.x, tops.y), max(tops.z, tops.w)) >> 23) - 127;
+                    int e = int(max(max(tops.x, tops.y), max(tops.z, tops.w)) >> 23) - 127;
+                    if (e > big && !full) {
+                        // the largest scale may be that of a key which this row
+                        // does not see: the largest of those that it does
+                        uint32_t own = 0u;
+#pragma unroll 1
+                        for (int c = 0; c < kKeys / 32; ++c) {
+                            const uint32_t adm = admitted(c);
+                            const uint32_t all = reinterpret_cast<const uint32_t *>(sm + C::oTops)[(i % kNotes) * 4 + c];
+                            own = max(own, adm == kAll ? all : adm != 0u ? largest_scale(vs + c * 8, adm) : 0u);
+                        }
+                        e = int(own >> 23) - 127;
+                    }
                     if (e > big) {
                         corr = exp2_int(max(big - e, -126));
                         big = e;

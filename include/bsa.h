@@ -591,9 +591,9 @@ typedef struct {
  * cache: arguments, results and errors are theirs.  Appending quantises the
  * bf16 rows; copies take the codes, the scales and the means; decoding attends
  * to what the rows stand for (no second rounding of K and V).  A key's weight
- * is rounded to 2^-11 of itself, or, where that is more, to 2^-29 of what the
- * largest |v| of the keys that are attended to beside it, by any of the rows
- * that share a tile (a token's heads, a step's tokens), would make it.
+ * is off by 2^-11 of itself at most, or, where that is more, its part of an
+ * output by 2^-31 of the largest 127 * v_scale among the keys that the same
+ * query row attends to.  Keys that a row does not attend to do not count.
  */
 bsa_status bsa_cache8_append(bsa_cache8 cache, const void *k, int64_t k_stride, const void *v,
                              int64_t v_stride, int64_t tokens, int64_t seqs,

@@ -139,3 +139,37 @@ def test_decoding_heads_that_select_unlike_blocks(d, page, seqs, huge):
     want, tol = (torch.stack([torch.stack([x[j] for x in row]) for row in want]) for j in (0, 1))
     ref.assert_within(out, want, tol, "decode")
     assert bsa.device_status() == 0
+
+
+MANY = [(40, 1), (40, 4), (64, 2), (1, 24)]             # many rows
+
+
+@pytest.mark.parametrize("huge", HUGE)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,group", MANY)
+def test_many_rows(new, group, d, huge):
+    """The same with tiles of 128 rows."""
+    for window in (1, 16, 100):
+        step = _step(46, d, group, 203, new, range(203 + 1 - window), huge)
+        _check(step, None, window, 0, f"window {window}")
+    step = _step(47, d, group, 300, new, range(3, 300 + 1 - 20), huge)
+    _check(step, None, 20, 3, "sinks")
+    words = [w & ~2 for w in att.tree_masks(range(-1, new - 1))]
+    step = _step(48, d, group, 37, new, [38] if new > 1 else [], huge)
+    _check(step, words, 0, 0, "a draft that nobody sees")
+    _check(step, att.tree_masks([-1] * new), 0, 0, "branches")
+    step = _step(49, d, group, 90, new, [90 - 20 + new // 2] if new > 1 else [], huge)
+    _check(step, None, 20, 0, "a key that the window of half of the tokens has passed")
+
+
+@pytest.mark.parametrize("huge", HUGE)
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_rows_over_many_tiles(d, huge):
+    """Pairs of tiles, long prefixes dealt to a cluster, keys of the edge of a
+    window seen by some rows only."""
+    step = _step(50, d, 4, 700, 150, [600, 640, 720, 800], huge)
+    _check(step, None, 130, 2, "window")
+    step = _step(51, d, 4, 5000, 40, [5003, 5010], huge)
+    words = att.tree_masks([-1] + [(i - 1) // 2 for i in range(1, 40)])
+    _check(step, words, 0, 0, "tree")
+    _check(step, words, 3000, 5, "tree in a window")
