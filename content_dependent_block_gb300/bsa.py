@@ -801,9 +801,16 @@ def cache_read(cache: PagedCache, table, start, tokens: int, *, cu_tokens=None,
     return k, v
 
 
-@functools.lru_cache(maxsize=64)
-def _window(window: int, sinks: int):
+def _window(window, sinks):
     """A reference to the bsa_window of these numbers, None for none."""
+    # what is kept goes by the values: a tensor or array may change in place
+    if type(window) is not int or type(sinks) is not int:
+        window, sinks = _whole(window, 32, "window"), _whole(sinks, 32, "sinks")
+    return _window_of(window, sinks)
+
+
+@functools.lru_cache(maxsize=64)
+def _window_of(window: int, sinks: int):
     window, sinks = _whole(window, 32, "window"), _whole(sinks, 32, "sinks")
     if window == 0 and sinks != 0:
         raise ValueError("sinks without a window")
