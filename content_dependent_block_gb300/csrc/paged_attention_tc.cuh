@@ -273,9 +273,9 @@ __device__ __forceinline__ void store_codes(uint8_t *row, int chunk, int r, cons
 }
 
 // The largest |scale| (bits) of those of 32 keys whose bits are set.  A call: in
-// line it costs every step at d 128 registers (3 prompts over 8-bit pages 1356 us,
-// so 1290; 1251 with the largest of the whole tile, which is wrong where a key
-// that the row does not see has it).
+// line it takes registers from every step at d 128 (3 prompts over 8-bit pages
+// 1356 us, so 1290; 1251 with the largest of the whole tile, which is wrong where
+// it is that of a key which the row does not see).
 __device__ __noinline__ uint32_t largest_scale(const float4 *scales, uint32_t keys) {
     uint32_t top = 0u;
 #pragma unroll
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
             tc::mbar_init(bars + C::bEmpty + i, users);
         }
         for (int i = 0; i < C::kRaw; ++i) {
-            tc::mbar_init(bars + C::bRawFull + i, 32);
+            tc::mbar_init(bars + C::bRawFull + i, 33);      // a lane's copies each, and the tile's note
             tc::mbar_init(bars + C::bRawEmpty + i, 128);
         }
         for (int s = 0; s < 2; ++s) {
@@ -902,7 +902,10 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                         there &= ~(((1u << (page / 16)) - 1) << ((__ffs(g) - 1) * (page / 16)));
                     notes[i % kNotes] = there;
                 }
+                // the copies' arrivals come when they end and say nothing of the
+                // stores before them: the note has one of its own
                 tc::cp_async_arrive(bars + C::bRawFull + raw);
+                if (lane == 0) tc::mbar_arrive(bars + C::bRawFull + raw);
                 return true;
             });
             tc::cp_async_wait_all();
