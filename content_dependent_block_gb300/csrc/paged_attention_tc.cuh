@@ -679,7 +679,9 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                         }
                 }
                 if (!Q8) {
-                    // a sum that is not a number comes from the row's own scores
+                    // a sum that is not a number comes from the row's own scores;
+                    // other lanes write over what this one wrote above
+                    __syncwarp();
                     for (uint32_t again = __ballot_sync(kAll, row < rows && !finite && l == l); again != 0;
                          again &= again - 1) {
                         const int which = (warp & 3) * 32 + __ffs(again) - 1;
@@ -687,7 +689,7 @@ __global__ void __launch_bounds__(TCfg<D, kPair, Q8>::kWarps * 32, 1)
                         row_alone<D>(a, r, sight_at(s, which), head, a.q + token_row(s, which, a.q_stride), x);
                         uint16_t *to = a.out + token_row(s, which, int64_t(a.q_heads) * D) + lane * (D / 32);
 #pragma unroll
-                            for (int e = 0; e < D / 32; ++e) to[e] = f32_to_bf16_bits(x[e]);
+                        for (int e = 0; e < D / 32; ++e) to[e] = f32_to_bf16_bits(x[e]);
                     }
                 }
             }
