@@ -79,8 +79,9 @@ __device__ __forceinline__ void mma_half(float (&c)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 
 // The power of two that brings a row of q to fp16: its largest |q| (bits of a
-// bf16) to [2^14, 2^15).  Values 2^-39 of that keep their bits, and what is
-// smaller is off by 2^-40 of it: below fp32's own rounding of the scores.
+// bf16) to [2^14, 2^15).  Values down to 2^-31 of that keep their eight bits, and
+// what is smaller is off by 2^-39 of the largest: below fp32's own rounding of the
+// scores.
 // `back` undoes it.
 __device__ __forceinline__ float half_factor(uint32_t bits, float *back) {
     const int e = min(max(int(bits >> 7), 15), 254) - 127;
@@ -185,7 +186,7 @@ __device__ __forceinline__ void attend_keys(const CacheView &c, float scale_log2
                 }
             }
             // P for the product is its bf16 value and what that leaves, again
-            // in bf16: off by 2^-18 of p at most (of one bf16 value, 2^-9)
+            // in bf16: off by 2^-17 of p at most (of one bf16 value, 2^-8)
             const uint32_t p0 = pack_bf16x2(s[t][0], s[t][1]), p1 = pack_bf16x2(s[t][2], s[t][3]);
             b0[t] = transpose_8x8(p0);
             b1[t] = transpose_8x8(p1);

@@ -653,9 +653,9 @@ bsa_status bsa_cache8_read(bsa_cache8 cache, int64_t tokens, int64_t seqs,
  *   out            [tokens][q_heads][d] bf16 (device); not q, nor in the
  *                  cache.  A token that sees no key gets zeros.
  * Softmax statistics and sums are fp32.  A weight enters the product with V
- * off by 2^-18 of itself where a sequence has few query rows per cache head on
- * average (8, or 16 with at most 1024 keys), by half a bf16 step where it has
- * more; over 8-bit pages as bsa_paged_decode8 says.
+ * off by at most 2^-17 of itself where a sequence has few query rows per cache
+ * head on average (8, or 16 with at most 1024 keys), by at most 2^-8 (half a
+ * bf16 step) where it has more; over 8-bit pages as bsa_paged_decode8 says.
  * q_heads a multiple of heads, at most 128 per cache head.  A masked key does
  * not count whatever its K and V hold; a key of the cache that is not finite
  * costs time where it is masked (its rows are computed again, one by one).
