@@ -36,8 +36,7 @@ struct RowsPlan {
     int64_t items_each;   // tiles of a sequence, where all have as many tokens
     int32_t cluster, takers;
     int32_t size;         // tokens of a tile
-    int32_t parts, gh;    // tiles a group of heads is dealt to, and its heads in each
-    int32_t rows_cap;     // size * gh
+    int32_t rows_cap;     // size times the heads of a cache head
     int32_t part_off, main_off;
 };
 
@@ -137,27 +136,23 @@ __global__ void __launch_bounds__(W * 32, W == kRowsWarpsSmall ? rows_ctas_per_s
     const int tid = threadIdx.x;
     const int rank = int(blockIdx.x % unsigned(p.cluster));
     const unsigned cluster = blockIdx.x / unsigned(p.cluster);
-    const unsigned per = unsigned(a.c.heads * p.parts);
-    const int64_t number = cluster / per;
-    const int hp = int(cluster - unsigned(number) * per);
-    const int head = hp / p.parts, part_of = hp - head * p.parts;
+    const int64_t number = cluster / unsigned(a.c.heads);
+    const int head = int(cluster - unsigned(number) * unsigned(a.c.heads));
     const int group = a.q_heads / a.c.heads;
-    const int gh = min(p.gh, group - part_of * p.gh);         // heads of this tile
-    const int head0 = head * group + part_of * p.gh;
     check_bounds(a.cu, a.seqs, a.tokens, int64_t(blockIdx.x) * (W * 32) + tid, a.status);
     Reach r;
     // the whole cluster leaves together
     if (!find_reach(a, p.size, p.items_each, number, rank == 0 && tid == 0, &r)) return;
-    const int rows = r.nt * gh;
+    const int rows = r.nt * group;
     if (tid < kMaxRows) {
         const int row = min(tid, rows - 1);                    // rows that are not there see what the last sees
-        f.sight[tid] = sight_of(a, r.start, r.lo, r.n, r.t0 + row / gh);
+        f.sight[tid] = sight_of(a, r.start, r.lo, r.n, r.t0 + row / group);
     }
     if (tid == 0) f.merge.redo = 0u;
     __syncthreads();
     const auto token_row = [&](int row, int64_t stride) {
-        const int t = row / gh;
-        return (r.lo + r.t0 + t) * stride + int64_t(head0 + row - t * gh) * D;
+        const int t = row / group;
+        return (r.lo + r.t0 + t) * stride + int64_t(head * group + row - t * group) * D;
     };
     const auto q_row = [&](int row) { return a.q + token_row(row, a.q_stride); };
     float o[NT][D / 16][4], m[NT][2], l[NT][2];
@@ -251,18 +246,15 @@ cudaError_t launch_rows(const AttentionArgs &a, const RowsPlan &p, size_t smem, 
 
 template <bool Q8>
 cudaError_t launch_rows_form(const AttentionArgs &a, cudaStream_t st) {
-    const int group = a.q_heads / a.c.heads;
+    const int group = a.q_heads / a.c.heads;                  // at most kMaxRows
     const int64_t mean = (a.tokens + a.seqs - 1) / a.seqs;
     RowsPlan p;
-    p.parts = (group + kMaxRows - 1) / kMaxRows;
-    p.gh = (group + p.parts - 1) / p.parts;
-    p.size = int32_t(std::min<int64_t>(std::max(1, kMaxRows / p.gh), mean));
-    if (p.parts > 1) p.size = 1;
-    p.rows_cap = p.size * p.gh;
+    p.size = int32_t(std::min<int64_t>(kMaxRows / group, mean));
+    p.rows_cap = p.size * group;
     const int nt = p.rows_cap > 8 ? 2 : 1;
     p.items_each = (a.tokens / a.seqs + p.size - 1) / p.size;
     const int64_t tiles = a.cu != nullptr ? a.tokens / p.size + 2 * a.seqs : a.seqs * p.items_each;
-    const int64_t items = tiles * a.c.heads * p.parts;
+    const int64_t items = tiles * a.c.heads;
     // Few items: large CTAs, one to an SM, in the largest clusters that fit the
     // card all at once, no more warps than have two 16-key tiles each.  Many:
     // small CTAs, several to an SM, in clusters of C.  A CTA costs what its
