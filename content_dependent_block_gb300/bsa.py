@@ -769,7 +769,8 @@ def cache_read(cache: PagedCache, table, start, tokens: int, *, cu_tokens=None,
     ``tokens`` in all, cut by ``cu_tokens`` (None: as many for each), as
     [tokens, heads, d], or [heads, tokens, d] with ``heads_first`` (the layout
     ``forward`` takes).  ``out``: a pair of tensors of that shape, of one
-    layout, with contiguous channels.  See bsa_cache_read in bsa.h."""
+    layout, with contiguous channels.  Rows of tokens that no sequence has are
+    not written.  See bsa_cache_read in bsa.h."""
     torch = _torch()
     seqs, width = table.shape
     heads, d = cache.heads, cache.d
@@ -824,7 +825,8 @@ def paged_attention(cache: PagedCache, q, table, start, *, cu_tokens=None, tree=
     themselves.  ``cu_tokens`` int32 [seqs + 1], None: as many tokens for each.
     ``tree`` int64 [tokens]: which of its sequence's (at most 64) new tokens a
     token sees, besides the prefix.  ``window`` W and ``sinks``: only the last W
-    positions and the first few; 0: all.  See bsa_paged_attention in bsa.h."""
+    positions and the first few; 0: all.  Rows of tokens that no sequence has are
+    not written.  See bsa_paged_attention in bsa.h."""
     torch = _torch()
     seqs, width = table.shape
     tokens, q_heads, d = q.shape

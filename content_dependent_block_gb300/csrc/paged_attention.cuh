@@ -122,8 +122,8 @@ struct Seen {
 template <int NT>
 constexpr int rows_warps_large() { return NT == 1 ? 12 : 8; }
 constexpr int kRowsWarpsSmall = 4;
-// (8-bit pages at d 128 leave registers for a fourth: 151 -> 131 us for 64
-// windows of 4096 keys)
+// (8-bit pages at d 128 leave registers for a fourth: 131 us for 64 windows of
+// 4096 keys where three take 151; 125 now)
 constexpr int rows_ctas_per_sm(int d, int nt, bool q8) { return nt == 2 ? 2 : d == 64 || q8 ? 4 : 3; }
 
 template <int D, int NT, int W, bool Q8>

@@ -21,14 +21,15 @@
 // so O is seldom rescaled.  Masks are bit sets of 32 keys, built only where a
 // tile is not seen whole.  P is one bf16 number (off by 2^-8 at most, as in the
 // prompt's sparse forward): with its remainder as a second one, as few rows
-// take it (paged_tiles.cuh), the products with V would double and there is no
-// room for it.  8-bit pages: P in fp16, as there.
+// take it (paged_tiles.cuh), the products with V would double, and at d 128 there
+// is no room for it (at d 64 there is; not tried).  8-bit pages: P in fp16, as there.
 //
 // Measured: 3 prompts of 8191 tokens in all, 32 heads over 8, d 128, a window of 4096:
-// 402 us, 1.37 PFLOP/s (71 % of cuBLAS's burst), over 8-bit pages 1290 us; 16
-// trees of 64 tokens behind 4096 to 32768 keys, the same heads: 292 us against
-// 184 us of traffic; 24 trees of 13 tokens, 24 heads over 4, d 64, over 8-bit
-// pages: 207 us against 36.  A step of a pair took about 3000 cycles with both
+// 402 to 431 us on several cards, 1.28 to 1.37 PFLOP/s (67 to 71 % of cuBLAS's
+// burst), over 8-bit pages 1290 us; 16 trees of 64 tokens behind 4096 to 32768
+// keys, the same heads: 292 to 341 us against 184 us of traffic, over 8-bit pages
+// 668 against 161; 24 trees of 13 tokens, 24 heads over 4, d 64, over 8-bit pages:
+// 208 to 222 us against 36.  A step of a pair took about 3000 cycles with both
 // streams in step: the softmax (loads 200, maximum 480, exponentials and P 2000, waits
 // 400), and the products, which at d 128 read 128 bytes a cycle of shared
 // memory for 2500.
@@ -63,7 +64,7 @@ constexpr int kNotes = 16;               // tiles whose notes are kept: more tha
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kMinusInf = -__builtin_huge_valf();
 constexpr float kLazy = 8.f;             // growth of a row's maximum that is let pass, log2
-constexpr int kWeightShift = 6;          // 8-bit pages: weights times 2^(6 - E)
+constexpr int kWeightShift = 6;          // 8-bit pages: weights times 2^(6 - E), below 2^(8 + 1 + 6)
 
 template <int D, bool kPair, bool Q8>
 struct TCfg {

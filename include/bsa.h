@@ -651,8 +651,11 @@ bsa_status bsa_cache8_read(bsa_cache8 cache, int64_t tokens, int64_t seqs,
  *                  a token to the next (multiple of 8, >= q_heads * d).
  *   scale          softmax scale; <= 0 selects 1/sqrt(d).
  *   out            [tokens][q_heads][d] bf16 (device); not q, nor in the
- *                  cache.  A token that sees no key gets zeros.
- * Softmax statistics and sums are fp32.  A weight enters the product with V
+ *                  cache.  A token that sees no key gets zeros (as does one
+ *                  whose scores are all -inf).
+ * Softmax statistics and sums are fp32; the weighted values are divided by the
+ * weights' sum at the end, so |v| times the number of keys has to stay below
+ * 2^119.  A weight enters the product with V
  * off by at most 2^-17 of itself where a sequence has few query rows per cache
  * head on average (8, or 16 with at most 1024 keys), by at most 2^-8 (half a
  * bf16 step) where it has more; over 8-bit pages as bsa_paged_decode8 says.
